@@ -281,6 +281,135 @@ moe_status moe_expert_ffn_prefill_stages(const moe_layer* L, const uint16_t* x_b
                                          void* ws, size_t ws_bytes, unsigned stages,
                                          void* stream);
 
+/* ---------------------------------------------------------------------------------
+ * The attention half of a decoder layer: norm and rotation of query and key heads, a
+ * paged key-value cache, and attention over it for decode windows and prefill chunks.
+ * (The engine explainer, m.lqnn.cn/news/264700, "Doorbell handshake": the first graph of
+ * a layer runs attention before the routing; "Speculative decoding": verify windows of
+ * up to 5 tokens; "Architecture overview": chunks of up to 8192 tokens. The pages give no
+ * layouts or formulas for it; those below are the library's own.)
+ *
+ * Element types, as `dtype` fields and arguments: */
+#define MOE_BF16 0
+#define MOE_F16 1
+#define MOE_E4M3 2 /* OCP e4m3, caches only                                          */
+
+#define MOE_MAX_WINDOW_TOKENS 16 /* window_tokens of moe_attn_decode                    */
+#define MOE_MAX_HEADS 512        /* heads of one row set                                */
+
+/* Heads of n tokens: element (t, h, c) at data[t * token_stride + h * head_stride + c],
+ * strides in elements. data 16-byte aligned, strides multiples of 8 and not negative, so
+ * the query part of a fused projection output [n][(Hq + 2 Hkv) * D] is a moe_heads. */
+typedef struct {
+  void* data; /* device; data == NULL: no such heads (where the call allows it)        */
+  int64_t token_stride, head_stride;
+  int32_t heads;
+} moe_heads;
+
+/* Paged key-value cache of one layer. A slot is page * page_size + row of the page.
+ *   k  [num_pages][kv_heads][page_size][head_dim]
+ *   v  [num_pages][kv_heads][page_size / 8][head_dim][8]   the last axis is the row
+ *      within a group of 8 rows: the matrix cores take 8 consecutive rows of one column
+ *      per lane, which this layout keeps in one 16-byte (8-byte at 8 bits) word.
+ * Both 16-byte aligned. head_dim 64, 128 or 256; page_size 16, 32, 64, 128 or 256;
+ * kv_heads 1..MOE_MAX_HEADS; num_pages * page_size below 2^31. An MOE_E4M3 cache holds
+ * value / scale of its head, rounded to nearest even and clamped to +-448 (NaN stays NaN);
+ * k_scale and v_scale are fp32 [kv_heads] in device memory, NULL for 1. For 16-bit caches
+ * they must be NULL. */
+typedef struct {
+  void* k;
+  void* v;
+  const float* k_scale;
+  const float* v_scale;
+  int32_t dtype, num_pages, page_size, kv_heads, head_dim;
+} moe_kv_cache;
+
+/* Norm and rotation of head rows, in fp32 with one rounding at the end:
+ *   y = x * (w + weight_offset) / sqrt(mean(x^2) + eps)     (w == NULL: y = x)
+ *   pair i < rot_dim/2, a = position * inv_freq[i] (product and reduction in binary64):
+ *   (y_p, y_q) -> (y_p cos a - y_q sin a, y_q cos a + y_p sin a), with p = i,
+ *   q = i + rot_dim/2, or, interleaved, p = 2i, q = 2i + 1; elements from rot_dim on keep
+ *   y. rot_dim: 0 (no rotation) or a multiple of 16 up to head_dim. */
+typedef struct {
+  const float* q_norm;   /* device fp32 [head_dim] or NULL                              */
+  const float* k_norm;   /* device fp32 [head_dim] or NULL                              */
+  const float* inv_freq; /* device fp32 [rot_dim / 2]                                   */
+  float eps, weight_offset;
+  int32_t rot_dim, interleaved;
+} moe_norm_rope;
+
+/* Pages and lengths of the sequences of one attention call, in device memory:
+ *   table    int32 [n_seqs][table_stride], entry (s, i) is the page that holds rows
+ *            i * page_size .. of sequence s; max_pages entries of a row may be read. Pages
+ *            without a visible key are not read, and their entries may hold anything;
+ *            keys on a page number outside [0, num_pages) count as not visible.
+ *   kv_lens  int32 [n_seqs], keys of each sequence, the call's own tokens included (they
+ *            have been appended before); clamped to [0, max_pages * page_size]. */
+typedef struct {
+  const int32_t* table;
+  const int32_t* kv_lens;
+  int64_t table_stride;
+  int32_t n_seqs, max_pages;
+} moe_pages;
+
+/* softmax(scale * q.k) over the visible keys. A query at position p sees key j when
+ * j <= p and (window == 0 or j > p - window or j < sinks). A query that sees no key (or
+ * whose visible scores are all -inf) gets zeros. Query head h reads kv head
+ * h / (heads / kv_heads). */
+typedef struct {
+  float scale;
+  int32_t window, sinks;
+} moe_attn;
+
+/* Norm and rotation of the query and key heads of n_tokens tokens, one pass, out of place
+ * or in place. q, k: input heads (either may have data == NULL); q_out, k_out: their
+ * outputs, same head counts, heads that do not overlap each other. An output may be its
+ * own input (same data and strides); any other overlap is rejected. dtype: MOE_BF16 or
+ * MOE_F16. positions: device int32 [n_tokens] (may be NULL when rot_dim == 0).
+ * n_tokens <= MOE_MAX_PREFILL_TOKENS. */
+moe_status moe_qk_norm_rope(const moe_heads* q, const moe_heads* k, const int32_t* positions,
+                            int n_tokens, int dtype, int head_dim, const moe_norm_rope* p,
+                            const moe_heads* q_out, const moe_heads* k_out, void* stream);
+
+/* Keys and values of n_tokens tokens into a paged cache: k normed and rotated by p (NULL:
+ * as it is), v as it is, both rounded to the cache's type. slots: device int32 [n_tokens],
+ * the slot of each token; a slot outside the cache (negative for padding) stores nothing.
+ * Slots inside the cache must differ from each other (of two equal ones, either token's
+ * elements may stay). q (NULL or data == NULL: none): query heads normed and rotated into
+ * q_out in the same launch, for every token. All other cache rows keep their contents. dtype is that of q,
+ * k and v; a 16-bit cache has the same. n_tokens <= MOE_MAX_PREFILL_TOKENS. */
+moe_status moe_kv_append(const moe_kv_cache* cache, const moe_heads* k, const moe_heads* v,
+                         const int32_t* slots, const int32_t* positions, int n_tokens,
+                         int dtype, const moe_norm_rope* p, const moe_heads* q,
+                         const moe_heads* q_out, void* stream);
+
+/* Attention of the newest window_tokens tokens of each sequence over the cache. q: heads of
+ * n_seqs * window_tokens tokens, sequence-major; token t of a sequence of length L is at
+ * position L - window_tokens + t (a negative one sees nothing). out: device
+ * [n_seqs * window_tokens][heads][head_dim], contiguous, of q's type, 16-byte aligned.
+ * q's heads: a multiple of kv_heads. window_tokens 1..MOE_MAX_WINDOW_TOKENS and
+ * n_seqs * window_tokens <= MOE_MAX_DECODE_TOKENS. A 16-bit cache has q's type. ws: device
+ * workspace of moe_attn_decode_workspace_bytes bytes, 256-byte aligned, no initialisation
+ * needed (NULL when that is 0). out overlaps none of the inputs. Keys are split over
+ * workgroups and joined; results do not depend on timing. */
+size_t moe_attn_decode_workspace_bytes(const moe_kv_cache* cache, int q_heads, int n_seqs,
+                                       int window_tokens, int max_pages, const moe_attn* a);
+moe_status moe_attn_decode(const moe_kv_cache* cache, const moe_heads* q, int dtype,
+                           const moe_pages* pages, int window_tokens, const moe_attn* a,
+                           void* out, void* ws, size_t ws_bytes, void* stream);
+
+/* Attention of prompt chunks. q: heads of n_tokens tokens; q_starts: device int32
+ * [n_seqs + 1], ascending from 0: sequence s has tokens q_starts[s] .. q_starts[s+1]-1, its
+ * m tokens at positions kv_lens[s] - m ... Tokens from q_starts[n_seqs] on are neither
+ * read nor written. Other arguments as moe_attn_decode. n_tokens <=
+ * MOE_MAX_PREFILL_TOKENS, n_seqs <= MOE_MAX_PREFILL_TOKENS. */
+size_t moe_attn_prefill_workspace_bytes(const moe_kv_cache* cache, int q_heads, int n_seqs,
+                                        int n_tokens, int max_pages, const moe_attn* a);
+moe_status moe_attn_prefill(const moe_kv_cache* cache, const moe_heads* q, int dtype,
+                            const int32_t* q_starts, int n_tokens, const moe_pages* pages,
+                            const moe_attn* a, void* out, void* ws, size_t ws_bytes,
+                            void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -12,12 +12,15 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 REPO_DIR = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
+JOBS = 8  # compilers at once
 
 # Packed-fp32 VALU forms are disabled for all device code; -ffp-contract=off keeps every
 # floating-point multiply and add separately rounded unless a kernel calls fma itself.
@@ -26,7 +29,6 @@ COMMON_FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     "-ffp-contract=off",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall",
@@ -34,17 +36,14 @@ COMMON_FLAGS = [
 ]
 
 LIBS = {
-    "libqmoe.so": ["qmoe.hip", "qmoe_route.hip", "qmoe_decode.hip", "qmoe_prefill.hip"],
+    "libqmoe.so": ["qmoe.hip", "qmoe_route.hip", "qmoe_decode.hip", "qmoe_prefill.hip",
+                   "qmoe_attn.hip", "qmoe_rows.hip", "qmoe_attn_decode.hip",
+                   "qmoe_attn_prefill.hip"],
     "libqmoe_synth.so": ["synth.hip"],
 }
 
 
-def _compile(out_name: str, sources: list[str], verbose: bool) -> None:
-    out = os.path.join(PKG_DIR, out_name)
-    tmp = out + ".tmp"
-    srcs = [os.path.join(CSRC, s) for s in sources]
-    cmd = [HIPCC, *COMMON_FLAGS, f"-I{os.path.join(REPO_DIR, 'include')}", f"-I{CSRC}", *srcs,
-           "-o", tmp]
+def _run(cmd: list[str], what: str, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -52,15 +51,29 @@ def _compile(out_name: str, sources: list[str], verbose: bool) -> None:
     noise = "is not a recognized feature for this target"
     msgs = [ln for ln in (res.stdout + res.stderr).splitlines() if noise not in ln]
     if res.returncode != 0:
-        raise RuntimeError(f"hipcc failed for {out_name}:\n" + "\n".join(msgs))
+        raise RuntimeError(f"hipcc failed for {what}:\n" + "\n".join(msgs))
     if msgs and verbose:
         print("\n".join(msgs), flush=True)
-    os.replace(tmp, out)
 
 
 def build(verbose: bool = False) -> None:
-    for name, sources in LIBS.items():
-        _compile(name, sources, verbose)
+    """Every source to an object of its own (the sources side by side: they share no device
+    code), then one link per library."""
+    with tempfile.TemporaryDirectory() as tmp, ThreadPoolExecutor(JOBS) as pool:
+        jobs, objects = [], {}
+        for name, sources in LIBS.items():
+            objects[name] = [os.path.join(tmp, src + ".o") for src in sources]
+            for src, obj in zip(sources, objects[name]):
+                cmd = [HIPCC, *COMMON_FLAGS, f"-I{os.path.join(REPO_DIR, 'include')}",
+                       f"-I{CSRC}", "-c", os.path.join(CSRC, src), "-o", obj]
+                jobs.append(pool.submit(_run, cmd, src, verbose))
+        for job in jobs:
+            job.result()
+        for name, objs in objects.items():
+            out = os.path.join(PKG_DIR, name)
+            _run([HIPCC, f"--offload-arch={ARCH}", "-fPIC", "-shared", *objs, "-o", out + ".tmp"],
+                 name, verbose)
+            os.replace(out + ".tmp", out)
 
 
 if __name__ == "__main__":

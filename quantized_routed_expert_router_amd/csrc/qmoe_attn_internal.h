@@ -1,0 +1,255 @@
+// Internal declarations of the attention half: kernel arguments, element types and the
+// masks shared by the decode and prefill attention kernels.
+#pragma once
+
+#include "qmoe_internal.h"
+
+namespace qmoe {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kNegInf = -__builtin_huge_valf();
+
+// ------------------------------------------------------------------ element types
+
+// 16-bit activation types: 8-element vectors, the matrix-core products and the expansion of
+// e4m3 codes (exact in either type).
+struct Bf16 {
+  typedef __bf16 T;
+  typedef bf16x8 V8;
+  typedef bf16x4 V4;
+  typedef bf16x2 V2;
+  static constexpr uint32_t kExpMask = 0x7f80u;
+#if defined(__HIP_DEVICE_COMPILE__)
+  static __device__ __forceinline__ f32x4 mfma16(V8 a, V8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x16 mfma32(V8 a, V8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+  template <bool HI>
+  static __device__ __forceinline__ V2 from_e4m3(uint32_t w) {
+    return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI);
+  }
+#endif
+};
+
+struct F16 {
+  typedef _Float16 T;
+  typedef f16x8 V8;
+  typedef f16x4 V4;
+  typedef f16x2 V2;
+  static constexpr uint32_t kExpMask = 0x7c00u;
+#if defined(__HIP_DEVICE_COMPILE__)
+  static __device__ __forceinline__ f32x4 mfma16(V8 a, V8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x16 mfma32(V8 a, V8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+  }
+  template <bool HI>
+  static __device__ __forceinline__ V2 from_e4m3(uint32_t w) {
+    return __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HI);
+  }
+#endif
+};
+
+template <typename TO, typename FROM>
+__device__ __forceinline__ TO bits_as(const FROM& x) {
+  static_assert(sizeof(TO) == sizeof(FROM), "size");
+  TO y;
+  __builtin_memcpy(&y, &x, sizeof(TO));
+  return y;
+}
+
+#if defined(__HIP_DEVICE_COMPILE__)
+// 8 e4m3 codes (two words) as 8 elements.
+template <typename A>
+__device__ __forceinline__ typename A::V8 expand_e4m3(uint32_t w0, uint32_t w1) {
+  const u32x4 r = {bits_as<uint32_t>(A::template from_e4m3<false>(w0)),
+                   bits_as<uint32_t>(A::template from_e4m3<true>(w0)),
+                   bits_as<uint32_t>(A::template from_e4m3<false>(w1)),
+                   bits_as<uint32_t>(A::template from_e4m3<true>(w1))};
+  return bits_as<typename A::V8>(r);
+}
+
+// Two fp32 values as e4m3 codes in the low 16 bits: nearest even, clamped to +-448, NaN
+// stays NaN (the clamp's comparisons are false for it).
+__device__ __forceinline__ uint32_t pack_e4m3(float a, float b) {
+  a = a > 448.0f ? 448.0f : a;
+  a = a < -448.0f ? -448.0f : a;
+  b = b > 448.0f ? 448.0f : b;
+  b = b < -448.0f ? -448.0f : b;
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false) & 0xffffu;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Replaces the non-finite 16-bit elements of v by zero; returns whether there were any.
+template <typename A>
+__device__ __forceinline__ bool clear_nonfinite(typename A::V8& v) {
+  u32x4 w = bits_as<u32x4>(v);
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool lo = (w[i] & A::kExpMask) == A::kExpMask;
+    const bool hi = ((w[i] >> 16) & A::kExpMask) == A::kExpMask;
+    w[i] = (lo ? 0u : (w[i] & 0xffffu)) | (hi ? 0u : (w[i] & 0xffff0000u));
+    any |= lo | hi;
+  }
+  v = bits_as<typename A::V8>(w);
+  return any;
+}
+#endif
+
+// ------------------------------------------------------------------ kernel arguments
+
+struct HeadView {
+  char* data;
+  long long token_stride, head_stride;  // elements
+  int heads;
+};
+
+struct RowsArgs {  // norm, rotation and append
+  HeadView q, k, v, q_out, k_out;
+  const int32_t* positions;
+  const int32_t* slots;  // append: slot of each token
+  int n, dtype, D;
+  moe_norm_rope p;
+  const moe_kv_cache* cache;  // nullptr: k goes to k_out
+  hipStream_t stream;
+  int num_cus;
+};
+
+struct AttnArgs {
+  HeadView q;
+  int dtype;
+  moe_kv_cache cache;
+  moe_pages pages;
+  moe_attn a;
+  const int32_t* q_starts;  // prefill
+  int n;                    // tokens
+  int window_tokens;        // decode
+  char* out;
+  char* ws;
+  hipStream_t stream;
+};
+
+// Split of one attention call over the key axis: `splits` workgroups per row tile, each
+// writing its partial sums (fp32 [rows][head_dim], with a maximum and a sum) to the
+// workspace, joined by a second kernel. splits == 1: no workspace, no second kernel.
+struct AttnPlan {
+  int row_tiles;  // row tiles of one kv head (decode: per sequence; prefill: upper bound)
+  int splits;
+  int tile_rows;
+  size_t partial, stats, total;  // workspace offsets and size
+};
+
+AttnPlan decode_plan(int q_heads, int kv_heads, int D, int n_seqs, int window_tokens,
+                     int max_pages, int page_size, const moe_attn& a, int num_cus);
+AttnPlan prefill_plan(int q_heads, int kv_heads, int D, int n_seqs, int n_tokens, int max_pages,
+                      int page_size, const moe_attn& a, int num_cus);
+
+hipError_t launch_rows(const RowsArgs& a);
+hipError_t launch_attn_decode(const AttnArgs& a, const AttnPlan& plan);
+hipError_t launch_attn_prefill(const AttnArgs& a, const AttnPlan& plan);
+
+// ------------------------------------------------------------------ masks and tiles
+
+struct KeyMask {
+  int window, sinks;
+};
+
+__device__ __forceinline__ bool key_visible(const KeyMask& m, int key, int pos) {
+  return key <= pos && (m.window == 0 || key > pos - m.window || key < m.sinks);
+}
+
+// The key tiles (of TILE keys) that queries at positions first..last can see: sink tiles
+// 0..ns-1, then tiles lo..hi-1.
+struct TileList {
+  int ns, lo, count;
+  __device__ __forceinline__ int tile(int i) const { return i < ns ? i : lo + (i - ns); }
+};
+
+template <int TILE>
+__device__ __forceinline__ TileList visible_tiles(const KeyMask& m, int first, int last) {
+  TileList t;
+  if (last < 0) {
+    t.ns = t.lo = t.count = 0;
+    return t;
+  }
+  const int hi = last / TILE + 1;
+  const int from = m.window == 0 ? 0 : max(0, first - m.window + 1);
+  t.lo = from / TILE;
+  t.ns = m.window == 0 ? 0 : min((int)(((long long)m.sinks + TILE - 1) / TILE), t.lo);
+  t.count = t.ns + (hi - t.lo);
+  return t;
+}
+
+// ------------------------------------------------------------------ joining splits
+
+constexpr int kJoinThreads = 256;
+constexpr int kMaxSplits = kJoinThreads;  // one statistic a thread
+
+#if defined(__HIP_DEVICE_COMPILE__)
+// One output row from its `live` splits, by a workgroup of kJoinThreads: each split's sums
+// are relative to its own maximum. row = token * q heads + q head.
+template <typename A, int D>
+__device__ __forceinline__ void join_row(const float* partial, const float2* stats, long long row,
+                                         int splits, int live, float v_scale, char* out) {
+  constexpr int LANES = D / 4, GROUPS = kJoinThreads / LANES, WAVES = kJoinThreads / kWave;
+  __shared__ float weight[kMaxSplits];
+  __shared__ float red[2][WAVES];
+  __shared__ f32x4 part[GROUPS][LANES];
+  const int tid = threadIdx.x;
+  float2 st = make_float2(kNegInf, 0.0f);
+  if (tid < live) st = stats[row * splits + tid];
+  float top = st.x;
+#pragma unroll
+  for (int s = 1; s < kWave; s *= 2) top = fmaxf(top, __shfl_xor(top, s));
+  if (tid % kWave == 0) red[0][tid / kWave] = top;
+  __syncthreads();
+#pragma unroll
+  for (int s = 0; s < WAVES; ++s) top = fmaxf(top, red[0][s]);
+  const float w = exp2_fast(st.x - (top == kNegInf ? 0.0f : top));
+  if (tid < live) weight[tid] = w;
+  float sum = w * st.y;
+#pragma unroll
+  for (int s = 1; s < kWave; s *= 2) sum += __shfl_xor(sum, s);
+  if (tid % kWave == 0) red[1][tid / kWave] = sum;
+  __syncthreads();
+  sum = red[1][0];
+#pragma unroll
+  for (int s = 1; s < WAVES; ++s) sum += red[1][s];
+  const int lane = tid % LANES, grp = tid / LANES;
+  const f32x4* src = reinterpret_cast<const f32x4*>(partial + row * splits * D) + lane;
+  f32x4 y = {0, 0, 0, 0};
+#pragma unroll 4
+  for (int s = grp; s < live; s += GROUPS) y += weight[s] * src[(long long)s * LANES];
+  part[grp][lane] = y;
+  __syncthreads();
+  if (grp == 0) {
+#pragma unroll
+    for (int s = 1; s < GROUPS; ++s) y += part[s][lane];
+    u32x2 w2;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) y[c] = sum == 0.0f ? 0.0f : y[c] / sum * v_scale;
+    w2 = bits_as<u32x2>(__builtin_convertvector(y, typename A::V4));
+    *reinterpret_cast<u32x2*>(out + 2 * (row * D + 4 * lane)) = w2;
+  }
+}
+#endif
+
+}  // namespace qmoe

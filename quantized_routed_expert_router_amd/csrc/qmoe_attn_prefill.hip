@@ -1,0 +1,518 @@
+// Causal attention of prompt chunks over the paged cache, with an optional sliding window
+// and first keys that stay visible.
+//
+// The rows of one sequence and one kv head are (token, query head of the group), token
+// outermost, so that all heads of a group share each key tile and the causal edge stays
+// narrow. A workgroup takes 32 rows a wave; key tiles of KT keys go through LDS, double
+// buffered, and every wave runs, on 32x32x16 matrix-core tiles,
+//   S^T = K Q^T        A: 8 columns of one key row a lane (LDS rows, 16-byte chunks swizzled
+//                      by the row so that 16 rows cover all banks); Q stays in registers
+//   O^T += V^T P^T     A: 8 keys of one column a lane, one 16-byte word of the cache's V
+//                      layout, copied to LDS as it is
+// The key rows of a 32-key half are dealt to the first product's rows (bits 2 and 3
+// exchanged) so that its accumulators 8u..8u+7 of a lane are 8 consecutive keys, which is
+// the second product's B operand: probabilities never leave the lane. Statistics and sums
+// are fp32; probabilities are rounded to the 16-bit type for the matrix cores (their
+// relative error, 2^-9 in bf16, is that of the output's own rounding).
+#include "qmoe_attn_internal.h"
+
+namespace qmoe {
+namespace {
+
+constexpr int kTileElems = 8192;  // keys x columns of one LDS tile: 16 KB each of keys and values
+constexpr int kMinSplitKeys = 512;
+// A row's reference maximum moves only when the new maximum exceeds it by this many powers
+// of two; probabilities then reach 2^8, which fp32 sums and both 16-bit types hold.
+constexpr float kLazy = 8.0f;
+
+struct PrefillParams {
+  HeadView q;
+  const char* ck;
+  const char* cv;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* table;
+  const int32_t* kv_lens;
+  const int32_t* q_starts;
+  long long table_stride;
+  char* out;
+  float* partial;
+  float2* stats;
+  float scale;  // times log2(e)
+  KeyMask mask;
+  int num_pages, page_shift, kv_heads, max_pages;
+  int n, n_seqs, group, splits, slots;
+};
+
+// Sequence s has the row-tile slots floor(q_starts[s] * group / BM) + s up to the next
+// sequence's: enough for its own tiles, found without a prefix sum. The values are held
+// inside [0, n] whatever the array says.
+__device__ __forceinline__ int q_start(const PrefillParams& p, int s) {
+  return max(0, min(p.q_starts[s], p.n));
+}
+
+template <int BM>
+__device__ __forceinline__ int first_slot(const PrefillParams& p, int s) {
+  return (int)((long long)q_start(p, s) * p.group / BM) + s;
+}
+
+// One row tile: rows row0 .. row0 + BM - 1 of sequence seq (fewer at its end).
+struct RowTile {
+  int seq, start, rows, row0, first_pos, len;  // first_pos: of the sequence's first token
+  TileList keys;
+  int per, live;
+};
+
+template <int BM, int KT>
+__device__ __forceinline__ RowTile row_tile(const PrefillParams& p, int seq, int tile) {
+  RowTile t;
+  t.seq = seq;
+  t.start = q_start(p, seq);
+  const int m = max(0, q_start(p, seq + 1) - t.start);
+  t.rows = m * p.group;
+  t.row0 = tile * BM;
+  const long long cap = (long long)p.max_pages << p.page_shift;
+  t.len = (int)max(0ll, min((long long)p.kv_lens[seq], cap));
+  t.first_pos = t.len - m;
+  const int a = t.first_pos + t.row0 / p.group;
+  const int b = t.first_pos + (min(t.row0 + BM, t.rows) - 1) / p.group;
+  t.keys = visible_tiles<KT>(p.mask, a, b);
+  t.per = max(kMinSplitKeys / KT, (t.keys.count + p.splits - 1) / p.splits);
+  t.live = (t.keys.count + t.per - 1) / t.per;
+  return t;
+}
+
+#if defined(__HIP_DEVICE_COMPILE__)
+
+template <int D>
+__device__ __forceinline__ int key_swizzle(int row) {
+  return D == 64 ? (row >> 1) & 7 : row & 15;
+}
+
+// A thread's part of one key tile on its way from the cache to LDS.
+template <typename A, int D, bool F8, int KT, int THREADS>
+struct Stage {
+  static constexpr int PER_CHUNK = F8 ? 16 : 8;  // elements of a 16-byte chunk
+  static constexpr int COLS = D / PER_CHUNK;     // chunks of a key row
+  static constexpr int N = KT * D / PER_CHUNK / THREADS;
+  static_assert(KT * D / PER_CHUNK % THREADS == 0, "whole chunks");
+  static constexpr int BLOCK = F8 ? D / 2 : D;  // chunks of a group of 8 value rows
+  u32x4 k[N], v[N];
+  int kid[N], vid[N];  // page numbers
+
+  __device__ __forceinline__ int page_of(const PrefillParams& p, const int32_t* table, int key) {
+    return table[min(key >> p.page_shift, p.max_pages - 1)];
+  }
+  __device__ __forceinline__ void ids(const PrefillParams& p, const int32_t* table, int key0,
+                                      int tid) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = tid + i * THREADS;
+      kid[i] = page_of(p, table, key0 + c / COLS);
+      vid[i] = page_of(p, table, key0 + 8 * (c / BLOCK));
+    }
+  }
+  __device__ __forceinline__ long long row_of(const PrefillParams& p, int id, int kvh, int key) {
+    const long long page = (unsigned)id < (unsigned)p.num_pages ? id : 0;
+    return ((page * p.kv_heads + kvh) << p.page_shift) + (key & ((1 << p.page_shift) - 1));
+  }
+  __device__ __forceinline__ void load(const PrefillParams& p, int kvh, int key0, int tid) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = tid + i * THREADS;
+      const long long kr = row_of(p, kid[i], kvh, key0 + c / COLS);
+      k[i] = *reinterpret_cast<const u32x4*>(p.ck + kr * (D * (F8 ? 1 : 2)) + 16 * (c % COLS));
+      const long long vr = row_of(p, vid[i], kvh, key0 + 8 * (c / BLOCK));
+      v[i] = *reinterpret_cast<const u32x4*>(p.cv + vr * (D * (F8 ? 1 : 2)) + 16 * (c % BLOCK));
+    }
+  }
+  __device__ __forceinline__ void store(u32x4* lk, u32x4* lv, int tid) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = tid + i * THREADS;
+      const int row = c / COLS, col = c % COLS, sw = key_swizzle<D>(row);
+      if constexpr (F8) {
+        lk[row * (D / 8) + ((2 * col) ^ sw)] = bits_as<u32x4>(expand_e4m3<A>(k[i][0], k[i][1]));
+        lk[row * (D / 8) + ((2 * col + 1) ^ sw)] =
+            bits_as<u32x4>(expand_e4m3<A>(k[i][2], k[i][3]));
+        lv[2 * c] = bits_as<u32x4>(expand_e4m3<A>(v[i][0], v[i][1]));
+        lv[2 * c + 1] = bits_as<u32x4>(expand_e4m3<A>(v[i][2], v[i][3]));
+      } else {
+        lk[row * (D / 8) + (col ^ sw)] = k[i];
+        lv[c] = v[i];
+      }
+    }
+  }
+};
+
+// Whether one of the tile's pages up to the last visible key lies outside the cache.
+template <int KT>
+__device__ __forceinline__ bool bad_page(const PrefillParams& p, const int32_t* table, int key0,
+                                         int last_key) {
+  const int i0 = key0 >> p.page_shift;
+  const int i1 = min(key0 + KT - 1, last_key) >> p.page_shift;
+  bool bad = false;
+  for (int i = i0; i <= i1; ++i)
+    bad |= (unsigned)load_uniform(table + i) >= (unsigned)p.num_pages;
+  return bad;
+}
+
+#endif  // __HIP_DEVICE_COMPILE__
+
+template <typename A, int D, bool F8, int NW>
+__global__ __launch_bounds__(64 * NW) void k_attn_prefill(PrefillParams p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef typename A::V8 V8;
+  constexpr int KT = kTileElems / D, BM = 32 * NW, THREADS = 64 * NW;
+  constexpr int KS = D / 16, DT = D / 32, HALVES = KT / 32;
+  __shared__ u32x4 lk[2][KT * D / 8], lv[2][KT * D / 8];
+
+  // Workgroups go to the 8 XCDs in turn: with the kv head in the low digits, an XCD's
+  // workgroups share few heads' keys in its L2. Later row tiles see more keys: they start
+  // first.
+  const int kvh = blockIdx.x % p.kv_heads;
+  const int slot = p.slots - 1 - blockIdx.x / p.kv_heads;
+  int seq = 0;
+  for (int lo = 0, hi = p.n_seqs - 1; lo <= hi;) {  // last sequence with first_slot <= slot
+    const int mid = (lo + hi) / 2;
+    if (first_slot<BM>(p, mid) <= slot) {
+      seq = mid;
+      lo = mid + 1;
+    } else {
+      hi = mid - 1;
+    }
+  }
+  const int index = slot - first_slot<BM>(p, seq);
+  if (index < 0 || (long long)index * BM >= (long long)max(0, q_start(p, seq + 1) -
+                                                              q_start(p, seq)) * p.group)
+    return;
+  const RowTile t = row_tile<BM, KT>(p, seq, index);
+  const int split = blockIdx.y;
+  const bool direct = t.live <= 1;
+  if (split >= t.live && !(direct && split == 0)) return;
+  const int i0 = split * t.per, i1 = min(i0 + t.per, t.keys.count);
+
+  const int tid = threadIdx.x, lane = tid % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int n32 = lane & 31, h = lane >> 5;
+  const int32_t* table = p.table + seq * p.table_stride;
+  const int hq = p.kv_heads * p.group;
+
+  // this lane's query row
+  const int wrow = t.row0 + 32 * wave;  // the wave's first row
+  const bool real = wrow + n32 < t.rows;
+  const int row = real ? wrow + n32 : t.row0;
+  const int token = t.start + row / p.group, head = kvh * p.group + row % p.group;
+  const int pos = real ? t.first_pos + row / p.group : -1;
+  const bool any = wrow < t.rows;
+  const int pos_min = t.first_pos + wrow / p.group;
+  const int pos_max = t.first_pos + (min(wrow + 32, t.rows) - 1) / p.group;
+  const int last_key = t.first_pos + (min(t.row0 + BM, t.rows) - 1) / p.group;
+
+  // scale >= 0 below, so that the maximum commutes with it: its sign goes into q, and a
+  // zero scale into q as a whole
+  float scale = p.scale * (p.k_scale ? p.k_scale[kvh] : 1.0f);
+  const uint32_t flip = scale < 0.0f ? 0x80008000u : 0u;
+  const uint32_t keep = scale == 0.0f || !real ? 0u : 0xffffffffu;
+  scale = scale == 0.0f ? 1.0f : __builtin_fabsf(scale);
+  V8 q[KS];
+  {
+    const char* src = p.q.data + 2 * ((long long)token * p.q.token_stride +
+                                      (long long)head * p.q.head_stride);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      u32x4 w = *reinterpret_cast<const u32x4*>(src + 2 * (16 * ks + 8 * h));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = (w[i] ^ flip) & keep;
+      q[ks] = bits_as<V8>(w);
+    }
+  }
+
+  f32x16 o[DT];
+#pragma unroll
+  for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) o[dt][r] = 0.0f;
+  float m = kNegInf, l = 0.0f;  // scaled reference maximum; this lane's part of the sum
+
+  Stage<A, D, F8, KT, THREADS> st;
+  bool bad = false, bad_next = false;
+  if (i0 < i1) {
+    const int key0 = t.keys.tile(i0) * KT;
+    st.ids(p, table, key0, tid);
+    st.load(p, kvh, key0, tid);
+    bad = bad_page<KT>(p, table, key0, last_key);
+    if (i0 + 1 < i1) st.ids(p, table, t.keys.tile(i0 + 1) * KT, tid);
+    st.store(lk[0], lv[0], tid);
+  }
+  __syncthreads();
+  for (int i = i0; i < i1; ++i) {
+    const int buf = (i - i0) & 1;
+    const int key0 = t.keys.tile(i) * KT;
+    const bool more = i + 1 < i1;
+    if (more) {
+      const int k1 = t.keys.tile(i + 1) * KT;
+      st.load(p, kvh, k1, tid);
+      bad_next = bad_page<KT>(p, table, k1, last_key);
+      if (i + 2 < i1) st.ids(p, table, t.keys.tile(i + 2) * KT, tid);
+    }
+    const bool sees = any && key0 <= pos_max &&
+                      (p.mask.window == 0 || key0 + KT - 1 > pos_min - p.mask.window ||
+                       key0 < p.mask.sinks);
+    if (sees) {
+      const bool full = !bad && key0 + KT - 1 <= pos_min &&
+                        (p.mask.window == 0 || key0 > pos_max - p.mask.window ||
+                         key0 + KT - 1 < p.mask.sinks);
+      f32x16 s[HALVES];
+      const int krow = (n32 & 19) | ((n32 & 4) << 1) | ((n32 & 8) >> 1);
+#pragma unroll
+      for (int x = 0; x < HALVES; ++x) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[x][r] = 0.0f;
+        const int kr = 32 * x + krow, sw = key_swizzle<D>(kr);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const V8 a = bits_as<V8>(lk[buf][kr * (D / 8) + ((2 * ks + h) ^ sw)]);
+          s[x] = A::mfma32(a, q[ks], s[x]);
+        }
+      }
+      // accumulator r of half x is key 32 x + 16 (r / 8) + 8 h + r % 8
+      if (!full) {
+#pragma unroll
+        for (int x = 0; x < HALVES; ++x)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int key = key0 + 32 * x + 16 * (r >> 3) + 8 * h + (r & 7);
+            bool ok = key_visible(p.mask, key, pos);
+            if (bad && ok) ok = (unsigned)table[key >> p.page_shift] < (unsigned)p.num_pages;
+            s[x][r] = ok ? s[x][r] : kNegInf;
+          }
+      }
+      float top = kNegInf;
+#pragma unroll
+      for (int x = 0; x < HALVES; ++x)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, s[x][r]);
+      top = fmaxf(top, __shfl_xor(top, 32)) * scale;
+      const bool moves = top > m + kLazy;
+      if (__builtin_amdgcn_ballot_w64(moves) != 0) {
+        const float now = moves ? top : m;
+        const float a = exp2_fast(m - (now == kNegInf ? 0.0f : now));
+        l *= a;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) o[dt] *= a;
+        m = now;
+      }
+      const float base = m == kNegInf ? 0.0f : -m;
+      V8 pr[2 * HALVES];
+#pragma unroll
+      for (int x = 0; x < HALVES; ++x) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          s[x][r] = exp2_fast(__builtin_fmaf(s[x][r], scale, base));
+          l += s[x][r];
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          f32x8 y;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[j] = s[x][8 * u + j];
+          pr[2 * x + u] = __builtin_convertvector(y, V8);
+        }
+      }
+      bool dirty = false;  // a masked tile with non-finite values somewhere
+#pragma unroll
+      for (int ks = 0; ks < 2 * HALVES; ++ks)
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) {
+          V8 a = bits_as<V8>(lv[buf][(2 * ks + h) * D + 32 * dt + n32]);
+          if (!full) dirty |= clear_nonfinite<A>(a);
+          o[dt] = A::mfma32(a, pr[ks], o[dt]);
+        }
+      if (!full && __builtin_amdgcn_ballot_w64(dirty) != 0) {
+        // A zero probability times a non-finite value is NaN, so such values of a tile that
+        // not all rows see were left out above; here they reach the rows that see them.
+#pragma unroll 1
+        for (int key = 0; key < KT; ++key) {
+          bool ok = key_visible(p.mask, key0 + key, pos);
+          if (bad && ok)
+            ok = (unsigned)table[(key0 + key) >> p.page_shift] < (unsigned)p.num_pages;
+          if (__builtin_amdgcn_ballot_w64(ok) == 0) continue;
+          float w = 0.0f;
+#pragma unroll
+          for (int x = 0; x < HALVES; ++x)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              w = (key & ~8) == 32 * x + 16 * (r >> 3) + (r & 7) ? s[x][r] : w;
+          w = __shfl(w, ((key & 8) << 2) | n32);
+          const typename A::T* col =
+              reinterpret_cast<const typename A::T*>(&lv[buf][(key >> 3) * D]) + (key & 7);
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              const float x = (float)col[8 * (32 * dt + 8 * (r >> 2) + 4 * h + (r & 3))];
+              if (ok && !__builtin_isfinite(x)) o[dt][r] += w * x;
+            }
+        }
+      }
+    }
+    if (more) st.store(lk[buf ^ 1], lv[buf ^ 1], tid);
+    bad = bad_next;
+    __syncthreads();
+  }
+
+  l += __shfl_xor(l, 32);
+  if (!real) return;
+  const long long at = (long long)token * hq + head;
+  if (direct) {
+    const float vs = p.v_scale ? p.v_scale[kvh] : 1.0f;
+    const float inv = l == 0.0f ? 0.0f : vs / l;
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+      for (int r4 = 0; r4 < 4; ++r4) {
+        f32x4 y;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) y[c] = o[dt][4 * r4 + c] * inv;
+        *reinterpret_cast<u32x2*>(p.out + 2 * (at * D + 32 * dt + 8 * r4 + 4 * h)) =
+            bits_as<u32x2>(__builtin_convertvector(y, typename A::V4));
+      }
+  } else {
+    const long long part = at * p.splits + split;
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+      for (int r4 = 0; r4 < 4; ++r4) {
+        f32x4 y;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) y[c] = o[dt][4 * r4 + c];
+        *reinterpret_cast<f32x4*>(p.partial + part * D + 32 * dt + 8 * r4 + 4 * h) = y;
+      }
+    if (h == 0) p.stats[part] = make_float2(m, l);
+  }
+#endif
+}
+
+// Joins the splits of one (token, query head) row.
+template <typename A, int D, int NW>
+__global__ __launch_bounds__(kJoinThreads) void k_attn_prefill_join(PrefillParams p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int KT = kTileElems / D, BM = 32 * NW;
+  const int hq = p.kv_heads * p.group;
+  const int token = blockIdx.x / hq, head = blockIdx.x % hq;
+  int seq = -1;
+  for (int lo = 0, hi = p.n_seqs - 1; lo <= hi;) {  // last sequence that starts at or before
+    const int mid = (lo + hi) / 2;
+    if (q_start(p, mid) <= token) {
+      seq = mid;
+      lo = mid + 1;
+    } else {
+      hi = mid - 1;
+    }
+  }
+  if (seq < 0 || token >= q_start(p, seq + 1)) return;
+  const int kvh = head / p.group;
+  const int row = (token - q_start(p, seq)) * p.group + head % p.group;
+  const RowTile t = row_tile<BM, KT>(p, seq, row / BM);
+  if (t.live <= 1) return;  // written by its only split
+  join_row<A, D>(p.partial, p.stats, blockIdx.x, p.splits, t.live,
+                 p.v_scale ? p.v_scale[kvh] : 1.0f, p.out);
+#endif
+}
+
+// Waves of a workgroup (32 rows each): 8 share a key tile among the most rows. Wide heads
+// need 128 accumulators a lane and more than 256 registers, one wave a SIMD; and few rows
+// fill the card better in halves.
+int prefill_waves(int q_heads, int D, int n_tokens, int num_cus) {
+  if (D == 256) return 4;
+  return (long long)n_tokens * q_heads >= 256ll * num_cus ? 8 : 4;
+}
+
+template <typename A, int D, bool F8, int NW>
+hipError_t launch_one(const PrefillParams& p, hipStream_t stream) {
+  k_attn_prefill<A, D, F8, NW><<<dim3((unsigned)(p.slots * p.kv_heads), p.splits),
+                                 dim3(64 * NW), 0, stream>>>(p);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.splits == 1) return e;
+  k_attn_prefill_join<A, D, NW><<<dim3((unsigned)(p.n * p.kv_heads * p.group)),
+                                  dim3(kJoinThreads), 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+template <typename A, int D, bool F8>
+hipError_t launch_waves(const PrefillParams& p, int nw, hipStream_t stream) {
+  if constexpr (D != 256) {
+    if (nw == 8) return launch_one<A, D, F8, 8>(p, stream);
+  }
+  return launch_one<A, D, F8, 4>(p, stream);
+}
+
+template <typename A>
+hipError_t launch_type(const PrefillParams& p, int D, bool f8, int nw, hipStream_t stream) {
+  if (D == 64)
+    return f8 ? launch_waves<A, 64, true>(p, nw, stream) : launch_waves<A, 64, false>(p, nw, stream);
+  if (D == 128)
+    return f8 ? launch_waves<A, 128, true>(p, nw, stream)
+              : launch_waves<A, 128, false>(p, nw, stream);
+  return f8 ? launch_waves<A, 256, true>(p, nw, stream)
+            : launch_waves<A, 256, false>(p, nw, stream);
+}
+
+}  // namespace
+
+AttnPlan prefill_plan(int q_heads, int kv_heads, int D, int n_seqs, int n_tokens, int max_pages,
+                      int page_size, const moe_attn& a, int num_cus) {
+  AttnPlan plan{};
+  plan.tile_rows = 32 * prefill_waves(q_heads, D, n_tokens, num_cus);
+  const long long rows = (long long)n_tokens * (q_heads / kv_heads);
+  plan.row_tiles = (int)(rows / plan.tile_rows) + n_seqs;
+  // Row tiles that have rows, at least; splits fill the card when they do not.
+  const long long base = std::max(1ll, (rows + plan.tile_rows - 1) / plan.tile_rows) * kv_heads;
+  long long keys = (long long)max_pages * page_size;
+  if (a.window > 0)
+    keys = std::min(keys, (long long)a.window + n_tokens + a.sinks + 128);
+  const long long most = std::max(1ll, keys / kMinSplitKeys);
+  const long long fill = num_cus / base;
+  plan.splits = (int)std::max(1ll, std::min<long long>({fill, most, kMaxSplits}));
+  if (plan.splits > 1) {
+    const size_t parts = (size_t)n_tokens * q_heads * plan.splits;
+    plan.partial = 0;
+    plan.stats = align256(parts * D * sizeof(float));
+    plan.total = plan.stats + align256(parts * sizeof(float2));
+  }
+  return plan;
+}
+
+hipError_t launch_attn_prefill(const AttnArgs& a, const AttnPlan& plan) {
+  PrefillParams p{};
+  p.q = a.q;
+  p.ck = (const char*)a.cache.k;
+  p.cv = (const char*)a.cache.v;
+  p.k_scale = a.cache.k_scale;
+  p.v_scale = a.cache.v_scale;
+  p.table = a.pages.table;
+  p.kv_lens = a.pages.kv_lens;
+  p.q_starts = a.q_starts;
+  p.table_stride = a.pages.table_stride;
+  p.out = a.out;
+  p.partial = (float*)(a.ws + plan.partial);
+  p.stats = (float2*)(a.ws + plan.stats);
+  p.scale = a.a.scale * kLog2e;
+  p.mask = KeyMask{a.a.window, a.a.sinks};
+  p.num_pages = a.cache.num_pages;
+  while ((1 << p.page_shift) < a.cache.page_size) ++p.page_shift;
+  p.kv_heads = a.cache.kv_heads;
+  p.max_pages = a.pages.max_pages;
+  p.n = a.n;
+  p.n_seqs = a.pages.n_seqs;
+  p.group = a.q.heads / a.cache.kv_heads;
+  p.splits = plan.splits;
+  p.slots = plan.row_tiles;
+  const int nw = plan.tile_rows / 32, D = a.cache.head_dim;
+  const bool f8 = a.cache.dtype == MOE_E4M3;
+  return a.dtype == MOE_BF16 ? launch_type<Bf16>(p, D, f8, nw, a.stream)
+                             : launch_type<F16>(p, D, f8, nw, a.stream);
+}
+
+}  // namespace qmoe

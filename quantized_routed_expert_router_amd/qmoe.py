@@ -27,7 +27,9 @@ MAX_PREFILL_TOKENS = 8192
 EXPORTS = ("moe_status_string", "moe_route_workspace_bytes", "moe_route",
            "moe_ffn_workspace_bytes", "moe_expert_ffn_decode", "moe_expert_ffn_decode_stages",
            "moe_layer_decode", "moe_layer_decode_stages", "moe_layer_decode_noalloc",
-           "moe_expert_ffn_prefill", "moe_expert_ffn_prefill_stages")
+           "moe_expert_ffn_prefill", "moe_expert_ffn_prefill_stages",
+           "moe_qk_norm_rope", "moe_kv_append", "moe_attn_decode_workspace_bytes",
+           "moe_attn_decode", "moe_attn_prefill_workspace_bytes", "moe_attn_prefill")
 
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
