@@ -8,9 +8,7 @@ outputs and workspaces that a call makes for itself belong to that stream.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
-import math
 from dataclasses import dataclass
 
 import torch
@@ -72,7 +70,15 @@ _declare()
 
 
 class _HeadArgs(_Args):
-    """Checks of one call's tensors; rows of heads may be strided views."""
+    """Checks of one call's tensors; rows of heads may be strided views. Short paths for
+    tensors that pass: these calls take a few microseconds on the GPU."""
+
+    def need(self, t, name, dtypes, shape=None, min_numel=None):
+        if type(t) is torch.Tensor and min_numel is None and t.dtype in dtypes and \
+                t.is_contiguous() and (shape is None or t.shape == shape):
+            self.seen.append((name, t))
+        else:
+            super().need(t, name, dtypes, shape, min_numel)
 
     def heads(self, t, name: str, dtypes, n=None, heads=None, D=None) -> _Heads:
         if not isinstance(t, torch.Tensor) or t.dim() != 3:
@@ -80,15 +86,16 @@ class _HeadArgs(_Args):
                              f"{getattr(t, 'shape', type(t))}")
         if t.dtype not in dtypes:
             raise ValueError(f"{name}: dtype {t.dtype}, expected one of {dtypes}")
-        shape, stride = t.shape, t.stride()
-        if (n is not None and shape[0] != n) or (heads is not None and shape[1] != heads) or \
-                (D is not None and shape[2] != D):
+        a, b, c = shape = t.shape
+        if (n is not None and a != n) or (heads is not None and b != heads) or \
+                (D is not None and c != D):
             raise ValueError(f"{name}: shape {tuple(shape)}, expected "
-                             f"{(n or shape[0], heads or shape[1], D or shape[2])}")
-        if stride[2] != 1 and shape[2] != 1:
+                             f"{(a if n is None else n, heads or b, D or c)}")
+        ts, hs, last = t.stride()
+        if last != 1 and c != 1:
             raise ValueError(f"{name}: the last axis must be contiguous")
         self.seen.append((name, t))
-        return _Heads(t.data_ptr(), stride[0], stride[1], shape[1])
+        return _Heads(t.data_ptr(), ts, hs, b)
 
     def table(self, t, name: str, lens) -> _Pages:
         if not isinstance(t, torch.Tensor) or t.dim() != 2:
@@ -97,43 +104,41 @@ class _HeadArgs(_Args):
         if t.dtype not in I32:
             raise ValueError(f"{name}: dtype {t.dtype}, expected one of {I32}")
         b, most = t.shape
-        if most > 1 and t.stride(1) != 1:
+        row, last = t.stride()
+        if most > 1 and last != 1:
             raise ValueError(f"{name}: the last axis must be contiguous")
-        if b > 1 and t.stride(0) < most:
+        if b > 1 and row < most:
             raise ValueError(f"{name}: rows overlap")
         self.seen.append((name, t))
-        self.need(lens, "kv_lens", I32, shape=(b,))
-        return _Pages(t.data_ptr(), lens.data_ptr(), t.stride(0) if b > 1 else most, b, most)
+        self.need(lens, "kv_lens", I32, (b,))
+        return _Pages(t.data_ptr(), lens.data_ptr(), row if b > 1 else most, b, most)
+
+    def gpu(self) -> int:
+        """The index of the one GPU that all tensors are on."""
+        at = self.seen[0][1].get_device()
+        if at < 0:
+            self.on_gpu()
+        for _, t in self.seen:
+            if t.get_device() != at:
+                self.on_gpu()
+        return at
 
 
-@contextlib.contextmanager
-def _elsewhere(device, stream):
-    with torch.cuda.device(device):
-        if stream is None:
-            yield torch.cuda.current_stream().cuda_stream
-        else:
-            with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+def _on_stream(fn, args, stream, t):
+    """The call with `stream` current, so that what it allocates belongs to that stream."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and stream.device != t.device:
+        raise ValueError(f"stream: on {stream.device}, the tensors on {t.device}")
+    with torch.cuda.stream(stream):
+        return fn(*args)
 
 
-class _here:
-    """The device and stream of a call: the common case (current device, current stream)
-    without touching either."""
+def _raw_stream(device: int) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
 
-    def __init__(self, args: _Args, stream):
-        args.on_gpu()
-        device = args.seen[0][1].device
-        self.other = None
-        if stream is not None or device.index != torch.cuda.current_device():
-            self.other = _elsewhere(device, stream)
 
-    def __enter__(self):
-        if self.other is not None:
-            return self.other.__enter__()
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *err):
-        return self.other.__exit__(*err) if self.other is not None else None
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+_current_device = torch.cuda.current_device
+_dense = torch.contiguous_format
 
 
 @dataclass
@@ -169,10 +174,10 @@ class KVCache:
             raise ValueError(f"cache.k: shape {tuple(k.shape)}, expected [num_pages, kv_heads, "
                              "page_size, head_dim]")
         pages, heads, size, D = k.shape
-        args.need(v, "cache.v", (k.dtype,), shape=(pages, heads, size // 8, D, 8))
+        args.need(v, "cache.v", (k.dtype,), (pages, heads, size // 8, D, 8))
         for name, s in (("cache.k_scale", self.k_scale), ("cache.v_scale", self.v_scale)):
             if s is not None:
-                args.need(s, name, F32, shape=(heads,))
+                args.need(s, name, F32, (heads,))
         return _KVCache(k.data_ptr(), v.data_ptr(), _ptr(self.k_scale), _ptr(self.v_scale),
                         DTYPES[k.dtype], pages, size, heads, D)
 
@@ -192,7 +197,7 @@ class NormRope:
     def check(self, D: int, args: _Args) -> _NormRope:
         for name, w in (("q_norm", self.q_norm), ("k_norm", self.k_norm)):
             if w is not None:
-                args.need(w, name, F32, shape=(D,))
+                args.need(w, name, F32, (D,))
         rot = 0
         if self.inv_freq is not None:
             args.need(self.inv_freq, "inv_freq", F32)
@@ -204,39 +209,51 @@ class NormRope:
 _ref = ctypes.byref
 
 
+def _new_heads(like: torch.Tensor):
+    t = torch.empty_like(like, memory_format=_dense)
+    _, heads, D = like.shape
+    return t, _Heads(t.data_ptr(), heads * D, D, heads)
+
+
 def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor | None,
                  p: NormRope, q_out: torch.Tensor | None = None,
                  k_out: torch.Tensor | None = None, stream=None):
     """moe_qk_norm_rope: norm and rotation of query and key heads ``[n, heads, head_dim]``
     (either may be None) at `positions` int32 ``[n]``. Returns (q_out, k_out), new tensors
     unless given; an output may be its own input."""
-    args = _HeadArgs()
     some = q if q is not None else k
     if some is None:
         raise ValueError("q, k: at least one is needed")
+    if stream is not None:
+        return _on_stream(qk_norm_rope, (q, k, positions, p, q_out, k_out), stream, some)
+    args = _HeadArgs()
     qs = ks = qo = ko = None
     if q is not None:
         qs = args.heads(q, "q", HALF)
     n, D = some.shape[0], some.shape[-1]
     if k is not None:
-        ks = args.heads(k, "k", (some.dtype,) if some.dtype in HALF else HALF, n=n, D=D)
+        ks = args.heads(k, "k", (some.dtype,) if some.dtype in HALF else HALF, n, None, D)
     rope = p.check(D, args)
     if positions is not None:
-        args.need(positions, "positions", I32, shape=(n,))
+        args.need(positions, "positions", I32, (n,))
+    for name, x, out in (("q_out", q, q_out), ("k_out", k, k_out)):
+        if out is not None and x is None:
+            raise ValueError(f"{name}: given without its input")
     if q_out is not None:
-        qo = args.heads(q_out, "q_out", (some.dtype,), *q.shape if q is not None else (0, 0, 0))
+        qo = args.heads(q_out, "q_out", (some.dtype,), *q.shape)
     if k_out is not None:
-        ko = args.heads(k_out, "k_out", (some.dtype,), *k.shape if k is not None else (0, 0, 0))
-    with _here(args, stream) as on:
-        if q is not None and qo is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            qo = _Heads(q_out.data_ptr(), q.shape[1] * D, D, q.shape[1])
-        if k is not None and ko is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-            ko = _Heads(k_out.data_ptr(), k.shape[1] * D, D, k.shape[1])
-        rc = lib.moe_qk_norm_rope(qs and _ref(qs), ks and _ref(ks), _ptr(positions), n,
-                                  DTYPES[some.dtype], D, _ref(rope), qo and _ref(qo),
-                                  ko and _ref(ko), on)
+        ko = args.heads(k_out, "k_out", (some.dtype,), *k.shape)
+    gpu = args.gpu()
+    if gpu != _current_device():
+        with torch.cuda.device(gpu):
+            return qk_norm_rope(q, k, positions, p, q_out, k_out)
+    if q is not None and qo is None:
+        q_out, qo = _new_heads(q)
+    if k is not None and ko is None:
+        k_out, ko = _new_heads(k)
+    rc = lib.moe_qk_norm_rope(qs and _ref(qs), ks and _ref(ks), _ptr(positions), n,
+                              DTYPES[some.dtype], D, _ref(rope), qo and _ref(qo),
+                              ko and _ref(ko), _raw_stream(gpu))
     if rc != MOE_OK:
         raise MoeError("moe_qk_norm_rope", rc)
     return q_out, k_out
@@ -249,34 +266,39 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Ten
     cache at `slots` int32 ``[n]`` (page * page_size + row; outside the cache: not stored).
     With `q`, its heads are normed and rotated in the same launch; returns q_out (a new
     tensor unless given; None without q)."""
+    if stream is not None:
+        return _on_stream(kv_append, (cache, k, v, slots, positions, p, q, q_out), stream, k)
     args = _HeadArgs()
     ks = args.heads(k, "k", HALF)
     n, heads, D = k.shape
-    vs = args.heads(v, "v", (k.dtype,), n, heads, D)
+    same = (k.dtype,)
+    vs = args.heads(v, "v", same, n, heads, D)
     cs = cache.check(args)
     if (cs.kv_heads, cs.head_dim) != (heads, D):
         raise ValueError(f"k: shape {tuple(k.shape)}, the cache has {cs.kv_heads} heads of "
                          f"{cs.head_dim}")
-    args.need(slots, "slots", I32, shape=(n,))
+    args.need(slots, "slots", I32, (n,))
     if positions is not None:
-        args.need(positions, "positions", I32, shape=(n,))
+        args.need(positions, "positions", I32, (n,))
     rope = p.check(D, args) if p is not None else None
     qs = qo = None
     if q is not None:
         if p is None:
             raise ValueError("q: needs p, its norm and rotation")
-        qs = args.heads(q, "q", (k.dtype,), n=n, D=D)
+        qs = args.heads(q, "q", same, n, None, D)
         if q_out is not None:
-            qo = args.heads(q_out, "q_out", (k.dtype,), *q.shape)
+            qo = args.heads(q_out, "q_out", same, *q.shape)
     elif q_out is not None:
         raise ValueError("q_out: given without q")
-    with _here(args, stream) as on:
-        if q is not None and qo is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            qo = _Heads(q_out.data_ptr(), q.shape[1] * D, D, q.shape[1])
-        rc = lib.moe_kv_append(_ref(cs), _ref(ks), _ref(vs), slots.data_ptr(), _ptr(positions), n,
-                               DTYPES[k.dtype], rope and _ref(rope), qs and _ref(qs),
-                               qo and _ref(qo), on)
+    gpu = args.gpu()
+    if gpu != _current_device():
+        with torch.cuda.device(gpu):
+            return kv_append(cache, k, v, slots, positions, p, q, q_out)
+    if q is not None and qo is None:
+        q_out, qo = _new_heads(q)
+    rc = lib.moe_kv_append(_ref(cs), _ref(ks), _ref(vs), slots.data_ptr(), _ptr(positions), n,
+                           DTYPES[k.dtype], rope and _ref(rope), qs and _ref(qs),
+                           qo and _ref(qo), _raw_stream(gpu))
     if rc != MOE_OK:
         raise MoeError("moe_kv_append", rc)
     return q_out
@@ -285,27 +307,26 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Ten
 def _attn(scale, window: int, sinks: int, D: int) -> _Attn:
     if not 0 <= window < 1 << 31 or not 0 <= sinks < 1 << 31:
         raise ValueError(f"window, sinks: {window}, {sinks}, expected 0..2^31-1")
-    return _Attn(1.0 / math.sqrt(D) if scale is None else scale, window, sinks)
+    return _Attn(D ** -0.5 if scale is None else scale, window, sinks)
 
 
 def decode_workspace_bytes(cache: KVCache, q_heads: int, n_seqs: int, window_tokens: int,
                            max_pages: int, window: int = 0, sinks: int = 0) -> int:
-    """moe_attn_decode_workspace_bytes."""
+    """moe_attn_decode_workspace_bytes: workspace of attn_decode calls of these sizes."""
     cs = cache.check(_HeadArgs())
-    return int(lib.moe_attn_decode_workspace_bytes(_ref(cs), q_heads, n_seqs, window_tokens,
-                                                   max_pages, _ref(_Attn(1.0, window, sinks))))
+    return lib.moe_attn_decode_workspace_bytes(_ref(cs), q_heads, n_seqs, window_tokens,
+                                               max_pages, _ref(_attn(1.0, window, sinks, 1)))
 
 
 def prefill_workspace_bytes(cache: KVCache, q_heads: int, n_seqs: int, n_tokens: int,
                             max_pages: int, window: int = 0, sinks: int = 0) -> int:
-    """moe_attn_prefill_workspace_bytes."""
+    """moe_attn_prefill_workspace_bytes: workspace of attn_prefill calls of these sizes."""
     cs = cache.check(_HeadArgs())
-    return int(lib.moe_attn_prefill_workspace_bytes(_ref(cs), q_heads, n_seqs, n_tokens,
-                                                    max_pages, _ref(_Attn(1.0, window, sinks))))
+    return lib.moe_attn_prefill_workspace_bytes(_ref(cs), q_heads, n_seqs, n_tokens, max_pages,
+                                                _ref(_attn(1.0, window, sinks, 1)))
 
 
-def _attend(fn: str, cache, q, page_table, kv_lens, scale, window, sinks, out, ws, stream,
-            q_starts):
+def _attend(cache, q, q_starts, page_table, kv_lens, scale, window, sinks, out, ws):
     args = _HeadArgs()
     qs = args.heads(q, "q", HALF)
     n, heads, D = q.shape
@@ -313,38 +334,46 @@ def _attend(fn: str, cache, q, page_table, kv_lens, scale, window, sinks, out, w
     if cs.head_dim != D:
         raise ValueError(f"q: head_dim {D}, the cache has {cs.head_dim}")
     pages = args.table(page_table, "page_table", kv_lens)
+    b = pages.n_seqs
     attn = _attn(scale, window, sinks, D)
-    if q_starts is not None:
-        args.need(q_starts, "q_starts", I32, shape=(pages.n_seqs + 1,))
+    prefill = q_starts is not None
+    if prefill:
+        args.need(q_starts, "q_starts", I32, (b + 1,))
         size = n
     else:
-        if n % max(1, pages.n_seqs) or (pages.n_seqs == 0) != (n == 0):
-            raise ValueError(f"q: {n} tokens, expected a multiple of {pages.n_seqs} sequences")
-        size = n // max(1, pages.n_seqs)
+        size = n // b if b else 0
+        if size * b != n:
+            raise ValueError(f"q: {n} tokens, expected a multiple of {b} sequences")
     if out is not None:
-        args.need(out, "out", (q.dtype,), shape=q.shape)
+        args.need(out, "out", (q.dtype,), q.shape)
     if ws is not None:
         args.need(ws, "ws", BYTES)
-    with _here(args, stream) as on:
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if n == 0:
-            return out
-        if ws is None:
-            query = (lib.moe_attn_prefill_workspace_bytes if q_starts is not None
-                     else lib.moe_attn_decode_workspace_bytes)
-            need = query(_ref(cs), heads, pages.n_seqs, size, pages.max_pages, _ref(attn))
-            if need:
-                ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-        at, room = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
-        if q_starts is not None:
-            rc = lib.moe_attn_prefill(_ref(cs), _ref(qs), DTYPES[q.dtype], q_starts.data_ptr(), n,
-                                      _ref(pages), _ref(attn), out.data_ptr(), at, room, on)
-        else:
-            rc = lib.moe_attn_decode(_ref(cs), _ref(qs), DTYPES[q.dtype], _ref(pages), size,
-                                     _ref(attn), out.data_ptr(), at, room, on)
+    gpu = args.gpu()
+    if gpu != _current_device():
+        with torch.cuda.device(gpu):
+            return _attend(cache, q, q_starts, page_table, kv_lens, scale, window, sinks, out, ws)
+    if out is None:
+        out = torch.empty_like(q, memory_format=_dense)
+    if n == 0:
+        return out
+    if ws is None:
+        query = (lib.moe_attn_prefill_workspace_bytes if prefill
+                 else lib.moe_attn_decode_workspace_bytes)
+        room = query(_ref(cs), heads, b, size, pages.max_pages, _ref(attn))
+        if room:
+            ws = q.new_empty(room, dtype=torch.uint8)
+    else:
+        room = ws.numel()
+    at = ws.data_ptr() if room else None
+    if prefill:
+        rc = lib.moe_attn_prefill(_ref(cs), _ref(qs), DTYPES[q.dtype], q_starts.data_ptr(), n,
+                                  _ref(pages), _ref(attn), out.data_ptr(), at, room,
+                                  _raw_stream(gpu))
+    else:
+        rc = lib.moe_attn_decode(_ref(cs), _ref(qs), DTYPES[q.dtype], _ref(pages), size,
+                                 _ref(attn), out.data_ptr(), at, room, _raw_stream(gpu))
     if rc != MOE_OK:
-        raise MoeError(fn, rc)
+        raise MoeError("moe_attn_prefill" if prefill else "moe_attn_decode", rc)
     return out
 
 
@@ -355,8 +384,10 @@ def attn_decode(cache: KVCache, q: torch.Tensor, page_table: torch.Tensor, kv_le
     ``[n_seqs * tokens, heads, head_dim]``, sequence-major, the same number of tokens (1..16)
     of each; page_table int32 ``[n_seqs, max_pages]``; kv_lens int32 ``[n_seqs]``, the new
     tokens included. scale: 1/sqrt(head_dim) unless given. Returns out."""
-    return _attend("moe_attn_decode", cache, q, page_table, kv_lens, scale, window, sinks, out, ws,
-                   stream, None)
+    if stream is not None:
+        return _on_stream(attn_decode, (cache, q, page_table, kv_lens, scale, window, sinks, out,
+                                        ws), stream, q)
+    return _attend(cache, q, None, page_table, kv_lens, scale, window, sinks, out, ws)
 
 
 def attn_prefill(cache: KVCache, q: torch.Tensor, q_starts: torch.Tensor,
@@ -368,5 +399,7 @@ def attn_prefill(cache: KVCache, q: torch.Tensor, q_starts: torch.Tensor,
     last of its kv_lens[s] keys. Rows from q_starts[n_seqs] on are not written. Returns out."""
     if q_starts is None:
         raise ValueError("q_starts: expected a tensor [n_seqs + 1]")
-    return _attend("moe_attn_prefill", cache, q, page_table, kv_lens, scale, window, sinks, out,
-                   ws, stream, q_starts)
+    if stream is not None:
+        return _on_stream(attn_prefill, (cache, q, q_starts, page_table, kv_lens, scale, window,
+                                         sinks, out, ws), stream, q)
+    return _attend(cache, q, q_starts, page_table, kv_lens, scale, window, sinks, out, ws)

@@ -12,14 +12,18 @@
 // are fp32; the probabilities enter the second product as a 16-bit value plus the 16-bit
 // rest (2^-16 relative and better), which costs matrix-core time that the memory-bound
 // loop has to spare.
+#include <type_traits>
+
 #include "qmoe_attn_internal.h"
 
 namespace qmoe {
 namespace {
 
-constexpr int kThreads = kJoinThreads;
-[[maybe_unused]] constexpr int kWaves = kThreads / kWave;
+constexpr int kWaves = 4;           // waves that share a row group's keys
 constexpr int kTile = 32;           // keys of one step of a wave
+// A row's reference maximum moves only when the new maximum exceeds it by this many powers
+// of two; probabilities then reach 2^8, which fp32 sums and both 16-bit types hold.
+constexpr float kLazy = 8.0f;
 constexpr int kMinSplitTiles = 8;   // 256 keys: below that a split costs more than it saves
 
 struct DecodeParams {
@@ -59,28 +63,21 @@ __device__ __forceinline__ SeqSplit seq_split(const DecodeParams& p, int seq) {
 
 #if defined(__HIP_DEVICE_COMPILE__)
 
-// Where a 32-key tile's two 16-row halves lie: for pages of 32 rows or more both are in
-// one page; with 16-row pages each has its own. An entry outside the cache counts as
-// invisible (ok false) and reads page 0 instead.
-struct TilePages {
-  long long base[2];  // row offset (rows of all heads' pages) of each half, head 0
-  bool ok[2];
-};
+// A 32-key tile's two 16-row halves: with pages of 32 rows or more both are in one page,
+// with 16-row pages each has its own. The page number of half u, -1 for an entry outside
+// the cache: its keys count as invisible, and page 0 is read instead.
+__device__ __forceinline__ int half_page(const DecodeParams& p, const int32_t* table, int tile,
+                                         int u) {
+  const int i = (tile * kTile + 16 * u) >> p.page_shift;
+  const int id = i < p.max_pages ? load_uniform(table + i) : -1;
+  return (unsigned)id < (unsigned)p.num_pages ? id : -1;
+}
 
-__device__ __forceinline__ TilePages tile_pages(const DecodeParams& p, const int32_t* table,
-                                                int tile) {
-  TilePages t;
-  const int row = tile * kTile;
-  const int i0 = row >> p.page_shift;
-  const int i1 = (row + 16) >> p.page_shift;
-  const int id0 = load_uniform(table + i0);
-  const int id1 = i1 < p.max_pages ? load_uniform(table + i1) : -1;
-  t.ok[0] = (unsigned)id0 < (unsigned)p.num_pages;
-  t.ok[1] = (unsigned)id1 < (unsigned)p.num_pages;
-  const int in = (1 << p.page_shift) - 1;
-  t.base[0] = ((long long)(t.ok[0] ? id0 : 0) * p.kv_heads << p.page_shift) + (row & in);
-  t.base[1] = ((long long)(t.ok[1] ? id1 : 0) * p.kv_heads << p.page_shift) + ((row + 16) & in);
-  return t;
+// First row of half u in the cache (counting the rows of all heads' pages).
+__device__ __forceinline__ long long half_row(const DecodeParams& p, int page, int kvh, int tile,
+                                              int u) {
+  const long long rows = ((long long)max(page, 0) * p.kv_heads + kvh) << p.page_shift;
+  return rows + ((tile * kTile + 16 * u) & ((1 << p.page_shift) - 1));
 }
 
 template <typename A, int D, bool F8>
@@ -94,36 +91,38 @@ struct ValueRegs {
   u32x4 w[N];
 };
 
+// Each cache line is used once a call: non-temporal loads read 7.1 TB/s here, plain ones 6.2.
+__device__ __forceinline__ u32x4 stream_load(const char* p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+}
+
 // Lane (m, g): 8 columns 32 i + 8 g of key row 8 (m / 4) + m % 4 + 4 u; at 8 bits, 16
 // columns 64 i + 16 g, two steps of the product.
 template <typename A, int D, bool F8>
-__device__ __forceinline__ void load_keys(KeyRegs<A, D, F8>& r, const char* ck, const TilePages& t,
-                                          long long head, int lane) {
+__device__ __forceinline__ void load_keys(KeyRegs<A, D, F8>& r, const char* ck, long long row0,
+                                          long long row1, int lane) {
   const int m = lane & 15, g = lane >> 4;
   const int row = 8 * (m >> 2) + (m & 3);
-  const long long base = (row & 16 ? t.base[1] : t.base[0]) + head + (row & 15);
+  constexpr int ROW = F8 ? D : 2 * D;  // bytes
+  const char* at = ck + ((row & 16 ? row1 : row0) + (row & 15)) * ROW + 16 * g;
 #pragma unroll
   for (int u = 0; u < 2; ++u)
 #pragma unroll
-    for (int i = 0; i < KeyRegs<A, D, F8>::N; ++i) {
-      const long long at = F8 ? (base + 4 * u) * D + 64 * i + 16 * g
-                              : ((base + 4 * u) * D + 32 * i + 8 * g) * 2;
-      r.w[u][i] = *reinterpret_cast<const u32x4*>(ck + at);
-    }
+    for (int i = 0; i < KeyRegs<A, D, F8>::N; ++i)
+      r.w[u][i] = stream_load(at + 4 * u * ROW + 64 * i);
 }
 
 // Lane (m, g): keys 8 g .. 8 g + 7 of column 16 i + m; at 8 bits of columns 32 i + 2 m and
 // the next.
 template <typename A, int D, bool F8>
-__device__ __forceinline__ void load_values(ValueRegs<A, D, F8>& r, const char* cv,
-                                            const TilePages& t, long long head, int lane) {
+__device__ __forceinline__ void load_values(ValueRegs<A, D, F8>& r, const char* cv, long long row0,
+                                            long long row1, int lane) {
   const int m = lane & 15, g = lane >> 4;
-  const long long block = (((g & 2 ? t.base[1] : t.base[0]) + head) >> 3) + (g & 1);
+  const long long block = ((g & 2 ? row1 : row0) >> 3) + (g & 1);
+  const char* at = cv + block * (D * (F8 ? 8 : 16)) + 16 * m;
 #pragma unroll
-  for (int i = 0; i < ValueRegs<A, D, F8>::N; ++i) {
-    const long long at = F8 ? (block * D + 32 * i + 2 * m) * 8 : (block * D + 16 * i + m) * 16;
-    r.w[i] = *reinterpret_cast<const u32x4*>(cv + at);
-  }
+  for (int i = 0; i < ValueRegs<A, D, F8>::N; ++i)
+    r.w[i] = stream_load(at + 256 * i);
 }
 
 template <typename A, int D, bool F8>
@@ -152,33 +151,41 @@ __device__ __forceinline__ int out_col(int dt, int row) {
   return F8 ? 32 * (dt >> 1) + 2 * row + (dt & 1) : 16 * dt + row;
 }
 
-// Element (key, column) of the tile's values, from the cache.
-template <typename A, int D, bool F8>
-__device__ __forceinline__ float value_at(const char* cv, const TilePages& t, long long head,
-                                          int key, int col) {
-  const long long block = (((key & 16 ? t.base[1] : t.base[0]) + head) >> 3) + ((key >> 3) & 1);
-  const long long at = (block * D + col) * 8 + (key & 7);
-  if constexpr (F8) {
-    const uint32_t code = (uint8_t)cv[at];
-    return (float)bits_as<typename A::V2>(A::template from_e4m3<false>(code))[0];
-  } else {
-    return (float)reinterpret_cast<const typename A::T*>(cv)[at];
-  }
-}
-
 #endif  // __HIP_DEVICE_COMPILE__
 
-template <typename A, int D, bool F8, int NT>
-__global__ __launch_bounds__(kThreads) void k_attn_decode(DecodeParams p) {
+// Row tiles (of 16 query rows) a wave takes, and row groups of a workgroup: each group's
+// four waves run through all of the split's keys for their own row tiles, the second
+// group's reads then come from the caches. What a wave takes is bounded by its registers:
+// accumulators (D/4 a row tile) beside a tile's keys and values (D/2 at 16 bits).
+template <int D>
+constexpr int kMostTiles = D == 64 ? 4 : 2;
+template <int D>
+constexpr int kMostGroups = D == 128 ? 2 : 1;
+
+// Waves a SIMD that the registers have to allow. Two rather than one where they fit: with
+// more than 256 registers a wave the accumulators would go to the accumulation registers.
+template <int D, int NT>
+constexpr int kMinWaves = D == 256 ? 1 : 2;
+
+// Wide heads leave no registers for the query fragments: they are read from LDS at each
+// tile (1 KB a step of the product, a small part of what LDS can deliver meanwhile).
+template <int D>
+constexpr bool kQueriesInLds = D == 256;
+
+template <typename A, int D, bool F8, int NT, int RG>
+__global__ __launch_bounds__(kWaves * RG * kWave, (kMinWaves<D, NT>)) void k_attn_decode(DecodeParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   typedef typename A::V8 V8;
   constexpr int KS = D / 32, DT = D / 16;
   constexpr int DC = D < 128 ? D : 128;  // columns joined at a time
-  __shared__ float sums[kWaves][16][DC + 4];
-  __shared__ float stat_m[kWaves][16], stat_l[kWaves][16];
+  __shared__ float sums[RG][kWaves][16][DC + 4];
+  __shared__ float stat_m[RG][kWaves][16], stat_l[RG][kWaves][16];
+  constexpr bool QLDS = kQueriesInLds<D>;
+  __shared__ u32x4 qs[RG][QLDS ? NT * KS : 1][kWave];
 
   const int lane = threadIdx.x % kWave;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) % kWaves;
+  const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) / kWaves;
   const int n16 = lane & 15, g = lane >> 4;
   const int split = blockIdx.x;
   const int kvh = blockIdx.y / p.row_tiles, rt = blockIdx.y % p.row_tiles;
@@ -188,17 +195,29 @@ __global__ __launch_bounds__(kThreads) void k_attn_decode(DecodeParams p) {
   if (split >= sp.live && !(direct && split == 0)) return;
   const int i0 = split * sp.per, i1 = min(i0 + sp.per, sp.tiles.count);
   const int32_t* table = p.table + seq * p.table_stride;
-  const long long head = (long long)kvh << p.page_shift;
   const int first_pos = sp.len - p.T;
   const int rows = p.T * p.group;
-  const int hq = p.kv_heads * p.group;
+  const int row0 = (rt * RG + group) * NT * 16;  // this row group's first row
+
+  KeyRegs<A, D, F8> k;
+  ValueRegs<A, D, F8> v;
+  int page0 = -1, page1 = -1, next0 = -1, next1 = -1;  // of this tile and the wave's next
+  auto first_tile = [&]() {
+    const int tile = sp.tiles.tile(i0 + wave);
+    page0 = half_page(p, table, tile, 0);
+    page1 = half_page(p, table, tile, 1);
+    load_keys<A, D, F8>(k, p.ck, half_row(p, page0, kvh, tile, 0),
+                        half_row(p, page1, kvh, tile, 1), lane);
+  };
+  if (i0 + wave < i1) first_tile();
 
   // this lane's query row of each row tile, as B operand: 8 columns a step
-  V8 q[NT][KS];
+  const ScaleSplit sc = split_scale(p.scale * (p.k_scale ? p.k_scale[kvh] : 1.0f));
+  V8 q[NT][QLDS ? 1 : KS];
   int pos[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int row = (rt * NT + nt) * 16 + n16;
+    const int row = row0 + nt * 16 + n16;
     const int t = row / p.group, h = kvh * p.group + row % p.group;
     const bool real = row < rows;
     pos[nt] = real ? first_pos + t : -1;
@@ -206,131 +225,153 @@ __global__ __launch_bounds__(kThreads) void k_attn_decode(DecodeParams p) {
                                       (long long)(real ? h : 0) * p.q.head_stride);
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
+      if (QLDS && ks % kWaves != wave) continue;
       const int col = F8 ? 64 * (ks >> 1) + 16 * g + 8 * (ks & 1) : 32 * ks + 8 * g;
       u32x4 w = *reinterpret_cast<const u32x4*>(src + 2 * col);
-      if (!real) w = u32x4{0, 0, 0, 0};
-      q[nt][ks] = bits_as<V8>(w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = real ? (w[i] ^ sc.flip) & sc.keep : 0u;
+      if constexpr (QLDS)
+        qs[group][nt * KS + ks][lane] = w;
+      else
+        q[nt][ks] = bits_as<V8>(w);
     }
   }
-  const float scale = p.scale * (p.k_scale ? p.k_scale[kvh] : 1.0f);
+  if constexpr (QLDS) __syncthreads();
 
-  KeyRegs<A, D, F8> k;
-  ValueRegs<A, D, F8> v;
-  TilePages here{}, next{};
   f32x4 o[NT][DT];
-  float m[NT], l[NT];  // reference maximum of the row; this lane's part of the running sum
+  float m[NT], l[NT];  // scaled reference maximum of the row; this lane's part of its sum
+
   // A second, careful pass runs only where the first one's sums are not all finite: there
-  // the split probability's small part would turn a visible infinity into NaN.
-  bool careful = false;
-again:
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    m[nt] = kNegInf;
-    l[nt] = 0.0f;
-#pragma unroll
-    for (int dt = 0; dt < DT; ++dt) o[nt][dt] = f32x4{0, 0, 0, 0};
-  }
-
-  if (i0 + wave < i1) {
-    here = tile_pages(p, table, sp.tiles.tile(i0 + wave));
-    load_keys<A, D, F8>(k, p.ck, here, head, lane);
-  }
-  for (int i = i0 + wave; i < i1; i += kWaves) {
-    const int tile = sp.tiles.tile(i);
-    load_values<A, D, F8>(v, p.cv, here, head, lane);
-    const bool more = i + kWaves < i1;
-    if (more) next = tile_pages(p, table, sp.tiles.tile(i + kWaves));
-
-    f32x4 s[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = f32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const V8 a = key_step<A, D, F8>(k, u, ks);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) s[nt][u] = A::mfma16(a, q[nt][ks], s[nt][u]);
-      }
-    if (more) load_keys<A, D, F8>(k, p.ck, next, head, lane);
-
-    // all keys of the tile visible to all of the window's rows?
-    const int key0 = tile * kTile;
-    const bool full = !careful && here.ok[0] && here.ok[1] && key0 + kTile - 1 <= first_pos &&
-                      (p.mask.window == 0 || key0 > sp.len - 1 - p.mask.window ||
-                       key0 + kTile - 1 < p.mask.sinks);
-    V8 ph[NT], pl[NT];
-    f32x8 pr[NT];
+  // the split probability's small part would turn a visible infinity into NaN. It treats
+  // every tile as one that not all rows see.
+#pragma unroll 1
+  for (bool careful = false;;) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float x[8];
+      m[nt] = kNegInf;
+      l[nt] = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = s[nt][j >> 2][j & 3] * scale;
-      if (!full) {
-        const bool ok = g & 2 ? here.ok[1] : here.ok[0];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          x[j] = ok && key_visible(p.mask, key0 + 8 * g + j, pos[nt]) ? x[j] : kNegInf;
-      }
-      float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
-                        fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
-      const float now = fmaxf(m[nt], top);
-      if (__builtin_amdgcn_ballot_w64(now > m[nt]) != 0) {
-        const float a = exp2_fast(m[nt] - (now == kNegInf ? 0.0f : now));
-        l[nt] *= a;
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt) o[nt][dt] *= a;
-        m[nt] = now;
-      }
-      const float base = m[nt] == kNegInf ? 0.0f : m[nt];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        pr[nt][j] = exp2_fast(x[j] - base);
-        l[nt] += pr[nt][j];
-      }
-      ph[nt] = __builtin_convertvector(pr[nt], V8);
-      pl[nt] = __builtin_convertvector(pr[nt] - __builtin_convertvector(ph[nt], f32x8), V8);
+      for (int dt = 0; dt < DT; ++dt) o[nt][dt] = f32x4{0, 0, 0, 0};
     }
+    if (careful) first_tile();
+#pragma unroll 1
+    for (int i = i0 + wave; i < i1; i += kWaves) {
+      const int tile = sp.tiles.tile(i), key0 = tile * kTile;
+      load_values<A, D, F8>(v, p.cv, half_row(p, page0, kvh, tile, 0),
+                            half_row(p, page1, kvh, tile, 1), lane);
+      const bool more = i + kWaves < i1;
+      const int tile1 = sp.tiles.tile(i + kWaves);
+      if (more) {
+        next0 = half_page(p, table, tile1, 0);
+        next1 = half_page(p, table, tile1, 1);
+      }
 
-    bool dirty = false;  // a masked tile with non-finite values somewhere
+      f32x4 s[NT][2];
 #pragma unroll
-    for (int dt = 0; dt < DT; ++dt) {
-      V8 a = value_step<A, D, F8>(v, dt);
-      if (!full) dirty |= clear_nonfinite<A>(a);
+      for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        V8 qf[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if constexpr (QLDS)
+            qf[nt] = bits_as<V8>(qs[group][nt * KS + ks][lane]);
+          else
+            qf[nt] = q[nt][ks];
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const V8 a = key_step<A, D, F8>(k, u, ks);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) s[nt][u] = A::mfma16(a, qf[nt], s[nt][u]);
+        }
+      }
+      if (more)
+        load_keys<A, D, F8>(k, p.ck, half_row(p, next0, kvh, tile1, 0),
+                            half_row(p, next1, kvh, tile1, 1), lane);
+
+      // all keys of the tile visible to all of the window's rows?
+      const bool full = !careful && (page0 | page1) >= 0 && key0 + kTile - 1 <= first_pos &&
+                        (p.mask.window == 0 || key0 > sp.len - 1 - p.mask.window ||
+                         key0 + kTile - 1 < p.mask.sinks);
+      bool dirty = false;  // not full, with non-finite values somewhere
+      const bool on_page = (g & 2 ? page1 : page0) >= 0;
+      if (!full) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (!(on_page && key_visible(p.mask, key0 + 8 * g + j, pos[nt])))
+              s[nt][j >> 2][j & 3] = kNegInf;
+#pragma unroll
+        for (int j = 0; j < ValueRegs<A, D, F8>::N; ++j) dirty |= clear_word<A, F8>(v.w[j]);
+      }
+
+      V8 ph[NT], pl[NT];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        o[nt][dt] = A::mfma16(a, ph[nt], o[nt][dt]);
-        o[nt][dt] = A::mfma16(a, pl[nt], o[nt][dt]);
-      }
-    }
-    if (!full && __builtin_amdgcn_ballot_w64(dirty) != 0) {
-      // A zero probability times a non-finite value is NaN, so such values of a tile that
-      // not all rows see were left out above; here they reach the rows that see them.
+        float top = fmaxf(fmaxf(fmaxf(s[nt][0][0], s[nt][0][1]), fmaxf(s[nt][0][2], s[nt][0][3])),
+                          fmaxf(fmaxf(s[nt][1][0], s[nt][1][1]), fmaxf(s[nt][1][2], s[nt][1][3])));
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32)) * sc.scale;
+        const bool moves = top > m[nt] + kLazy;
+        if (__builtin_amdgcn_ballot_w64(moves) != 0) {
+          const float now = moves ? top : m[nt];
+          const float a = rescale(m[nt] - (now == kNegInf ? 0.0f : now));
+          l[nt] *= a;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll 1
-        for (int key = 0; key < kTile; ++key) {
-          const bool seen = (key & 16 ? here.ok[1] : here.ok[0]) &&
-                            key_visible(p.mask, key0 + key, pos[nt]);
-          if (__builtin_amdgcn_ballot_w64(seen) == 0) continue;
-          float w = pr[nt][0];
-#pragma unroll
-          for (int j = 1; j < 8; ++j) w = (key & 7) == j ? pr[nt][j] : w;
-          w = __shfl(w, ((key >> 3) << 4) + n16);
-#pragma unroll
-          for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float x = value_at<A, D, F8>(p.cv, here, head, key, out_col<F8>(dt, 4 * g + r));
-              if (seen && !__builtin_isfinite(x)) o[nt][dt][r] += w * x;
-            }
+          for (int dt = 0; dt < DT; ++dt) o[nt][dt] *= a;
+          m[nt] = now;
         }
+        const float base = m[nt] == kNegInf ? 0.0f : -m[nt];
+        f32x8 pr;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          pr[j] = exp2_fast(__builtin_fmaf(s[nt][j >> 2][j & 3], sc.scale, base));
+          l[nt] += pr[j];
+        }
+        ph[nt] = __builtin_convertvector(pr, V8);
+        pl[nt] = __builtin_convertvector(pr - __builtin_convertvector(ph[nt], f32x8), V8);
+      }
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) {
+        const V8 a = value_step<A, D, F8>(v, dt);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          o[nt][dt] = A::mfma16(a, ph[nt], o[nt][dt]);
+          o[nt][dt] = A::mfma16(a, pl[nt], o[nt][dt]);
+        }
+      }
+      if (!full && __builtin_amdgcn_ballot_w64(dirty) != 0) {
+        // the values as they are, once more: what they do to the rows that see them
+        load_values<A, D, F8>(v, p.cv, half_row(p, page0, kvh, tile, 0),
+                              half_row(p, page1, kvh, tile, 1), lane);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          uint32_t seen = 0;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            seen |= (uint32_t)(on_page && key_visible(p.mask, key0 + 8 * g + j, pos[nt])) << j;
+          const V8 rows_seen = mask_elements<A>(seen);
+#pragma unroll 1
+          for (int i = 0; i < 3; ++i) {
+            const NonFinite kind = non_finite_kind<A>(i);
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt) {
+              // nothing computed from the values is kept from one kind to the next
+              asm volatile("" : "+v"(v.w[dt * ValueRegs<A, D, F8>::N / DT]));
+              const f32x4 c = A::mfma16(non_finite<A>(value_step<A, D, F8>(v, dt), kind),
+                                        rows_seen, f32x4{0, 0, 0, 0});
+#pragma unroll
+              for (int r = 0; r < 4; ++r) o[nt][dt][r] += spread(c[r], kind);
+            }
+          }
+        }
+      }
+      page0 = next0;
+      page1 = next1;
     }
-    here = next;
-  }
-  if (!careful) {
+    if (careful) break;
     bool bad = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -338,20 +379,21 @@ again:
       for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
         for (int r = 0; r < 4; ++r) bad |= !__builtin_isfinite(o[nt][dt][r]);
-    careful = __builtin_amdgcn_ballot_w64(bad) != 0;
-    if (careful) goto again;
+    if (__builtin_amdgcn_ballot_w64(bad) == 0) break;
+    careful = true;
   }
 
   // join the waves: one row tile and DC columns at a time
   const float vs = p.v_scale ? p.v_scale[kvh] : 1.0f;
+  const int hq = p.kv_heads * p.group;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     float lsum = l[nt];
     lsum += __shfl_xor(lsum, 16);
     lsum += __shfl_xor(lsum, 32);
     if (g == 0) {
-      stat_m[wave][n16] = m[nt];
-      stat_l[wave][n16] = lsum;
+      stat_m[group][wave][n16] = m[nt];
+      stat_l[group][wave][n16] = lsum;
     }
 #pragma unroll
     for (int c0 = 0; c0 < D; c0 += DC) {
@@ -360,42 +402,45 @@ again:
         if constexpr (F8) {
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            sums[wave][n16][out_col<F8>(dt, 4 * g + r) - c0] = o[nt][dt][r];
+            sums[group][wave][n16][out_col<F8>(dt, 4 * g + r) - c0] = o[nt][dt][r];
         } else {
-          *reinterpret_cast<f32x4*>(&sums[wave][n16][16 * dt + 4 * g - c0]) = o[nt][dt];
+          *reinterpret_cast<f32x4*>(&sums[group][wave][n16][16 * dt + 4 * g - c0]) = o[nt][dt];
         }
       }
       __syncthreads();
-      constexpr int PER = 16 * DC / kThreads;  // columns a thread: 4 or 8
-      const int r = threadIdx.x / 16, col = (threadIdx.x % 16) * PER;
-      const int row = (rt * NT + nt) * 16 + r;
+      constexpr int PER = DC / 16;  // columns a thread: 4 or 8
+      const int in = threadIdx.x % (kWaves * kWave);
+      const int r = in / 16, col = (in % 16) * PER;
+      const int row = row0 + nt * 16 + r;
       if (row < rows) {
-        float top = kNegInf, sum = 0.0f, weight[kWaves], y[PER];
+        float top = kNegInf, sum = 0.0f, weight[kWaves];
+        typedef float FP __attribute__((ext_vector_type(PER)));
+        FP y = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) top = fmaxf(top, stat_m[w][r]);
+        for (int w = 0; w < kWaves; ++w) top = fmaxf(top, stat_m[group][w][r]);
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-          weight[w] = exp2_fast(stat_m[w][r] - (top == kNegInf ? 0.0f : top));
-          sum += weight[w] * stat_l[w][r];
+          weight[w] = rescale(stat_m[group][w][r] - (top == kNegInf ? 0.0f : top));
+          sum += weight[w] * stat_l[group][w][r];
         }
 #pragma unroll
-        for (int c = 0; c < PER; ++c) {
-          y[c] = 0.0f;
+        for (int w = 0; w < kWaves; ++w)
 #pragma unroll
-          for (int w = 0; w < kWaves; ++w) y[c] += weight[w] * sums[w][r][col + c];
-        }
+          for (int c = 0; c < PER; ++c) y[c] += weight[w] * sums[group][w][r][col + c];
         const long long token = (long long)seq * p.T + row / p.group;
         const long long at = token * hq + kvh * p.group + row % p.group;
         if (direct) {
-          typename A::T* out = reinterpret_cast<typename A::T*>(p.out) + at * D + c0 + col;
+          typedef typename A::T TP __attribute__((ext_vector_type(PER)));
 #pragma unroll
-          for (int c = 0; c < PER; ++c)
-            out[c] = (typename A::T)(sum == 0.0f ? 0.0f : y[c] / sum * vs);
+          for (int c = 0; c < PER; ++c) y[c] = sum == 0.0f ? 0.0f : y[c] / sum * vs;
+          *reinterpret_cast<TP*>(p.out + 2 * (at * D + c0 + col)) = __builtin_convertvector(y, TP);
         } else {
           const long long part = at * p.splits + split;
 #pragma unroll
-          for (int c = 0; c < PER; ++c) p.partial[part * D + c0 + col + c] = y[c];
-          if (c0 == 0 && threadIdx.x % 16 == 0) p.stats[part] = make_float2(top, sum);
+          for (int c = 0; c < PER; c += 4)
+            *reinterpret_cast<f32x4*>(p.partial + part * D + c0 + col + c) =
+                f32x4{y[c], y[c + 1], y[c + 2], y[c + 3]};
+          if (c0 == 0 && in % 16 == 0) p.stats[part] = make_float2(top, sum);
         }
       }
       __syncthreads();
@@ -406,7 +451,7 @@ again:
 
 // Joins the splits of one (token, query head) row.
 template <typename A, int D>
-__global__ __launch_bounds__(kThreads) void k_attn_decode_join(DecodeParams p) {
+__global__ __launch_bounds__(kJoinThreads) void k_attn_decode_join(DecodeParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   const int hq = p.kv_heads * p.group;
   const long long at = blockIdx.x;
@@ -418,33 +463,42 @@ __global__ __launch_bounds__(kThreads) void k_attn_decode_join(DecodeParams p) {
 #endif
 }
 
-// Row tiles (of 16 rows) that one workgroup takes: as many as the window has, while their
-// accumulators fit beside the tile's keys and values.
-int tiles_per_group(int rows, int D) {
-  const int most = D == 256 ? 2 : 4;
-  int nt = 1;
-  while (nt < most && 16 * nt < rows) nt *= 2;
-  return nt;
+// Row tiles a wave takes and row groups of a workgroup for a window of `rows` rows.
+struct Shape {
+  int tiles, groups;
+};
+Shape window_shape(int rows, int D) {
+  const int most = D == 64 ? kMostTiles<64> : D == 128 ? kMostTiles<128> : kMostTiles<256>;
+  Shape s{1, 1};
+  while (s.tiles < most && 16 * s.tiles < rows) s.tiles *= 2;
+  if (16 * s.tiles < rows && D == 128) s.groups = 2;
+  return s;
 }
 
-template <typename A, int D, bool F8, int NT>
+template <typename A, int D, bool F8, int NT, int RG>
 hipError_t launch_one(const DecodeParams& p, int n_seqs, hipStream_t stream) {
-  k_attn_decode<A, D, F8, NT><<<dim3(p.splits, p.kv_heads * p.row_tiles, n_seqs),
-                                dim3(kThreads), 0, stream>>>(p);
+  k_attn_decode<A, D, F8, NT, RG><<<dim3(p.splits, p.kv_heads * p.row_tiles, n_seqs),
+                                    dim3(kWaves * RG * kWave), 0, stream>>>(p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  k_attn_decode_join<A, D><<<dim3((unsigned)(n_seqs * p.T * p.kv_heads * p.group)),
-                             dim3(kThreads), 0, stream>>>(p);
+  k_attn_decode_join<A, D><<<dim3((unsigned)(n_seqs * p.T * p.kv_heads * p.group),
+                                  D / kJoinCols), dim3(kJoinThreads), 0, stream>>>(p);
   return hipGetLastError();
 }
 
 template <typename A, int D, bool F8>
 hipError_t launch_tiles(const DecodeParams& p, int n_seqs, hipStream_t stream) {
-  const int nt = tiles_per_group(p.T * p.group, D);
-  if (nt == 1) return launch_one<A, D, F8, 1>(p, n_seqs, stream);
-  if (nt == 2) return launch_one<A, D, F8, 2>(p, n_seqs, stream);
-  if constexpr (D != 256) return launch_one<A, D, F8, 4>(p, n_seqs, stream);
-  return hipErrorInvalidValue;
+  const Shape s = window_shape(p.T * p.group, D);
+  if constexpr (kMostGroups<D> == 2) {
+    if (s.groups == 2) return launch_one<A, D, F8, kMostTiles<D>, 2>(p, n_seqs, stream);
+  }
+  if constexpr (kMostTiles<D> >= 4) {
+    if (s.tiles == 4) return launch_one<A, D, F8, 4, 1>(p, n_seqs, stream);
+  }
+  if constexpr (kMostTiles<D> >= 2) {
+    if (s.tiles == 2) return launch_one<A, D, F8, 2, 1>(p, n_seqs, stream);
+  }
+  return launch_one<A, D, F8, 1, 1>(p, n_seqs, stream);
 }
 
 template <typename A>
@@ -465,7 +519,8 @@ AttnPlan decode_plan(int q_heads, int kv_heads, int D, int n_seqs, int window_to
                      int max_pages, int page_size, const moe_attn& a, int num_cus) {
   AttnPlan plan{};
   const int rows = window_tokens * (q_heads / kv_heads);
-  plan.tile_rows = 16 * tiles_per_group(rows, D);
+  const Shape shape = window_shape(rows, D);
+  plan.tile_rows = 16 * shape.tiles * shape.groups;
   plan.row_tiles = (rows + plan.tile_rows - 1) / plan.tile_rows;
   // tiles of the longest possible sequence (of its visible part)
   long long tiles = ((long long)max_pages * page_size + kTile - 1) / kTile;
@@ -473,7 +528,9 @@ AttnPlan decode_plan(int q_heads, int kv_heads, int D, int n_seqs, int window_to
     tiles = std::min(tiles, ((long long)a.window + window_tokens) / kTile + 2 +
                                 ((long long)a.sinks + kTile - 1) / kTile);
   const long long base = (long long)n_seqs * kv_heads * plan.row_tiles;
-  const long long fill = (2 * num_cus + base - 1) / base;
+  // workgroups that run at once: two a CU, one where a wave takes more than 256 registers
+  const long long at_once = (D == 256 && shape.tiles == 2 ? 1 : 2) * num_cus;
+  const long long fill = (at_once + base - 1) / base;
   const long long even = (tiles + 63) / 64;  // 2048 keys, so that long sequences share out
   const long long most = std::max(1ll, tiles / kMinSplitTiles);
   plan.splits = (int)std::min<long long>({std::max(fill, even), most, kMaxSplits});

@@ -31,7 +31,7 @@ struct Bf16 {
   typedef bf16x8 V8;
   typedef bf16x4 V4;
   typedef bf16x2 V2;
-  static constexpr uint32_t kExpMask = 0x7f80u;
+  static constexpr uint32_t kExpMask = 0x7f80u, kOne = 0x3f80u;
 #if defined(__HIP_DEVICE_COMPILE__)
   static __device__ __forceinline__ f32x4 mfma16(V8 a, V8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -51,7 +51,7 @@ struct F16 {
   typedef f16x8 V8;
   typedef f16x4 V4;
   typedef f16x2 V2;
-  static constexpr uint32_t kExpMask = 0x7c00u;
+  static constexpr uint32_t kExpMask = 0x7c00u, kOne = 0x3c00u;
 #if defined(__HIP_DEVICE_COMPILE__)
   static __device__ __forceinline__ f32x4 mfma16(V8 a, V8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -97,7 +97,11 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b) {
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// Replaces the non-finite 16-bit elements of v by zero; returns whether there were any.
+// Non-finite values behind a mask. A masked probability is 0, and 0 times NaN or infinity
+// is NaN, so the products of a tile that not all rows see leave such values out
+// (clear_nonfinite), and what they do to the rows that see them is added from counts:
+// non_finite<kind> marks a kind's values by ones, their product with the mask counts them
+// per row and column, and spread() turns a count into the value itself.
 template <typename A>
 __device__ __forceinline__ bool clear_nonfinite(typename A::V8& v) {
   u32x4 w = bits_as<u32x4>(v);
@@ -112,6 +116,93 @@ __device__ __forceinline__ bool clear_nonfinite(typename A::V8& v) {
   v = bits_as<typename A::V8>(w);
   return any;
 }
+
+// The same for e4m3 codes (NaN is their only non-finite value).
+__device__ __forceinline__ bool clear_nan_codes(u32x4& w) {
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const bool is = (w[i] >> (8 * b) & 0x7fu) == 0x7fu;
+      w[i] &= is ? ~(0xffu << (8 * b)) : 0xffffffffu;
+      any |= is;
+    }
+  return any;
+}
+
+template <typename A, bool F8>
+__device__ __forceinline__ bool clear_word(u32x4& w) {
+  if constexpr (F8) return clear_nan_codes(w);
+  typename A::V8 v = bits_as<typename A::V8>(w);
+  const bool any = clear_nonfinite<A>(v);
+  w = bits_as<u32x4>(v);
+  return any;
+}
+
+// One kind of non-finite value. The fields are opaque to the compiler (made in registers it
+// cannot see through), so that it keeps one small loop over the kinds instead of three
+// copies of its body.
+struct NonFinite {
+  uint32_t pattern;  // bits of the infinity
+  uint32_t nan;      // all ones for the NaN kind
+  float value;
+};
+template <typename A>
+__device__ __forceinline__ NonFinite non_finite_kind(int kind) {  // 0, 1: +-infinity, 2: NaN
+  NonFinite k{A::kExpMask | (kind == 1 ? 0x8000u : 0u), kind == 2 ? 0xffffffffu : 0u,
+              kind == 0 ? -kNegInf : kind == 1 ? kNegInf : __builtin_nanf("")};
+  asm volatile("" : "+v"(k.pattern), "+v"(k.nan), "+v"(k.value));
+  return k;
+}
+
+template <typename A>
+__device__ __forceinline__ typename A::V8 non_finite(const typename A::V8& v, const NonFinite& k) {
+  const u32x4 w = bits_as<u32x4>(v);
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r[i] = 0;
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+      const uint32_t x = (w[i] >> (16 * part)) & 0xffffu;
+      // the sign bit of a difference: above the infinity's exponent, or equal to the pattern
+      const uint32_t is =
+          ((k.nan & (A::kExpMask - (x & 0x7fffu))) | (~k.nan & ((x ^ k.pattern) - 1u))) >> 31;
+      r[i] |= is * (A::kOne << (16 * part));
+    }
+  }
+  return bits_as<typename A::V8>(r);
+}
+
+__device__ __forceinline__ float spread(float count, const NonFinite& k) {
+  return count > 0.0f ? k.value : 0.0f;
+}
+
+// 8 flags (bit j) as ones and zeros.
+template <typename A>
+__device__ __forceinline__ typename A::V8 mask_elements(uint32_t bits) {
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    r[i] = ((bits >> (2 * i)) & 1 ? A::kOne : 0u) | ((bits >> (2 * i + 1)) & 1 ? A::kOne << 16 : 0u);
+  return bits_as<typename A::V8>(r);
+}
+
+// The sign of the score scale goes into the queries, and a zero scale into them as a whole:
+// the scale itself is then positive, so that masked scores stay -inf under it and maxima
+// commute with it.
+struct ScaleSplit {
+  float scale;
+  uint32_t flip, keep;  // query words: (w ^ flip) & keep
+};
+__device__ __forceinline__ ScaleSplit split_scale(float scale) {
+  return {scale == 0.0f ? 1.0f : __builtin_fabsf(scale), scale < 0.0f ? 0x80008000u : 0u,
+          scale == 0.0f ? 0u : 0xffffffffu};
+}
+
+// 2^x for rescaling sums: never 0, so that an infinite sum stays infinite.
+__device__ __forceinline__ float rescale(float x) { return fmaxf(exp2_fast(x), 1e-38f); }
 #endif
 
 // ------------------------------------------------------------------ kernel arguments
@@ -202,14 +293,16 @@ __device__ __forceinline__ TileList visible_tiles(const KeyMask& m, int first, i
 
 constexpr int kJoinThreads = 256;
 constexpr int kMaxSplits = kJoinThreads;  // one statistic a thread
+constexpr int kJoinCols = 64;              // columns a workgroup joins
 
 #if defined(__HIP_DEVICE_COMPILE__)
-// One output row from its `live` splits, by a workgroup of kJoinThreads: each split's sums
-// are relative to its own maximum. row = token * q heads + q head.
+// kJoinCols columns (from blockIdx.y on) of one output row from its `live` splits, by a
+// workgroup of kJoinThreads: each split's sums are relative to its own maximum.
+// row = token * q heads + q head.
 template <typename A, int D>
 __device__ __forceinline__ void join_row(const float* partial, const float2* stats, long long row,
                                          int splits, int live, float v_scale, char* out) {
-  constexpr int LANES = D / 4, GROUPS = kJoinThreads / LANES, WAVES = kJoinThreads / kWave;
+  constexpr int LANES = kJoinCols / 4, GROUPS = kJoinThreads / LANES, WAVES = kJoinThreads / kWave;
   __shared__ float weight[kMaxSplits];
   __shared__ float red[2][WAVES];
   __shared__ f32x4 part[GROUPS][LANES];
@@ -223,7 +316,7 @@ __device__ __forceinline__ void join_row(const float* partial, const float2* sta
   __syncthreads();
 #pragma unroll
   for (int s = 0; s < WAVES; ++s) top = fmaxf(top, red[0][s]);
-  const float w = exp2_fast(st.x - (top == kNegInf ? 0.0f : top));
+  const float w = rescale(st.x - (top == kNegInf ? 0.0f : top));
   if (tid < live) weight[tid] = w;
   float sum = w * st.y;
 #pragma unroll
@@ -234,10 +327,11 @@ __device__ __forceinline__ void join_row(const float* partial, const float2* sta
 #pragma unroll
   for (int s = 1; s < WAVES; ++s) sum += red[1][s];
   const int lane = tid % LANES, grp = tid / LANES;
-  const f32x4* src = reinterpret_cast<const f32x4*>(partial + row * splits * D) + lane;
+  const int col = blockIdx.y * kJoinCols + 4 * lane;
+  const float* src = partial + row * splits * D + col;
   f32x4 y = {0, 0, 0, 0};
 #pragma unroll 4
-  for (int s = grp; s < live; s += GROUPS) y += weight[s] * src[(long long)s * LANES];
+  for (int s = grp; s < live; s += GROUPS) y += weight[s] * *reinterpret_cast<const f32x4*>(src + (long long)s * D);
   part[grp][lane] = y;
   __syncthreads();
   if (grp == 0) {
@@ -247,7 +341,7 @@ __device__ __forceinline__ void join_row(const float* partial, const float2* sta
 #pragma unroll
     for (int c = 0; c < 4; ++c) y[c] = sum == 0.0f ? 0.0f : y[c] / sum * v_scale;
     w2 = bits_as<u32x2>(__builtin_convertvector(y, typename A::V4));
-    *reinterpret_cast<u32x2*>(out + 2 * (row * D + 4 * lane)) = w2;
+    *reinterpret_cast<u32x2*>(out + 2 * (row * D + col)) = w2;
   }
 }
 #endif

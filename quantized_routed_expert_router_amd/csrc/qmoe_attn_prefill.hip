@@ -14,6 +14,8 @@
 // the second product's B operand: probabilities never leave the lane. Statistics and sums
 // are fp32; probabilities are rounded to the 16-bit type for the matrix cores (their
 // relative error, 2^-9 in bf16, is that of the output's own rounding).
+#include <type_traits>
+
 #include "qmoe_attn_internal.h"
 
 namespace qmoe {
@@ -126,6 +128,13 @@ struct Stage {
       v[i] = *reinterpret_cast<const u32x4*>(p.cv + vr * (D * (F8 ? 1 : 2)) + 16 * (c % BLOCK));
     }
   }
+  // Leaves the non-finite values of the tile out; whether there were any.
+  __device__ __forceinline__ bool clear_values() {
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i) any |= clear_word<A, F8>(v[i]);
+    return any;
+  }
   __device__ __forceinline__ void store(u32x4* lk, u32x4* lv, int tid) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -166,6 +175,7 @@ __global__ __launch_bounds__(64 * NW) void k_attn_prefill(PrefillParams p) {
   constexpr int KT = kTileElems / D, BM = 32 * NW, THREADS = 64 * NW;
   constexpr int KS = D / 16, DT = D / 32, HALVES = KT / 32;
   __shared__ u32x4 lk[2][KT * D / 8], lv[2][KT * D / 8];
+  __shared__ int dirty[2][NW];  // an edge tile had non-finite values in a wave's part
 
   // Workgroups go to the 8 XCDs in turn: with the kv head in the low digits, an XCD's
   // workgroups share few heads' keys in its L2. Later row tiles see more keys: they start
@@ -207,14 +217,15 @@ __global__ __launch_bounds__(64 * NW) void k_attn_prefill(PrefillParams p) {
   const bool any = wrow < t.rows;
   const int pos_min = t.first_pos + wrow / p.group;
   const int pos_max = t.first_pos + (min(wrow + 32, t.rows) - 1) / p.group;
+  const int first_key = t.first_pos + t.row0 / p.group;  // positions of the workgroup's rows
   const int last_key = t.first_pos + (min(t.row0 + BM, t.rows) - 1) / p.group;
+  auto visible = [&](int key, bool bad_tile) {
+    bool ok = key_visible(p.mask, key, pos);
+    if (bad_tile && ok) ok = (unsigned)table[key >> p.page_shift] < (unsigned)p.num_pages;
+    return ok;
+  };
 
-  // scale >= 0 below, so that the maximum commutes with it: its sign goes into q, and a
-  // zero scale into q as a whole
-  float scale = p.scale * (p.k_scale ? p.k_scale[kvh] : 1.0f);
-  const uint32_t flip = scale < 0.0f ? 0x80008000u : 0u;
-  const uint32_t keep = scale == 0.0f || !real ? 0u : 0xffffffffu;
-  scale = scale == 0.0f ? 1.0f : __builtin_fabsf(scale);
+  const ScaleSplit sc = split_scale(p.scale * (p.k_scale ? p.k_scale[kvh] : 1.0f));
   V8 q[KS];
   {
     const char* src = p.q.data + 2 * ((long long)token * p.q.token_stride +
@@ -223,7 +234,7 @@ __global__ __launch_bounds__(64 * NW) void k_attn_prefill(PrefillParams p) {
     for (int ks = 0; ks < KS; ++ks) {
       u32x4 w = *reinterpret_cast<const u32x4*>(src + 2 * (16 * ks + 8 * h));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = (w[i] ^ flip) & keep;
+      for (int i = 0; i < 4; ++i) w[i] = real ? (w[i] ^ sc.flip) & sc.keep : 0u;
       q[ks] = bits_as<V8>(w);
     }
   }
@@ -236,16 +247,32 @@ __global__ __launch_bounds__(64 * NW) void k_attn_prefill(PrefillParams p) {
   float m = kNegInf, l = 0.0f;  // scaled reference maximum; this lane's part of the sum
 
   Stage<A, D, F8, KT, THREADS> st;
-  bool bad = false, bad_next = false;
+  // Of the tile in LDS and the next: a page of it lies outside the cache; it is an edge tile,
+  // which not all of the workgroup's rows see.
+  bool bad = false, bad_next = false, edge = false, edge_next = false;
+  auto is_edge = [&](bool bad_tile, int key0) {
+    return bad_tile || key0 + KT - 1 > first_key ||
+           (p.mask.window != 0 && key0 <= last_key - p.mask.window &&
+            key0 + KT - 1 >= p.mask.sinks);
+  };
+  auto stage_store = [&](int buf, bool edge_tile) {
+    if (edge_tile) {
+      const bool any = __builtin_amdgcn_ballot_w64(st.clear_values()) != 0;
+      if (lane == 0) dirty[buf][wave] = any;
+    }
+    st.store(lk[buf], lv[buf], tid);
+  };
   if (i0 < i1) {
     const int key0 = t.keys.tile(i0) * KT;
     st.ids(p, table, key0, tid);
     st.load(p, kvh, key0, tid);
     bad = bad_page<KT>(p, table, key0, last_key);
+    edge = is_edge(bad, key0);
     if (i0 + 1 < i1) st.ids(p, table, t.keys.tile(i0 + 1) * KT, tid);
-    st.store(lk[0], lv[0], tid);
+    stage_store(0, edge);
   }
   __syncthreads();
+#pragma unroll 1
   for (int i = i0; i < i1; ++i) {
     const int buf = (i - i0) & 1;
     const int key0 = t.keys.tile(i) * KT;
@@ -254,15 +281,13 @@ __global__ __launch_bounds__(64 * NW) void k_attn_prefill(PrefillParams p) {
       const int k1 = t.keys.tile(i + 1) * KT;
       st.load(p, kvh, k1, tid);
       bad_next = bad_page<KT>(p, table, k1, last_key);
+      edge_next = is_edge(bad_next, k1);
       if (i + 2 < i1) st.ids(p, table, t.keys.tile(i + 2) * KT, tid);
     }
     const bool sees = any && key0 <= pos_max &&
                       (p.mask.window == 0 || key0 + KT - 1 > pos_min - p.mask.window ||
                        key0 < p.mask.sinks);
     if (sees) {
-      const bool full = !bad && key0 + KT - 1 <= pos_min &&
-                        (p.mask.window == 0 || key0 > pos_max - p.mask.window ||
-                         key0 + KT - 1 < p.mask.sinks);
       f32x16 s[HALVES];
       const int krow = (n32 & 19) | ((n32 & 4) << 1) | ((n32 & 8) >> 1);
 #pragma unroll
@@ -277,27 +302,24 @@ __global__ __launch_bounds__(64 * NW) void k_attn_prefill(PrefillParams p) {
         }
       }
       // accumulator r of half x is key 32 x + 16 (r / 8) + 8 h + r % 8
-      if (!full) {
+      if (edge && (bad || key0 + KT - 1 > pos_min ||
+                   (p.mask.window != 0 && key0 <= pos_max - p.mask.window))) {
 #pragma unroll
         for (int x = 0; x < HALVES; ++x)
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int key = key0 + 32 * x + 16 * (r >> 3) + 8 * h + (r & 7);
-            bool ok = key_visible(p.mask, key, pos);
-            if (bad && ok) ok = (unsigned)table[key >> p.page_shift] < (unsigned)p.num_pages;
-            s[x][r] = ok ? s[x][r] : kNegInf;
-          }
+          for (int r = 0; r < 16; ++r)
+            if (!visible(key0 + 32 * x + 16 * (r >> 3) + 8 * h + (r & 7), bad)) s[x][r] = kNegInf;
       }
       float top = kNegInf;
 #pragma unroll
       for (int x = 0; x < HALVES; ++x)
 #pragma unroll
         for (int r = 0; r < 16; ++r) top = fmaxf(top, s[x][r]);
-      top = fmaxf(top, __shfl_xor(top, 32)) * scale;
+      top = fmaxf(top, __shfl_xor(top, 32)) * sc.scale;
       const bool moves = top > m + kLazy;
       if (__builtin_amdgcn_ballot_w64(moves) != 0) {
         const float now = moves ? top : m;
-        const float a = exp2_fast(m - (now == kNegInf ? 0.0f : now));
+        const float a = rescale(m - (now == kNegInf ? 0.0f : now));
         l *= a;
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt) o[dt] *= a;
@@ -309,7 +331,7 @@ __global__ __launch_bounds__(64 * NW) void k_attn_prefill(PrefillParams p) {
       for (int x = 0; x < HALVES; ++x) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          s[x][r] = exp2_fast(__builtin_fmaf(s[x][r], scale, base));
+          s[x][r] = exp2_fast(__builtin_fmaf(s[x][r], sc.scale, base));
           l += s[x][r];
         }
 #pragma unroll
@@ -320,45 +342,49 @@ __global__ __launch_bounds__(64 * NW) void k_attn_prefill(PrefillParams p) {
           pr[2 * x + u] = __builtin_convertvector(y, V8);
         }
       }
-      bool dirty = false;  // a masked tile with non-finite values somewhere
 #pragma unroll
       for (int ks = 0; ks < 2 * HALVES; ++ks)
 #pragma unroll
-        for (int dt = 0; dt < DT; ++dt) {
-          V8 a = bits_as<V8>(lv[buf][(2 * ks + h) * D + 32 * dt + n32]);
-          if (!full) dirty |= clear_nonfinite<A>(a);
-          o[dt] = A::mfma32(a, pr[ks], o[dt]);
-        }
-      if (!full && __builtin_amdgcn_ballot_w64(dirty) != 0) {
-        // A zero probability times a non-finite value is NaN, so such values of a tile that
-        // not all rows see were left out above; here they reach the rows that see them.
+        for (int dt = 0; dt < DT; ++dt)
+          o[dt] = A::mfma32(bits_as<V8>(lv[buf][(2 * ks + h) * D + 32 * dt + n32]), pr[ks], o[dt]);
+      if (edge) {
+        int found = 0;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) found |= dirty[buf][w];
+        if (found != 0) {
+          // the values as the cache has them: what they do to the rows that see them
 #pragma unroll 1
-        for (int key = 0; key < KT; ++key) {
-          bool ok = key_visible(p.mask, key0 + key, pos);
-          if (bad && ok)
-            ok = (unsigned)table[(key0 + key) >> p.page_shift] < (unsigned)p.num_pages;
-          if (__builtin_amdgcn_ballot_w64(ok) == 0) continue;
-          float w = 0.0f;
+          for (int i3 = 0; i3 < 3 * 2 * HALVES; ++i3) {
+            const NonFinite kind = non_finite_kind<A>(i3 % 3);
+            const int from = key0 + 16 * (i3 / 3) + 8 * h;
+            uint32_t seen = 0;
 #pragma unroll
-          for (int x = 0; x < HALVES; ++x)
+            for (int j = 0; j < 8; ++j) seen |= (uint32_t)visible(from + j, bad) << j;
+            const V8 rows_seen = mask_elements<A>(seen);
+            const long long at = st.row_of(p, st.page_of(p, table, from), kvh, from) * D + 8 * n32;
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-              w = (key & ~8) == 32 * x + 16 * (r >> 3) + (r & 7) ? s[x][r] : w;
-          w = __shfl(w, ((key & 8) << 2) | n32);
-          const typename A::T* col =
-              reinterpret_cast<const typename A::T*>(&lv[buf][(key >> 3) * D]) + (key & 7);
+            for (int dt = 0; dt < DT; ++dt) {
+              V8 a;
+              if constexpr (F8) {
+                const u32x2 w = *reinterpret_cast<const u32x2*>(p.cv + at + 256 * dt);
+                a = expand_e4m3<A>(w[0], w[1]);
+              } else {
+                a = *reinterpret_cast<const V8*>(p.cv + 2 * (at + 256 * dt));
+              }
+              f32x16 c;
 #pragma unroll
-          for (int dt = 0; dt < DT; ++dt)
+              for (int r = 0; r < 16; ++r) c[r] = 0.0f;
+              c = A::mfma32(non_finite<A>(a, kind), rows_seen, c);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-              const float x = (float)col[8 * (32 * dt + 8 * (r >> 2) + 4 * h + (r & 3))];
-              if (ok && !__builtin_isfinite(x)) o[dt][r] += w * x;
+              for (int r = 0; r < 16; ++r) o[dt][r] += spread(c[r], kind);
             }
+          }
         }
       }
     }
-    if (more) st.store(lk[buf ^ 1], lv[buf ^ 1], tid);
+    if (more) stage_store(buf ^ 1, edge_next);
     bad = bad_next;
+    edge = edge_next;
     __syncthreads();
   }
 
@@ -435,7 +461,7 @@ hipError_t launch_one(const PrefillParams& p, hipStream_t stream) {
                                  dim3(64 * NW), 0, stream>>>(p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  k_attn_prefill_join<A, D, NW><<<dim3((unsigned)(p.n * p.kv_heads * p.group)),
+  k_attn_prefill_join<A, D, NW><<<dim3((unsigned)(p.n * p.kv_heads * p.group), D / kJoinCols),
                                   dim3(kJoinThreads), 0, stream>>>(p);
   return hipGetLastError();
 }
