@@ -298,7 +298,7 @@ moe_status moe_expert_ffn_prefill_stages(const moe_layer* L, const uint16_t* x_b
 #define MOE_MAX_HEADS 512        /* heads of one row set                                */
 
 /* Heads of n tokens: element (t, h, c) at data[t * token_stride + h * head_stride + c],
- * strides in elements. data 16-byte aligned, strides multiples of 8 and not negative, so
+ * strides in elements. data 16-byte aligned, strides multiples of 8 in 0..2^31-1, so
  * the query part of a fused projection output [n][(Hq + 2 Hkv) * D] is a moe_heads. */
 typedef struct {
   void* data; /* device; data == NULL: no such heads (where the call allows it)        */

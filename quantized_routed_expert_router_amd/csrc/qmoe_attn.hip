@@ -27,11 +27,11 @@ size_t span_bytes(const moe_heads& h, int n, int D) {
 
 Range range(const moe_heads& h, int n, int D) { return range(h.data, span_bytes(h, n, D)); }
 
-// Strides are below 2^40 elements, so that no span of an accepted call wraps around.
+// Strides are below 2^31 elements: the kernels multiply them as 32-bit numbers.
 moe_status check_heads(const moe_heads& h) {
   if (h.heads < 1 || h.heads > MOE_MAX_HEADS) return MOE_ERR_INVALID_ARGUMENT;
   if (!aligned(h.data, 16)) return MOE_ERR_INVALID_ARGUMENT;
-  const int64_t most = (int64_t)1 << 40;
+  const int64_t most = kMaxLayoutInt;
   if (h.token_stride < 0 || h.head_stride < 0 || h.token_stride > most || h.head_stride > most)
     return MOE_ERR_INVALID_ARGUMENT;
   if (h.token_stride % 8 || h.head_stride % 8) return MOE_ERR_INVALID_ARGUMENT;

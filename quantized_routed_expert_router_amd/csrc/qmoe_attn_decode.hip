@@ -19,11 +19,11 @@
 namespace qmoe {
 namespace {
 
-constexpr int kWaves = 4;           // waves that share a row group's keys
 constexpr int kTile = 32;           // keys of one step of a wave
 // A row's reference maximum moves only when the new maximum exceeds it by this many powers
 // of two; probabilities then reach 2^8, which fp32 sums and both 16-bit types hold.
 constexpr float kLazy = 8.0f;
+constexpr int kUnsplitTiles = 32;
 constexpr int kMinSplitTiles = 8;   // 256 keys: below that a split costs more than it saves
 
 struct DecodeParams {
@@ -161,7 +161,6 @@ template <int D>
 constexpr int kMostTiles = D == 64 ? 4 : 2;
 template <int D>
 constexpr int kMostGroups = D == 128 ? 2 : 1;
-
 // Waves a SIMD that the registers have to allow. Two rather than one where they fit: with
 // more than 256 registers a wave the accumulators would go to the accumulation registers.
 template <int D, int NT>
@@ -172,11 +171,12 @@ constexpr int kMinWaves = D == 256 ? 1 : 2;
 template <int D>
 constexpr bool kQueriesInLds = D == 256;
 
-template <typename A, int D, bool F8, int NT, int RG>
-__global__ __launch_bounds__(kWaves * RG * kWave, (kMinWaves<D, NT>)) void k_attn_decode(DecodeParams p) {
+// KW: waves that share a row group's keys.
+template <typename A, int D, bool F8, int NT, int RG, int KW>
+__global__ __launch_bounds__(KW * RG * kWave, (kMinWaves<D, NT>)) void k_attn_decode(DecodeParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   typedef typename A::V8 V8;
-  constexpr int KS = D / 32, DT = D / 16;
+  constexpr int KS = D / 32, DT = D / 16, kWaves = KW;
   constexpr int DC = D < 128 ? D : 128;  // columns joined at a time
   __shared__ float sums[RG][kWaves][16][DC + 4];
   __shared__ float stat_m[RG][kWaves][16], stat_l[RG][kWaves][16];
@@ -408,9 +408,9 @@ __global__ __launch_bounds__(kWaves * RG * kWave, (kMinWaves<D, NT>)) void k_att
         }
       }
       __syncthreads();
-      constexpr int PER = DC / 16;  // columns a thread: 4 or 8
+      constexpr int PER = DC / (4 * kWaves);  // columns a thread: 4 or 8
       const int in = threadIdx.x % (kWaves * kWave);
-      const int r = in / 16, col = (in % 16) * PER;
+      const int r = in / (4 * kWaves), col = (in % (4 * kWaves)) * PER;
       const int row = row0 + nt * 16 + r;
       if (row < rows) {
         float top = kNegInf, sum = 0.0f, weight[kWaves];
@@ -436,11 +436,8 @@ __global__ __launch_bounds__(kWaves * RG * kWave, (kMinWaves<D, NT>)) void k_att
           *reinterpret_cast<TP*>(p.out + 2 * (at * D + c0 + col)) = __builtin_convertvector(y, TP);
         } else {
           const long long part = at * p.splits + split;
-#pragma unroll
-          for (int c = 0; c < PER; c += 4)
-            *reinterpret_cast<f32x4*>(p.partial + part * D + c0 + col + c) =
-                f32x4{y[c], y[c + 1], y[c + 2], y[c + 3]};
-          if (c0 == 0 && in % 16 == 0) p.stats[part] = make_float2(top, sum);
+          *reinterpret_cast<FP*>(p.partial + part * D + c0 + col) = y;
+          if (c0 == 0 && col == 0) p.stats[part] = make_float2(top, sum);
         }
       }
       __syncthreads();
@@ -475,10 +472,10 @@ Shape window_shape(int rows, int D) {
   return s;
 }
 
-template <typename A, int D, bool F8, int NT, int RG>
+template <typename A, int D, bool F8, int NT, int RG, int KW = 4>
 hipError_t launch_one(const DecodeParams& p, int n_seqs, hipStream_t stream) {
-  k_attn_decode<A, D, F8, NT, RG><<<dim3(p.splits, p.kv_heads * p.row_tiles, n_seqs),
-                                    dim3(kWaves * RG * kWave), 0, stream>>>(p);
+  k_attn_decode<A, D, F8, NT, RG, KW><<<dim3(p.splits, p.kv_heads * p.row_tiles, n_seqs),
+                                        dim3(KW * RG * kWave), 0, stream>>>(p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   k_attn_decode_join<A, D><<<dim3((unsigned)(n_seqs * p.T * p.kv_heads * p.group),
@@ -497,6 +494,13 @@ hipError_t launch_tiles(const DecodeParams& p, int n_seqs, hipStream_t stream) {
   }
   if constexpr (kMostTiles<D> >= 2) {
     if (s.tiles == 2) return launch_one<A, D, F8, 2, 1>(p, n_seqs, stream);
+  }
+  // A short context on few workgroups is a chain of latencies, which twice the waves halve
+  // (517 keys: 10.7 us against 8.3 and a joining launch of 3.9); on many, four waves run
+  // nearer to the memory's rate (64 sequences at 8 bits: 370 us, with eight 447).
+  if constexpr (D <= 128) {
+    if (p.splits == 1 && (long long)n_seqs * p.kv_heads * p.row_tiles <= device_cu_count())
+      return launch_one<A, D, F8, 1, 1, 8>(p, n_seqs, stream);
   }
   return launch_one<A, D, F8, 1, 1>(p, n_seqs, stream);
 }
@@ -532,7 +536,8 @@ AttnPlan decode_plan(int q_heads, int kv_heads, int D, int n_seqs, int window_to
   const long long at_once = (D == 256 && shape.tiles == 2 ? 1 : 2) * num_cus;
   const long long fill = (at_once + base - 1) / base;
   const long long even = (tiles + 63) / 64;  // 2048 keys, so that long sequences share out
-  const long long most = std::max(1ll, tiles / kMinSplitTiles);
+  // a few tiles are done sooner than a second launch
+  const long long most = tiles <= kUnsplitTiles ? 1 : std::max(1ll, tiles / kMinSplitTiles);
   plan.splits = (int)std::min<long long>({std::max(fill, even), most, kMaxSplits});
   if (plan.splits > 1) {
     const size_t parts = (size_t)n_seqs * window_tokens * q_heads * plan.splits;

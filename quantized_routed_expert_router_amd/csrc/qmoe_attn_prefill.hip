@@ -86,6 +86,29 @@ __device__ __forceinline__ RowTile row_tile(const PrefillParams& p, int seq, int
 
 #if defined(__HIP_DEVICE_COMPILE__)
 
+// The last sequence s for which at_or_before(s, q_starts[s]) holds (it does for a first part
+// of them), -1 if none: one load by the wave for up to 64 sequences, a binary search beyond.
+template <typename F>
+__device__ __forceinline__ int find_sequence(const PrefillParams& p, F at_or_before) {
+  if (p.n_seqs <= kWave) {
+    const int s = min((int)threadIdx.x % kWave, p.n_seqs - 1);
+    const uint64_t before = __builtin_amdgcn_ballot_w64(at_or_before(s, q_start(p, s)));
+    const uint64_t mine = p.n_seqs == kWave ? before : before & ((1ull << p.n_seqs) - 1);
+    return mine == 0 ? -1 : 63 - __builtin_clzll(mine);
+  }
+  int seq = -1;
+  for (int lo = 0, hi = p.n_seqs - 1; lo <= hi;) {
+    const int mid = (lo + hi) / 2;
+    if (at_or_before(mid, q_start(p, mid))) {
+      seq = mid;
+      lo = mid + 1;
+    } else {
+      hi = mid - 1;
+    }
+  }
+  return seq;
+}
+
 template <int D>
 __device__ __forceinline__ int key_swizzle(int row) {
   return D == 64 ? (row >> 1) & 7 : row & 15;
@@ -182,21 +205,13 @@ __global__ __launch_bounds__(64 * NW) void k_attn_prefill(PrefillParams p) {
   // first.
   const int kvh = blockIdx.x % p.kv_heads;
   const int slot = p.slots - 1 - blockIdx.x / p.kv_heads;
-  int seq = 0;
-  for (int lo = 0, hi = p.n_seqs - 1; lo <= hi;) {  // last sequence with first_slot <= slot
-    const int mid = (lo + hi) / 2;
-    if (first_slot<BM>(p, mid) <= slot) {
-      seq = mid;
-      lo = mid + 1;
-    } else {
-      hi = mid - 1;
-    }
-  }
+  const int seq = find_sequence(p, [&](int s, int start) {
+    return (int)((long long)start * p.group / BM) + s <= slot;
+  });
+  if (seq < 0) return;
   const int index = slot - first_slot<BM>(p, seq);
-  if (index < 0 || (long long)index * BM >= (long long)max(0, q_start(p, seq + 1) -
-                                                              q_start(p, seq)) * p.group)
-    return;
   const RowTile t = row_tile<BM, KT>(p, seq, index);
+  if ((long long)index * BM >= t.rows) return;
   const int split = blockIdx.y;
   const bool direct = t.live <= 1;
   if (split >= t.live && !(direct && split == 0)) return;
@@ -427,16 +442,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_attn_prefill_join(PrefillParam
   constexpr int KT = kTileElems / D, BM = 32 * NW;
   const int hq = p.kv_heads * p.group;
   const int token = blockIdx.x / hq, head = blockIdx.x % hq;
-  int seq = -1;
-  for (int lo = 0, hi = p.n_seqs - 1; lo <= hi;) {  // last sequence that starts at or before
-    const int mid = (lo + hi) / 2;
-    if (q_start(p, mid) <= token) {
-      seq = mid;
-      lo = mid + 1;
-    } else {
-      hi = mid - 1;
-    }
-  }
+  const int seq = find_sequence(p, [&](int, int start) { return start <= token; });
   if (seq < 0 || token >= q_start(p, seq + 1)) return;
   const int kvh = head / p.group;
   const int row = (token - q_start(p, seq)) * p.group + head % p.group;

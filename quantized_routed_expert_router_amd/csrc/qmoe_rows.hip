@@ -31,31 +31,44 @@ enum CacheKind { kNoCache = 0, kCache16 = 1, kCacheE4m3 = 2 };
 #if defined(__HIP_DEVICE_COMPILE__)
 
 template <typename A>
-__device__ __forceinline__ f32x8 widen(const u32x4& w) {
-  return __builtin_convertvector(bits_as<typename A::V8>(w), f32x8);
-}
-
-template <typename A>
 __device__ __forceinline__ float widen1(uint32_t half) {
   const uint16_t b = (uint16_t)half;
   return (float)bits_as<typename A::T>(b);
 }
 
+// sin and cos of r in [-pi/4, pi/4] by their Taylor sums to r^9 and r^10: the terms left out
+// are below 2^-28.
+__device__ __forceinline__ void sin_cos_octant(float r, float& s, float& c) {
+  const float z = r * r;
+  float ps = __builtin_fmaf(z, 1.0f / 362880.0f, -1.0f / 5040.0f);
+  ps = __builtin_fmaf(z, ps, 1.0f / 120.0f);
+  ps = __builtin_fmaf(z, ps, -1.0f / 6.0f);
+  s = __builtin_fmaf(r * z, ps, r);
+  float pc = __builtin_fmaf(z, -1.0f / 3628800.0f, 1.0f / 40320.0f);
+  pc = __builtin_fmaf(z, pc, -1.0f / 720.0f);
+  pc = __builtin_fmaf(z, pc, 1.0f / 24.0f);
+  pc = __builtin_fmaf(z, pc, -0.5f);
+  c = __builtin_fmaf(z, pc, 1.0f);
+}
+
 // cos and sin of the token's angles into the wave's part of LDS: angle i in entry i. The
-// product and the reduction to (-pi, pi) are in binary64 (positions far into a context
+// product and the reduction to a quarter turn are in binary64 (positions far into a context
 // leave no fraction bits in fp32), the functions of the reduced angle in fp32.
-__device__ __forceinline__ void token_angles(const RowsParams& p, int token, int lane, float* cs,
-                                             float* sn) {
-  const double pos = (double)p.positions[token];
+__device__ __forceinline__ void token_angles(const RowsParams& p, int position, int lane,
+                                             float* cs, float* sn) {
+  const double pos = (double)position;
   for (int i = lane; i < p.rot / 2; i += kWave) {
     const double a = pos * (double)p.inv_freq[i];
-    const double turns = __builtin_rint(a * 0.15915494309189533577);
-    double r = __builtin_fma(-turns, 6.28318530717958623200, a);
-    r = __builtin_fma(-turns, 2.44929359829470641435e-16, r);
+    const double quarters = __builtin_rint(a * 0.63661977236758134308);
+    double r = __builtin_fma(-quarters, 1.57079632679489655800, a);
+    r = __builtin_fma(-quarters, 6.12323399573676603587e-17, r);
     float s, c;
-    sincosf((float)r, &s, &c);
-    cs[i] = c;
-    sn[i] = s;
+    sin_cos_octant((float)r, s, c);
+    // quarters modulo 4, exact up to 2^53
+    const int n = (int)(quarters - 4.0 * __builtin_floor(quarters * 0.25));
+    const float x = n & 1 ? s : c, y = n & 1 ? c : s;
+    cs[i] = n == 1 || n == 2 ? -x : x;
+    sn[i] = n >= 2 ? -y : y;
   }
   // the wave's own writes, read back by the same wave
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -63,107 +76,162 @@ __device__ __forceinline__ void token_angles(const RowsParams& p, int token, int
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// Sum over the LPR (8, 16 or 32) neighbouring lanes of a row, in every one of them.
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float x) {
+  return x + bits_as<float>(
+                 __builtin_amdgcn_update_dpp(0, bits_as<int>(x), CTRL, 0xf, 0xf, true));
+}
+template <int LPR>
+__device__ __forceinline__ float row_sum(float x) {
+  x = add_dpp<0xb1>(x);                          // quad_perm 1 0 3 2
+  x = add_dpp<0x4e>(x);                          // quad_perm 2 3 0 1
+  x = add_dpp<0x141>(x);                         // row_half_mirror
+  if constexpr (LPR >= 16) x = add_dpp<0x140>(x);  // row_mirror
+  if constexpr (LPR >= 32) x += __shfl_xor(x, 16);
+  return x;
+}
+
+// 1 / sqrt(x): the hardware's (1 ulp), with small arguments scaled into its range.
+__device__ __forceinline__ float inv_sqrt(float x) {
+  const bool small = x < 0x1p-96f;
+  const float r = __builtin_amdgcn_rsqf(small ? x * 0x1p64f : x);
+  return small ? r * 0x1p32f : r;
+}
+
+struct Weights {
+  f32x4 lo, hi;
+};
+__device__ __forceinline__ f32x4 load4(const float* p) {  // 4-byte aligned
+  f32x4 v;
+  __builtin_memcpy(&v, p, sizeof v);
+  return v;
+}
+
 // One wave's share of a token's query and key rows: LPR = D/8 lanes hold one row, 8
-// elements a lane, 64/LPR rows at a time.
+// elements a lane, 64/LPR rows at a time, first the query heads, then the key heads. A
+// lane's 8 elements are 4 rotation pairs: 4 elements of the first half and their partners
+// in the second (interleaved, or beyond the rotation: 8 consecutive ones), so that the
+// rotation needs no other lane.
 template <typename A, int D, int CACHE>
 __device__ __forceinline__ void rows_wave(const RowsParams& p, int token, int part, int lane,
                                           float* cs, float* sn) {
+  typedef typename A::V4 V4;
   constexpr int LPR = D / 8, RPI = kWave / LPR;
   const int sub = lane / LPR, j = lane % LPR;
-  const int hq = p.q.heads, rows = hq + p.k.heads;
-  const int half = p.rot / 2;
-
-  if (p.rot > 0) token_angles(p, token, lane, cs, sn);
-  // this lane's 8 elements: which angles turn them, and which lane holds their partners
-  const bool turned = 8 * j < p.rot;
-  const bool second = !p.interleaved && 8 * j >= half;
-  const int first_angle = !turned ? 0 : p.interleaved ? 4 * j : 8 * j - (second ? half : 0);
-  const int hop = turned && !p.interleaved ? (second ? -half / 8 : half / 8) : 0;
-  f32x8 c8, s8;  // interleaved: entries 0..3
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const bool live = turned && (!p.interleaved || e < 4);
-    c8[e] = live ? cs[first_angle + e] : 1.0f;
-    s8[e] = live ? sn[first_angle + e] : 0.0f;
-  }
-  f32x8 wq, wk;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    wq[e] = p.q_norm ? p.q_norm[8 * j + e] + p.weight_offset : 1.0f;
-    wk[e] = p.k_norm ? p.k_norm[8 * j + e] + p.weight_offset : 1.0f;
-  }
-  int slot = 0;
-  bool stored = true;
-  if constexpr (CACHE != kNoCache) {
-    slot = p.slots[token];
-    stored = slot >= 0 && slot < p.num_slots;
-  }
-
+  const int qgroups = (p.q.heads + RPI - 1) / RPI;
   const int it0 = part * p.iters_per_part;
-  const int it1 = min(it0 + p.iters_per_part, (rows + RPI - 1) / RPI);
-  auto source = [&](int it) -> const u32x4* {
-    const int r = min(it * RPI + sub, rows - 1);
-    const HeadView& v = r < hq ? p.q : p.k;
-    const long long h = r < hq ? r : r - hq;
-    return reinterpret_cast<const u32x4*>(
-        v.data + 2 * ((long long)token * v.token_stride + h * v.head_stride + 8 * j));
-  };
+  const int it1 = min(it0 + p.iters_per_part, qgroups + (p.k.heads + RPI - 1) / RPI);
   if (it0 >= it1) return;
-  u32x4 next = *source(it0);
+  const bool turned = 8 * j < p.rot;
+  const bool halves = turned && !p.interleaved;
+  const int e0 = halves ? 4 * j : 8 * j, e1 = halves ? p.rot / 2 + 4 * j : 8 * j + 4;
+
+  struct Raw {
+    u32x2 lo, hi;
+  };
+  auto load = [&](int it) -> Raw {
+    const bool is_q = it < qgroups;
+    const HeadView& v = is_q ? p.q : p.k;
+    const uint32_t row = (uint32_t)min((is_q ? it : it - qgroups) * RPI + sub, v.heads - 1);
+    const char* at = v.data + 2 * ((uint64_t)(uint32_t)token * (uint32_t)v.token_stride +
+                                   (uint64_t)row * (uint32_t)v.head_stride);
+    return {*reinterpret_cast<const u32x2*>(at + 2 * e0),
+            *reinterpret_cast<const u32x2*>(at + 2 * e1)};
+  };
+  // everything that the first rows need is on its way before the angles are computed
+  Raw next = load(it0);
+  Raw after = load(min(it0 + 1, it1 - 1));
+  Weights wq{1.0f, 1.0f}, wk{1.0f, 1.0f};
+  if (p.q_norm) wq = {load4(p.q_norm + e0), load4(p.q_norm + e1)};
+  if (p.k_norm) wk = {load4(p.k_norm + e0), load4(p.k_norm + e1)};
+  int slot = 0;
+  if constexpr (CACHE != kNoCache) slot = p.slots[token];
+  f32x4 c4 = 1.0f, s4 = 0.0f;
+  if (p.rot > 0) {
+    token_angles(p, p.positions[token], lane, cs, sn);
+    if (turned) {
+      c4 = *reinterpret_cast<const f32x4*>(cs + 4 * j);
+      s4 = *reinterpret_cast<const f32x4*>(sn + 4 * j);
+    }
+  }
+  if (p.q_norm) wq = {wq.lo + p.weight_offset, wq.hi + p.weight_offset};
+  if (p.k_norm) wk = {wk.lo + p.weight_offset, wk.hi + p.weight_offset};
+  const bool stored = slot >= 0 && slot < p.num_slots;
+
   for (int it = it0; it < it1; ++it) {
-    const u32x4 raw = next;
-    if (it + 1 < it1) next = *source(it + 1);
-    const int r = it * RPI + sub;
-    const bool is_q = r < hq;
-    f32x8 y = widen<A>(raw);
-    const bool normed = is_q ? p.q_norm != nullptr : p.k_norm != nullptr;
-    float ss = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(y[e], y[e], ss);
-#pragma unroll
-    for (int m = 1; m < LPR; m *= 2) ss += __shfl_xor(ss, m);
-    const float inv = normed ? 1.0f / sqrtf(ss * (1.0f / D) + p.eps) : 1.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = y[e] * inv * (is_q ? wq[e] : wk[e]);
-    if (p.interleaved) {
+    const Raw raw = next;
+    next = after;
+    after = load(min(it + 2, it1 - 1));
+    const bool is_q = it < qgroups;
+    const HeadView& in = is_q ? p.q : p.k;
+    const int row = (is_q ? it : it - qgroups) * RPI + sub;
+    f32x4 lo = __builtin_convertvector(bits_as<V4>(raw.lo), f32x4);
+    f32x4 hi = __builtin_convertvector(bits_as<V4>(raw.hi), f32x4);
+    if (is_q ? p.q_norm != nullptr : p.k_norm != nullptr) {
+      float ss = 0.0f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float a = y[2 * e], b = y[2 * e + 1];
-        if (turned) {
-          y[2 * e] = a * c8[e] - b * s8[e];
-          y[2 * e + 1] = b * c8[e] + a * s8[e];
-        }
+        ss = __builtin_fmaf(lo[e], lo[e], ss);
+        ss = __builtin_fmaf(hi[e], hi[e], ss);
       }
-    } else if (p.rot > 0) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float other = __shfl(y[e], lane + hop);
-        const float cross = second ? other * s8[e] : -(other * s8[e]);
-        if (turned) y[e] = y[e] * c8[e] + cross;
+      const float inv = inv_sqrt(row_sum<LPR>(ss) * (1.0f / D) + p.eps);
+      lo *= inv;
+      hi *= inv;
+      if (is_q) {
+        lo *= wq.lo;
+        hi *= wq.hi;
+      } else {
+        lo *= wk.lo;
+        hi *= wk.hi;
       }
     }
-    if (r >= rows) continue;
+    if (p.rot > 0) {
+      // (without rotation cos is 1 and sin 0: exact, except that 0 times an infinity must
+      // not be added)
+      f32x4 x = lo, y = hi;
+      if (p.interleaved) {
+        x = f32x4{lo[0], lo[2], hi[0], hi[2]};
+        y = f32x4{lo[1], lo[3], hi[1], hi[3]};
+      }
+      f32x4 a, b;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        a[e] = __builtin_fmaf(x[e], c4[e], -(y[e] * s4[e]));
+        b[e] = __builtin_fmaf(y[e], c4[e], x[e] * s4[e]);
+      }
+      if (turned) {
+        lo = p.interleaved ? f32x4{a[0], b[0], a[1], b[1]} : a;
+        hi = p.interleaved ? f32x4{a[2], b[2], a[3], b[3]} : b;
+      }
+    }
+    if (row >= in.heads) continue;
     if (is_q || CACHE == kNoCache) {
       const HeadView& o = is_q ? p.q_out : p.k_out;
-      const long long h = is_q ? r : r - hq;
-      const u32x4 w = bits_as<u32x4>(__builtin_convertvector(y, typename A::V8));
-      *reinterpret_cast<u32x4*>(
-          o.data + 2 * ((long long)token * o.token_stride + h * o.head_stride + 8 * j)) = w;
+      char* at = o.data + 2 * ((uint64_t)(uint32_t)token * (uint32_t)o.token_stride +
+                               (uint64_t)(uint32_t)row * (uint32_t)o.head_stride);
+      *reinterpret_cast<u32x2*>(at + 2 * e0) = bits_as<u32x2>(__builtin_convertvector(lo, V4));
+      *reinterpret_cast<u32x2*>(at + 2 * e1) = bits_as<u32x2>(__builtin_convertvector(hi, V4));
     } else if (stored) {
-      const int h = r - hq;
       const long long page = slot >> p.page_shift;
-      const long long at = (((page * p.kv_heads + h) << p.page_shift) +
-                            (slot & ((1 << p.page_shift) - 1))) * D + 8 * j;
+      const long long at = (((page * p.kv_heads + row) << p.page_shift) +
+                            (slot & ((1 << p.page_shift) - 1))) * D;
       if constexpr (CACHE == kCacheE4m3) {
-        const float scale = p.k_scale ? p.k_scale[h] : 1.0f;
+        const float scale = p.k_scale ? p.k_scale[row] : 1.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = y[e] / scale;
-        const u32x2 w = {pack_e4m3(y[0], y[1]) | pack_e4m3(y[2], y[3]) << 16,
-                         pack_e4m3(y[4], y[5]) | pack_e4m3(y[6], y[7]) << 16};
-        *reinterpret_cast<u32x2*>(p.ck + at) = w;
+        for (int e = 0; e < 4; ++e) {
+          lo[e] = lo[e] / scale;
+          hi[e] = hi[e] / scale;
+        }
+        *reinterpret_cast<uint32_t*>(p.ck + at + e0) =
+            pack_e4m3(lo[0], lo[1]) | pack_e4m3(lo[2], lo[3]) << 16;
+        *reinterpret_cast<uint32_t*>(p.ck + at + e1) =
+            pack_e4m3(hi[0], hi[1]) | pack_e4m3(hi[2], hi[3]) << 16;
       } else {
-        *reinterpret_cast<u32x4*>(p.ck + 2 * at) =
-            bits_as<u32x4>(__builtin_convertvector(y, typename A::V8));
+        *reinterpret_cast<u32x2*>(p.ck + 2 * (at + e0)) =
+            bits_as<u32x2>(__builtin_convertvector(lo, V4));
+        *reinterpret_cast<u32x2*>(p.ck + 2 * (at + e1)) =
+            bits_as<u32x2>(__builtin_convertvector(hi, V4));
       }
     }
   }
@@ -251,26 +319,23 @@ __device__ __forceinline__ void values_wave(const RowsParams& p, int token, int 
 template <typename A, int D, int CACHE>
 __global__ __launch_bounds__(kRowsThreads) void k_rows(RowsParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  __shared__ float angles[kRowsWaves][2][kMaxAngles];
+  __shared__ __align__(16) float angles[kRowsWaves][2][kMaxAngles];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int lane = threadIdx.x % kWave;
-  const int id = blockIdx.x * kRowsWaves + wave;
-  const int nrows = p.n * p.parts;
-  if (id < nrows) {
-    rows_wave<A, D, CACHE>(p, id / p.parts, id % p.parts, lane, angles[wave][0], angles[wave][1]);
-  } else if constexpr (CACHE != kNoCache) {
-    const int v = id - nrows;
-    if (v < p.n * p.vparts) values_wave<A, D, CACHE>(p, v / p.vparts, v % p.vparts, lane);
-  }
+  const int token = blockIdx.x * kRowsWaves + wave, part = blockIdx.y;
+  if (token >= p.n) return;
+  if (part < p.parts)
+    rows_wave<A, D, CACHE>(p, token, part, lane, angles[wave][0], angles[wave][1]);
+  else if constexpr (CACHE != kNoCache)
+    values_wave<A, D, CACHE>(p, token, part - p.parts, lane);
 #endif
 }
 
 template <typename A, int D, int CACHE>
 hipError_t launch_one(const RowsParams& p, hipStream_t stream) {
-  const long long waves =
-      (long long)p.n * p.parts + (CACHE != kNoCache ? (long long)p.n * p.vparts : 0);
-  const unsigned blocks = (unsigned)((waves + kRowsWaves - 1) / kRowsWaves);
-  k_rows<A, D, CACHE><<<dim3(blocks), dim3(kRowsThreads), 0, stream>>>(p);
+  const unsigned blocks = (unsigned)((p.n + kRowsWaves - 1) / kRowsWaves);
+  const unsigned parts = (unsigned)(p.parts + (CACHE != kNoCache ? p.vparts : 0));
+  k_rows<A, D, CACHE><<<dim3(blocks, parts), dim3(kRowsThreads), 0, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -308,7 +373,7 @@ hipError_t launch_rows(const RowsArgs& a) {
   p.rot = a.p.rot_dim;
   p.interleaved = a.p.interleaved != 0;
   const int per_iter = kWave / (a.D / 8);
-  const int iters = (a.q.heads + a.k.heads + per_iter - 1) / per_iter;
+  const int iters = (a.q.heads + per_iter - 1) / per_iter + (a.k.heads + per_iter - 1) / per_iter;
   // enough waves for 8 on every CU; beyond that a token's rows stay with one wave
   const int want = 8 * a.num_cus;
   p.parts = std::max(1, std::min(iters, (want + a.n - 1) / a.n));
