@@ -312,7 +312,7 @@ typedef struct {
  *      within a group of 8 rows: the matrix cores take 8 consecutive rows of one column
  *      per lane, which this layout keeps in one 16-byte (8-byte at 8 bits) word.
  * Both 16-byte aligned. head_dim 64, 128 or 256; page_size 16, 32, 64, 128 or 256;
- * kv_heads 1..MOE_MAX_HEADS; num_pages * page_size below 2^31. An MOE_E4M3 cache holds
+ * kv_heads 1..MOE_MAX_HEADS; num_pages * page_size and num_pages * kv_heads below 2^31. An MOE_E4M3 cache holds
  * value / scale of its head, rounded to nearest even and clamped to +-448 (NaN stays NaN);
  * k_scale and v_scale are fp32 [kv_heads] in device memory, NULL for 1. For 16-bit caches
  * they must be NULL. */

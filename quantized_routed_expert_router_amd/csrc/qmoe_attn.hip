@@ -75,7 +75,8 @@ moe_status check_cache(const moe_kv_cache* c) {
   const int ps = c->page_size;
   if (ps != 16 && ps != 32 && ps != 64 && ps != 128 && ps != 256) return MOE_ERR_UNSUPPORTED;
   if (c->kv_heads < 1 || c->kv_heads > MOE_MAX_HEADS) return MOE_ERR_INVALID_ARGUMENT;
-  if (c->num_pages < 1 || (long long)c->num_pages * ps > kMaxLayoutInt)
+  if (c->num_pages < 1 || (long long)c->num_pages * ps > kMaxLayoutInt ||
+      (long long)c->num_pages * c->kv_heads > kMaxLayoutInt)
     return MOE_ERR_INVALID_ARGUMENT;
   return MOE_OK;
 }

@@ -97,6 +97,13 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b) {
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// Workgroup barrier for LDS alone: global loads in flight stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // Non-finite values behind a mask. A masked probability is 0, and 0 times NaN or infinity
 // is NaN, so the products of a tile that not all rows see leave such values out
 // (clear_nonfinite), and what they do to the rows that see them is added from counts:

@@ -192,7 +192,7 @@ __device__ __forceinline__ bool bad_page(const PrefillParams& p, const int32_t* 
 #endif  // __HIP_DEVICE_COMPILE__
 
 template <typename A, int D, bool F8, int NW>
-__global__ __launch_bounds__(64 * NW) void k_attn_prefill(PrefillParams p) {
+__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prefill(PrefillParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   typedef typename A::V8 V8;
   constexpr int KT = kTileElems / D, BM = 32 * NW, THREADS = 64 * NW;
@@ -286,7 +286,7 @@ __global__ __launch_bounds__(64 * NW) void k_attn_prefill(PrefillParams p) {
     if (i0 + 1 < i1) st.ids(p, table, t.keys.tile(i0 + 1) * KT, tid);
     stage_store(0, edge);
   }
-  __syncthreads();
+  lds_barrier();
 #pragma unroll 1
   for (int i = i0; i < i1; ++i) {
     const int buf = (i - i0) & 1;
@@ -400,7 +400,7 @@ __global__ __launch_bounds__(64 * NW) void k_attn_prefill(PrefillParams p) {
     if (more) stage_store(buf ^ 1, edge_next);
     bad = bad_next;
     edge = edge_next;
-    __syncthreads();
+    lds_barrier();
   }
 
   l += __shfl_xor(l, 32);
