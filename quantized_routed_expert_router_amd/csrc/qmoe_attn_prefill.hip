@@ -197,8 +197,9 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prefill(Pref
   typedef typename A::V8 V8;
   constexpr int KT = kTileElems / D, BM = 32 * NW, THREADS = 64 * NW;
   constexpr int KS = D / 16, DT = D / 32, HALVES = KT / 32;
-  __shared__ u32x4 lk[2][KT * D / 8], lv[2][KT * D / 8];
-  __shared__ int dirty[2][NW];  // an edge tile had non-finite values in a wave's part
+  constexpr int STEP = NW == 8 ? 2 : 1, BUFS = 2 * STEP;  // tiles between barriers
+  __shared__ u32x4 lk[BUFS][KT * D / 8], lv[BUFS][KT * D / 8];
+  __shared__ int dirty[BUFS][NW];  // an edge tile had non-finite values in a wave's part
 
   // Workgroups go to the 8 XCDs in turn: with the kv head in the low digits, an XCD's
   // workgroups share few heads' keys in its L2. Later row tiles see more keys: they start
@@ -262,9 +263,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prefill(Pref
   float m = kNegInf, l = 0.0f;  // scaled reference maximum; this lane's part of the sum
 
   Stage<A, D, F8, KT, THREADS> st;
-  // Of the tile in LDS and the next: a page of it lies outside the cache; it is an edge tile,
-  // which not all of the workgroup's rows see.
-  bool bad = false, bad_next = false, edge = false, edge_next = false;
+  // An edge tile: not all of the workgroup's rows see all of it.
   auto is_edge = [&](bool bad_tile, int key0) {
     return bad_tile || key0 + KT - 1 > first_key ||
            (p.mask.window != 0 && key0 <= last_key - p.mask.window &&
@@ -277,27 +276,40 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prefill(Pref
     }
     st.store(lk[buf], lv[buf], tid);
   };
-  if (i0 < i1) {
-    const int key0 = t.keys.tile(i0) * KT;
-    st.ids(p, table, key0, tid);
+  // Tile i0 + j lies in buffer j % BUFS. While tile j is worked on, tile j + STEP is loaded;
+  // it goes to a buffer that was last read before the last barrier.
+  int flags = 0;  // bits 2 (j % BUFS), + 1: tile j is bad, an edge tile
+  auto note = [&](int j, int key0) {
+    const bool bad_tile = bad_page<KT>(p, table, key0, last_key);
+    const bool edge_tile = is_edge(bad_tile, key0);
+    const int at = 2 * (j & (BUFS - 1));
+    flags = (flags & ~(3 << at)) | (bad_tile ? 1 << at : 0) | (edge_tile ? 2 << at : 0);
+    return edge_tile;
+  };
+  const int count = i1 - i0;
+  if (count > 0) st.ids(p, table, t.keys.tile(i0) * KT, tid);
+#pragma unroll
+  for (int j = 0; j < STEP; ++j) {
+    if (j >= count) continue;
+    const int key0 = t.keys.tile(i0 + j) * KT;
     st.load(p, kvh, key0, tid);
-    bad = bad_page<KT>(p, table, key0, last_key);
-    edge = is_edge(bad, key0);
-    if (i0 + 1 < i1) st.ids(p, table, t.keys.tile(i0 + 1) * KT, tid);
-    stage_store(0, edge);
+    if (j + 1 < count) st.ids(p, table, t.keys.tile(i0 + j + 1) * KT, tid);
+    const bool edge_tile = note(j, key0);
+    stage_store(j, edge_tile);
   }
   lds_barrier();
 #pragma unroll 1
-  for (int i = i0; i < i1; ++i) {
-    const int buf = (i - i0) & 1;
-    const int key0 = t.keys.tile(i) * KT;
-    const bool more = i + 1 < i1;
+  for (int j = 0; j < count; ++j) {
+    const int buf = j & (BUFS - 1);
+    const int key0 = t.keys.tile(i0 + j) * KT;
+    const bool bad = flags >> (2 * buf) & 1, edge = flags >> (2 * buf) & 2;
+    const bool more = j + STEP < count;
+    bool edge_next = false;
     if (more) {
-      const int k1 = t.keys.tile(i + 1) * KT;
+      const int k1 = t.keys.tile(i0 + j + STEP) * KT;
       st.load(p, kvh, k1, tid);
-      bad_next = bad_page<KT>(p, table, k1, last_key);
-      edge_next = is_edge(bad_next, k1);
-      if (i + 2 < i1) st.ids(p, table, t.keys.tile(i + 2) * KT, tid);
+      edge_next = note(j + STEP, k1);
+      if (j + STEP + 1 < count) st.ids(p, table, t.keys.tile(i0 + j + STEP + 1) * KT, tid);
     }
     const bool sees = any && key0 <= pos_max &&
                       (p.mask.window == 0 || key0 + KT - 1 > pos_min - p.mask.window ||
@@ -397,10 +409,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prefill(Pref
         }
       }
     }
-    if (more) stage_store(buf ^ 1, edge_next);
-    bad = bad_next;
-    edge = edge_next;
-    lds_barrier();
+    if (more) stage_store((j + STEP) & (BUFS - 1), edge_next);
+    if (STEP == 1 || (j & 1)) lds_barrier();
   }
 
   l += __shfl_xor(l, 32);
