@@ -2,7 +2,9 @@
 rotation of query and key heads, the paged key-value cache, and attention over it for
 decode windows and prefill chunks.
 
-Argument marshalling only, as in `qmoe`. Every call works on the GPU of its tensors (made
+Argument marshalling only, as in `qmoe`. The usual calls (nothing given for outputs,
+workspace and stream, tensors on the current device) go through a native short path with
+the same checks; whatever it does not take is checked and marshalled here. Every call works on the GPU of its tensors (made
 current for the call when it is not) and on that GPU's current stream, or on `stream`;
 outputs and workspaces that a call makes for itself belong to that stream.
 """
@@ -14,6 +16,12 @@ from dataclasses import dataclass
 import torch
 
 from .qmoe import BYTES, F32, I32, MOE_OK, MoeError, _Args, _ptr, lib
+
+try:
+    from . import _fastcall
+except ImportError as e:
+    raise ImportError("_fastcall.so is missing or does not load: build it with "
+                      "`python -m quantized_routed_expert_router_amd.build`") from e
 
 MAX_WINDOW_TOKENS = 16
 MAX_HEADS = 512
@@ -124,6 +132,13 @@ class _HeadArgs(_Args):
         return at
 
 
+def _result(fn: str, r):
+    """The outputs of a call on the short path, or its error."""
+    if type(r) is int:
+        raise MoeError(fn, r)
+    return r
+
+
 def _on_stream(fn, args, stream, t):
     """The call with `stream` current, so that what it allocates belongs to that stream."""
     if isinstance(t, torch.Tensor) and t.is_cuda and stream.device != t.device:
@@ -221,6 +236,13 @@ def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torc
     """moe_qk_norm_rope: norm and rotation of query and key heads ``[n, heads, head_dim]``
     (either may be None) at `positions` int32 ``[n]``. Returns (q_out, k_out), new tensors
     unless given; an output may be its own input."""
+    if stream is None and q_out is None and k_out is None and type(q) is torch.Tensor and \
+            q.is_cuda:
+        gpu = _current_device()
+        r = _fastcall.qk_norm_rope(gpu, q, k, positions, p.q_norm, p.k_norm, p.inv_freq, p.eps,
+                                   p.weight_offset, p.interleaved, _raw_stream(gpu))
+        if r is not None:
+            return _result("moe_qk_norm_rope", r)
     some = q if q is not None else k
     if some is None:
         raise ValueError("q, k: at least one is needed")
@@ -266,6 +288,14 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Ten
     cache at `slots` int32 ``[n]`` (page * page_size + row; outside the cache: not stored).
     With `q`, its heads are normed and rotated in the same launch; returns q_out (a new
     tensor unless given; None without q)."""
+    if stream is None and q_out is None and p is not None and type(q) is torch.Tensor and \
+            q.is_cuda:
+        gpu = _current_device()
+        r = _fastcall.kv_append(gpu, cache.k, cache.v, cache.k_scale, cache.v_scale, k, v, slots,
+                                positions, p.q_norm, p.k_norm, p.inv_freq, p.eps, p.weight_offset,
+                                p.interleaved, q, _raw_stream(gpu))
+        if r is not None:
+            return _result("moe_kv_append", r)
     if stream is not None:
         return _on_stream(kv_append, (cache, k, v, slots, positions, p, q, q_out), stream, k)
     args = _HeadArgs()
@@ -327,6 +357,13 @@ def prefill_workspace_bytes(cache: KVCache, q_heads: int, n_seqs: int, n_tokens:
 
 
 def _attend(cache, q, q_starts, page_table, kv_lens, scale, window, sinks, out, ws):
+    if out is None and ws is None and type(q) is torch.Tensor and q.is_cuda:
+        gpu = _current_device()
+        r = _fastcall.attend(gpu, cache.k, cache.v, cache.k_scale, cache.v_scale, q, q_starts,
+                             page_table, kv_lens, q.shape[-1] ** -0.5 if scale is None else scale,
+                             window, sinks, _raw_stream(gpu))
+        if r is not None:
+            return _result("moe_attn_decode" if q_starts is None else "moe_attn_prefill", r)
     args = _HeadArgs()
     qs = args.heads(q, "q", HALF)
     n, heads, D = q.shape

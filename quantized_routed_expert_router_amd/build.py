@@ -1,9 +1,10 @@
-"""Compile the gfx950 shared libraries of this package in-tree with hipcc.
+"""Compile the shared libraries of this package in-tree, the gfx950 ones with hipcc.
 
-Two libraries are produced next to this file:
+Produced next to this file:
 
 * ``libqmoe.so``       - the MoE layer library (C ABI declared in ``include/qmoe.h``);
-* ``libqmoe_synth.so`` - the seeded input generator (host and device fill routines).
+* ``libqmoe_synth.so`` - the seeded input generator (host and device fill routines);
+* ``_fastcall.so``     - the short path of the attention half's Python calls (host code).
 
 Run ``python -m quantized_routed_expert_router_amd.build`` or call :func:`build`.
 """
@@ -43,6 +44,24 @@ LIBS = {
 }
 
 
+FASTCALL = "_fastcall.so"
+
+
+def _fastcall_command(source: str, out: str) -> list[str]:
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    includes = [*include_paths(), sysconfig.get_paths()["include"]]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Wno-sign-compare",
+            f"-D_GLIBCXX_USE_CXX11_ABI={abi}", f"-I{os.path.join(REPO_DIR, 'include')}",
+            *(arg for d in includes for arg in ("-isystem", d)), source, "-o", out,
+            *(f"-L{d}" for d in library_paths()), "-ltorch_python", "-ltorch_cpu", "-lc10",
+            f"-L{PKG_DIR}", "-lqmoe", "-Wl,-rpath,$ORIGIN"]
+
+
 def _run(cmd: list[str], what: str, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
@@ -51,7 +70,7 @@ def _run(cmd: list[str], what: str, verbose: bool) -> None:
     noise = "is not a recognized feature for this target"
     msgs = [ln for ln in (res.stdout + res.stderr).splitlines() if noise not in ln]
     if res.returncode != 0:
-        raise RuntimeError(f"hipcc failed for {what}:\n" + "\n".join(msgs))
+        raise RuntimeError(f"{cmd[0]} failed for {what}:\n" + "\n".join(msgs))
     if msgs and verbose:
         print("\n".join(msgs), flush=True)
 
@@ -74,6 +93,10 @@ def build(verbose: bool = False) -> None:
             _run([HIPCC, f"--offload-arch={ARCH}", "-fPIC", "-shared", *objs, "-o", out + ".tmp"],
                  name, verbose)
             os.replace(out + ".tmp", out)
+    # links against libqmoe.so
+    out = os.path.join(PKG_DIR, FASTCALL)
+    _run(_fastcall_command(os.path.join(CSRC, "fastcall.cpp"), out + ".tmp"), FASTCALL, verbose)
+    os.replace(out + ".tmp", out)
 
 
 if __name__ == "__main__":
