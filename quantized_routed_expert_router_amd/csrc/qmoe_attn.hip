@@ -1,6 +1,6 @@
 // C ABI of the attention half: argument validation and workspace queries. Every check runs
 // on the host before anything is enqueued.
-#include "qmoe_attn_internal.h"
+#include "qmoe_attn_plan.h"
 
 namespace qmoe {
 namespace {

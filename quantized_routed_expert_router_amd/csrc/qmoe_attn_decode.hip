@@ -14,17 +14,14 @@
 // loop has to spare.
 #include <type_traits>
 
-#include "qmoe_attn_internal.h"
+#include "qmoe_attn_plan.h"
 
 namespace qmoe {
 namespace {
 
-constexpr int kTile = 32;           // keys of one step of a wave
 // A row's reference maximum moves only when the new maximum exceeds it by this many powers
 // of two; probabilities then reach 2^8, which fp32 sums and both 16-bit types hold.
-constexpr float kLazy = 8.0f;
-constexpr int kUnsplitTiles = 32;
-constexpr int kMinSplitTiles = 8;   // 256 keys: below that a split costs more than it saves
+[[maybe_unused]] constexpr float kLazy = 8.0f;
 
 struct DecodeParams {
   HeadView q;
@@ -153,14 +150,6 @@ __device__ __forceinline__ int out_col(int dt, int row) {
 
 #endif  // __HIP_DEVICE_COMPILE__
 
-// Row tiles (of 16 query rows) a wave takes, and row groups of a workgroup: each group's
-// four waves run through all of the split's keys for their own row tiles, the second
-// group's reads then come from the caches. What a wave takes is bounded by its registers:
-// accumulators (D/4 a row tile) beside a tile's keys and values (D/2 at 16 bits).
-template <int D>
-constexpr int kMostTiles = D == 64 ? 4 : 2;
-template <int D>
-constexpr int kMostGroups = D == 128 ? 2 : 1;
 // Waves a SIMD that the registers have to allow. Two rather than one where they fit: with
 // more than 256 registers a wave the accumulators would go to the accumulation registers.
 template <int D, int NT>
@@ -460,18 +449,6 @@ __global__ __launch_bounds__(kJoinThreads) void k_attn_decode_join(DecodeParams 
 #endif
 }
 
-// Row tiles a wave takes and row groups of a workgroup for a window of `rows` rows.
-struct Shape {
-  int tiles, groups;
-};
-Shape window_shape(int rows, int D) {
-  const int most = D == 64 ? kMostTiles<64> : D == 128 ? kMostTiles<128> : kMostTiles<256>;
-  Shape s{1, 1};
-  while (s.tiles < most && 16 * s.tiles < rows) s.tiles *= 2;
-  if (16 * s.tiles < rows && D == 128) s.groups = 2;
-  return s;
-}
-
 template <typename A, int D, bool F8, int NT, int RG, int KW = 4>
 hipError_t launch_one(const DecodeParams& p, int n_seqs, hipStream_t stream) {
   k_attn_decode<A, D, F8, NT, RG, KW><<<dim3(p.splits, p.kv_heads * p.row_tiles, n_seqs),
@@ -518,35 +495,6 @@ hipError_t launch_type(const DecodeParams& p, int D, bool f8, int n_seqs, hipStr
 }
 
 }  // namespace
-
-AttnPlan decode_plan(int q_heads, int kv_heads, int D, int n_seqs, int window_tokens,
-                     int max_pages, int page_size, const moe_attn& a, int num_cus) {
-  AttnPlan plan{};
-  const int rows = window_tokens * (q_heads / kv_heads);
-  const Shape shape = window_shape(rows, D);
-  plan.tile_rows = 16 * shape.tiles * shape.groups;
-  plan.row_tiles = (rows + plan.tile_rows - 1) / plan.tile_rows;
-  // tiles of the longest possible sequence (of its visible part)
-  long long tiles = ((long long)max_pages * page_size + kTile - 1) / kTile;
-  if (a.window > 0)
-    tiles = std::min(tiles, ((long long)a.window + window_tokens) / kTile + 2 +
-                                ((long long)a.sinks + kTile - 1) / kTile);
-  const long long base = (long long)n_seqs * kv_heads * plan.row_tiles;
-  // workgroups that run at once: two a CU, one where a wave takes more than 256 registers
-  const long long at_once = (D == 256 && shape.tiles == 2 ? 1 : 2) * num_cus;
-  const long long fill = (at_once + base - 1) / base;
-  const long long even = (tiles + 63) / 64;  // 2048 keys, so that long sequences share out
-  // a few tiles are done sooner than a second launch
-  const long long most = tiles <= kUnsplitTiles ? 1 : std::max(1ll, tiles / kMinSplitTiles);
-  plan.splits = (int)std::min<long long>({std::max(fill, even), most, kMaxSplits});
-  if (plan.splits > 1) {
-    const size_t parts = (size_t)n_seqs * window_tokens * q_heads * plan.splits;
-    plan.partial = 0;
-    plan.stats = align256(parts * D * sizeof(float));
-    plan.total = plan.stats + align256(parts * sizeof(float2));
-  }
-  return plan;
-}
 
 hipError_t launch_attn_decode(const AttnArgs& a, const AttnPlan& plan) {
   DecodeParams p{};

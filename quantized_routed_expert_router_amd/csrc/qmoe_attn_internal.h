@@ -255,11 +255,6 @@ struct AttnPlan {
   size_t partial, stats, total;  // workspace offsets and size
 };
 
-AttnPlan decode_plan(int q_heads, int kv_heads, int D, int n_seqs, int window_tokens,
-                     int max_pages, int page_size, const moe_attn& a, int num_cus);
-AttnPlan prefill_plan(int q_heads, int kv_heads, int D, int n_seqs, int n_tokens, int max_pages,
-                      int page_size, const moe_attn& a, int num_cus);
-
 hipError_t launch_rows(const RowsArgs& a);
 hipError_t launch_attn_decode(const AttnArgs& a, const AttnPlan& plan);
 hipError_t launch_attn_prefill(const AttnArgs& a, const AttnPlan& plan);

@@ -1,0 +1,103 @@
+// How an attention call is cut into workgroups: row tiles, splits of the key axis and the
+// workspace for joining them. Host code, and the constants that the kernels share with it.
+#pragma once
+
+#include "qmoe_attn_internal.h"
+
+namespace qmoe {
+
+// ------------------------------------------------------------------ decode windows
+
+constexpr int kTile = 32;  // keys of one step of a wave
+// A context of a few tiles is done sooner than a second launch; below 256 keys a split costs
+// more than it saves.
+constexpr int kUnsplitTiles = 32;
+constexpr int kMinSplitTiles = 8;
+
+// Row tiles (of 16 query rows) a wave takes, and row groups of a workgroup: each group's
+// four waves run through all of the split's keys for their own row tiles, the second
+// group's reads then come from the caches. What a wave takes is bounded by its registers:
+// accumulators (D/4 a row tile) beside a tile's keys and values (D/2 at 16 bits).
+template <int D>
+constexpr int kMostTiles = D == 64 ? 4 : 2;
+template <int D>
+constexpr int kMostGroups = D == 128 ? 2 : 1;
+
+// Row tiles a wave takes and row groups of a workgroup for a window of `rows` rows.
+struct Shape {
+  int tiles, groups;
+};
+inline Shape window_shape(int rows, int D) {
+  const int most = D == 64 ? kMostTiles<64> : D == 128 ? kMostTiles<128> : kMostTiles<256>;
+  Shape s{1, 1};
+  while (s.tiles < most && 16 * s.tiles < rows) s.tiles *= 2;
+  if (16 * s.tiles < rows && D == 128) s.groups = 2;
+  return s;
+}
+
+inline AttnPlan decode_plan(int q_heads, int kv_heads, int D, int n_seqs, int window_tokens,
+                            int max_pages, int page_size, const moe_attn& a, int num_cus) {
+  AttnPlan plan{};
+  const int rows = window_tokens * (q_heads / kv_heads);
+  const Shape shape = window_shape(rows, D);
+  plan.tile_rows = 16 * shape.tiles * shape.groups;
+  plan.row_tiles = (rows + plan.tile_rows - 1) / plan.tile_rows;
+  // tiles of the longest possible sequence (of its visible part)
+  long long tiles = ((long long)max_pages * page_size + kTile - 1) / kTile;
+  if (a.window > 0)
+    tiles = std::min(tiles, ((long long)a.window + window_tokens) / kTile + 2 +
+                                ((long long)a.sinks + kTile - 1) / kTile);
+  const long long base = (long long)n_seqs * kv_heads * plan.row_tiles;
+  // workgroups that run at once: two a CU, one where a wave takes more than 256 registers
+  const long long at_once = (D == 256 && shape.tiles == 2 ? 1 : 2) * num_cus;
+  const long long fill = (at_once + base - 1) / base;
+  const long long even = (tiles + 63) / 64;  // 2048 keys, so that long sequences share out
+  const long long most = tiles <= kUnsplitTiles ? 1 : std::max(1ll, tiles / kMinSplitTiles);
+  plan.splits = (int)std::min<long long>({std::max(fill, even), most, kMaxSplits});
+  if (plan.splits > 1) {
+    const size_t parts = (size_t)n_seqs * window_tokens * q_heads * plan.splits;
+    plan.partial = 0;
+    plan.stats = align256(parts * D * sizeof(float));
+    plan.total = plan.stats + align256(parts * sizeof(float2));
+  }
+  return plan;
+}
+
+// ------------------------------------------------------------------ prefill chunks
+
+constexpr int kMinSplitKeys = 512;
+
+// Waves of a workgroup (32 rows each): 8 share a key tile among the most rows. Wide heads
+// need 128 accumulators a lane and more than 256 registers, one wave a SIMD; and few rows
+// fill the card better in halves.
+inline int prefill_waves(int q_heads, int D, int n_tokens, int num_cus) {
+  if (D == 256) return 4;
+  return (long long)n_tokens * q_heads >= 256ll * num_cus ? 8 : 4;
+}
+
+inline AttnPlan prefill_plan(int q_heads, int kv_heads, int D, int n_seqs, int n_tokens,
+                             int max_pages, int page_size, const moe_attn& a, int num_cus) {
+  AttnPlan plan{};
+  plan.tile_rows = 32 * prefill_waves(q_heads, D, n_tokens, num_cus);
+  const long long rows = (long long)n_tokens * (q_heads / kv_heads);
+  plan.row_tiles = (int)(rows / plan.tile_rows) + n_seqs;
+  // row tiles that have rows, about; splits fill the card when they do not
+  const long long base =
+      std::max<long long>((rows + plan.tile_rows - 1) / plan.tile_rows,
+                          std::min(n_seqs, n_tokens)) * kv_heads;
+  long long keys = (long long)max_pages * page_size;
+  if (a.window > 0)
+    keys = std::min(keys, (long long)a.window + n_tokens + a.sinks + 128);
+  const long long most = std::max(1ll, keys / kMinSplitKeys);
+  const long long fill = num_cus / base;
+  plan.splits = (int)std::max(1ll, std::min<long long>({fill, most, kMaxSplits}));
+  if (plan.splits > 1) {
+    const size_t parts = (size_t)n_tokens * q_heads * plan.splits;
+    plan.partial = 0;
+    plan.stats = align256(parts * D * sizeof(float));
+    plan.total = plan.stats + align256(parts * sizeof(float2));
+  }
+  return plan;
+}
+
+}  // namespace qmoe

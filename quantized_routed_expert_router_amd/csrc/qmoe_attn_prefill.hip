@@ -16,16 +16,15 @@
 // relative error, 2^-9 in bf16, is that of the output's own rounding).
 #include <type_traits>
 
-#include "qmoe_attn_internal.h"
+#include "qmoe_attn_plan.h"
 
 namespace qmoe {
 namespace {
 
-constexpr int kTileElems = 8192;  // keys x columns of one LDS tile: 16 KB each of keys and values
-constexpr int kMinSplitKeys = 512;
+[[maybe_unused]] constexpr int kTileElems = 8192;  // keys x columns of one LDS tile: 16 KB each of keys and values
 // A row's reference maximum moves only when the new maximum exceeds it by this many powers
 // of two; probabilities then reach 2^8, which fp32 sums and both 16-bit types hold.
-constexpr float kLazy = 8.0f;
+[[maybe_unused]] constexpr float kLazy = 8.0f;
 
 struct PrefillParams {
   HeadView q;
@@ -463,14 +462,6 @@ __global__ __launch_bounds__(kJoinThreads) void k_attn_prefill_join(PrefillParam
 #endif
 }
 
-// Waves of a workgroup (32 rows each): 8 share a key tile among the most rows. Wide heads
-// need 128 accumulators a lane and more than 256 registers, one wave a SIMD; and few rows
-// fill the card better in halves.
-int prefill_waves(int q_heads, int D, int n_tokens, int num_cus) {
-  if (D == 256) return 4;
-  return (long long)n_tokens * q_heads >= 256ll * num_cus ? 8 : 4;
-}
-
 template <typename A, int D, bool F8, int NW>
 hipError_t launch_one(const PrefillParams& p, hipStream_t stream) {
   k_attn_prefill<A, D, F8, NW><<<dim3((unsigned)(p.slots * p.kv_heads), p.splits),
@@ -502,29 +493,6 @@ hipError_t launch_type(const PrefillParams& p, int D, bool f8, int nw, hipStream
 }
 
 }  // namespace
-
-AttnPlan prefill_plan(int q_heads, int kv_heads, int D, int n_seqs, int n_tokens, int max_pages,
-                      int page_size, const moe_attn& a, int num_cus) {
-  AttnPlan plan{};
-  plan.tile_rows = 32 * prefill_waves(q_heads, D, n_tokens, num_cus);
-  const long long rows = (long long)n_tokens * (q_heads / kv_heads);
-  plan.row_tiles = (int)(rows / plan.tile_rows) + n_seqs;
-  // Row tiles that have rows, at least; splits fill the card when they do not.
-  const long long base = std::max(1ll, (rows + plan.tile_rows - 1) / plan.tile_rows) * kv_heads;
-  long long keys = (long long)max_pages * page_size;
-  if (a.window > 0)
-    keys = std::min(keys, (long long)a.window + n_tokens + a.sinks + 128);
-  const long long most = std::max(1ll, keys / kMinSplitKeys);
-  const long long fill = num_cus / base;
-  plan.splits = (int)std::max(1ll, std::min<long long>({fill, most, kMaxSplits}));
-  if (plan.splits > 1) {
-    const size_t parts = (size_t)n_tokens * q_heads * plan.splits;
-    plan.partial = 0;
-    plan.stats = align256(parts * D * sizeof(float));
-    plan.total = plan.stats + align256(parts * sizeof(float2));
-  }
-  return plan;
-}
 
 hipError_t launch_attn_prefill(const AttnArgs& a, const AttnPlan& plan) {
   PrefillParams p{};
