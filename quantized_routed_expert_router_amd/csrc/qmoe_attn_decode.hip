@@ -150,31 +150,25 @@ __device__ __forceinline__ int out_col(int dt, int row) {
 
 #endif  // __HIP_DEVICE_COMPILE__
 
-// Waves a SIMD that the registers have to allow. Two rather than one where they fit: with
-// more than 256 registers a wave the accumulators would go to the accumulation registers.
-template <int D, int NT>
-constexpr int kMinWaves = D == 256 ? 1 : 2;
-
 // Wide heads leave no registers for the query fragments: they are read from LDS at each
 // tile (1 KB a step of the product, a small part of what LDS can deliver meanwhile).
-template <int D>
-constexpr bool kQueriesInLds = D == 256;
+template <int D, int NT>
+constexpr bool kQueriesInLds = D * NT >= 256 && D != 64;
 
-// KW: waves that share a row group's keys.
-template <typename A, int D, bool F8, int NT, int RG, int KW>
-__global__ __launch_bounds__(KW * RG * kWave, (kMinWaves<D, NT>)) void k_attn_decode(DecodeParams p) {
+// NT: row tiles of 16 rows; KW: waves, which take the split's key tiles in turn.
+template <typename A, int D, bool F8, int NT, int KW>
+__global__ __launch_bounds__(KW * kWave, decode_waves(NT, D)) void k_attn_decode(DecodeParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   typedef typename A::V8 V8;
   constexpr int KS = D / 32, DT = D / 16, kWaves = KW;
   constexpr int DC = D < 128 ? D : 128;  // columns joined at a time
-  __shared__ float sums[RG][kWaves][16][DC + 4];
-  __shared__ float stat_m[RG][kWaves][16], stat_l[RG][kWaves][16];
-  constexpr bool QLDS = kQueriesInLds<D>;
-  __shared__ u32x4 qs[RG][QLDS ? NT * KS : 1][kWave];
+  __shared__ float sums[kWaves][16][DC + 4];
+  __shared__ float stat_m[kWaves][16], stat_l[kWaves][16];
+  constexpr bool QLDS = kQueriesInLds<D, NT>;
+  __shared__ u32x4 qs[QLDS ? NT * KS : 1][kWave];
 
   const int lane = threadIdx.x % kWave;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) % kWaves;
-  const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) / kWaves;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int n16 = lane & 15, g = lane >> 4;
   const int split = blockIdx.x;
   const int kvh = blockIdx.y / p.row_tiles, rt = blockIdx.y % p.row_tiles;
@@ -186,7 +180,7 @@ __global__ __launch_bounds__(KW * RG * kWave, (kMinWaves<D, NT>)) void k_attn_de
   const int32_t* table = p.table + seq * p.table_stride;
   const int first_pos = sp.len - p.T;
   const int rows = p.T * p.group;
-  const int row0 = (rt * RG + group) * NT * 16;  // this row group's first row
+  const int row0 = rt * NT * 16;  // the workgroup's first row
 
   KeyRegs<A, D, F8> k;
   ValueRegs<A, D, F8> v;
@@ -214,13 +208,13 @@ __global__ __launch_bounds__(KW * RG * kWave, (kMinWaves<D, NT>)) void k_attn_de
                                       (long long)(real ? h : 0) * p.q.head_stride);
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      if (QLDS && ks % kWaves != wave) continue;
+      if (QLDS && (nt * KS + ks) % kWaves != wave) continue;
       const int col = F8 ? 64 * (ks >> 1) + 16 * g + 8 * (ks & 1) : 32 * ks + 8 * g;
       u32x4 w = *reinterpret_cast<const u32x4*>(src + 2 * col);
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[i] = real ? (w[i] ^ sc.flip) & sc.keep : 0u;
       if constexpr (QLDS)
-        qs[group][nt * KS + ks][lane] = w;
+        qs[nt * KS + ks][lane] = w;
       else
         q[nt][ks] = bits_as<V8>(w);
     }
@@ -264,7 +258,7 @@ __global__ __launch_bounds__(KW * RG * kWave, (kMinWaves<D, NT>)) void k_attn_de
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           if constexpr (QLDS)
-            qf[nt] = bits_as<V8>(qs[group][nt * KS + ks][lane]);
+            qf[nt] = bits_as<V8>(qs[nt * KS + ks][lane]);
           else
             qf[nt] = q[nt][ks];
         }
@@ -381,8 +375,8 @@ __global__ __launch_bounds__(KW * RG * kWave, (kMinWaves<D, NT>)) void k_attn_de
     lsum += __shfl_xor(lsum, 16);
     lsum += __shfl_xor(lsum, 32);
     if (g == 0) {
-      stat_m[group][wave][n16] = m[nt];
-      stat_l[group][wave][n16] = lsum;
+      stat_m[wave][n16] = m[nt];
+      stat_l[wave][n16] = lsum;
     }
 #pragma unroll
     for (int c0 = 0; c0 < D; c0 += DC) {
@@ -391,31 +385,30 @@ __global__ __launch_bounds__(KW * RG * kWave, (kMinWaves<D, NT>)) void k_attn_de
         if constexpr (F8) {
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            sums[group][wave][n16][out_col<F8>(dt, 4 * g + r) - c0] = o[nt][dt][r];
+            sums[wave][n16][out_col<F8>(dt, 4 * g + r) - c0] = o[nt][dt][r];
         } else {
-          *reinterpret_cast<f32x4*>(&sums[group][wave][n16][16 * dt + 4 * g - c0]) = o[nt][dt];
+          *reinterpret_cast<f32x4*>(&sums[wave][n16][16 * dt + 4 * g - c0]) = o[nt][dt];
         }
       }
       __syncthreads();
       constexpr int PER = DC / (4 * kWaves);  // columns a thread: 4 or 8
-      const int in = threadIdx.x % (kWaves * kWave);
-      const int r = in / (4 * kWaves), col = (in % (4 * kWaves)) * PER;
+      const int r = threadIdx.x / (4 * kWaves), col = (threadIdx.x % (4 * kWaves)) * PER;
       const int row = row0 + nt * 16 + r;
       if (row < rows) {
         float top = kNegInf, sum = 0.0f, weight[kWaves];
         typedef float FP __attribute__((ext_vector_type(PER)));
         FP y = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) top = fmaxf(top, stat_m[group][w][r]);
+        for (int w = 0; w < kWaves; ++w) top = fmaxf(top, stat_m[w][r]);
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-          weight[w] = rescale(stat_m[group][w][r] - (top == kNegInf ? 0.0f : top));
-          sum += weight[w] * stat_l[group][w][r];
+          weight[w] = rescale(stat_m[w][r] - (top == kNegInf ? 0.0f : top));
+          sum += weight[w] * stat_l[w][r];
         }
 #pragma unroll
         for (int w = 0; w < kWaves; ++w)
 #pragma unroll
-          for (int c = 0; c < PER; ++c) y[c] += weight[w] * sums[group][w][r][col + c];
+          for (int c = 0; c < PER; ++c) y[c] += weight[w] * sums[w][r][col + c];
         const long long token = (long long)seq * p.T + row / p.group;
         const long long at = token * hq + kvh * p.group + row % p.group;
         if (direct) {
@@ -449,10 +442,10 @@ __global__ __launch_bounds__(kJoinThreads) void k_attn_decode_join(DecodeParams 
 #endif
 }
 
-template <typename A, int D, bool F8, int NT, int RG, int KW = 4>
+template <typename A, int D, bool F8, int NT, int KW = 4>
 hipError_t launch_one(const DecodeParams& p, int n_seqs, hipStream_t stream) {
-  k_attn_decode<A, D, F8, NT, RG, KW><<<dim3(p.splits, p.kv_heads * p.row_tiles, n_seqs),
-                                        dim3(KW * RG * kWave), 0, stream>>>(p);
+  k_attn_decode<A, D, F8, NT, KW><<<dim3(p.splits, p.kv_heads * p.row_tiles, n_seqs),
+                                    dim3(KW * kWave), 0, stream>>>(p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   k_attn_decode_join<A, D><<<dim3((unsigned)(n_seqs * p.T * p.kv_heads * p.group),
@@ -462,24 +455,19 @@ hipError_t launch_one(const DecodeParams& p, int n_seqs, hipStream_t stream) {
 
 template <typename A, int D, bool F8>
 hipError_t launch_tiles(const DecodeParams& p, int n_seqs, hipStream_t stream) {
-  const Shape s = window_shape(p.T * p.group, D);
-  if constexpr (kMostGroups<D> == 2) {
-    if (s.groups == 2) return launch_one<A, D, F8, kMostTiles<D>, 2>(p, n_seqs, stream);
+  const int nt = window_tiles(p.T * p.group, D);
+  if constexpr (D != 256) {
+    if (nt == 4) return launch_one<A, D, F8, 4>(p, n_seqs, stream);
   }
-  if constexpr (kMostTiles<D> >= 4) {
-    if (s.tiles == 4) return launch_one<A, D, F8, 4, 1>(p, n_seqs, stream);
-  }
-  if constexpr (kMostTiles<D> >= 2) {
-    if (s.tiles == 2) return launch_one<A, D, F8, 2, 1>(p, n_seqs, stream);
-  }
+  if (nt == 2) return launch_one<A, D, F8, 2>(p, n_seqs, stream);
   // A short context on few workgroups is a chain of latencies, which twice the waves halve
   // (517 keys: 10.7 us against 8.3 and a joining launch of 3.9); on many, four waves run
   // nearer to the memory's rate (64 sequences at 8 bits: 370 us, with eight 447).
-  if constexpr (D <= 128) {
+  if constexpr (D != 256) {
     if (p.splits == 1 && (long long)n_seqs * p.kv_heads * p.row_tiles <= device_cu_count())
-      return launch_one<A, D, F8, 1, 1, 8>(p, n_seqs, stream);
+      return launch_one<A, D, F8, 1, 8>(p, n_seqs, stream);
   }
-  return launch_one<A, D, F8, 1, 1>(p, n_seqs, stream);
+  return launch_one<A, D, F8, 1>(p, n_seqs, stream);
 }
 
 template <typename A>

@@ -14,33 +14,25 @@ constexpr int kTile = 32;  // keys of one step of a wave
 constexpr int kUnsplitTiles = 32;
 constexpr int kMinSplitTiles = 8;
 
-// Row tiles (of 16 query rows) a wave takes, and row groups of a workgroup: each group's
-// four waves run through all of the split's keys for their own row tiles, the second
-// group's reads then come from the caches. What a wave takes is bounded by its registers:
-// accumulators (D/4 a row tile) beside a tile's keys and values (D/2 at 16 bits).
-template <int D>
-constexpr int kMostTiles = D == 64 ? 4 : 2;
-template <int D>
-constexpr int kMostGroups = D == 128 ? 2 : 1;
-
-// Row tiles a wave takes and row groups of a workgroup for a window of `rows` rows.
-struct Shape {
-  int tiles, groups;
-};
-inline Shape window_shape(int rows, int D) {
-  const int most = D == 64 ? kMostTiles<64> : D == 128 ? kMostTiles<128> : kMostTiles<256>;
-  Shape s{1, 1};
-  while (s.tiles < most && 16 * s.tiles < rows) s.tiles *= 2;
-  if (16 * s.tiles < rows && D == 128) s.groups = 2;
-  return s;
+// Row tiles (of 16 query rows) a wave takes: as many as the window has, while accumulators
+// (D/4 registers a row tile) fit beside a tile's keys and values (D/2 at 16 bits). More row
+// tiles go to workgroups of their own, which read the keys again.
+constexpr int kMostAccumulators = 128;
+inline int window_tiles(int rows, int D) {
+  int tiles = 1;
+  while (16 * tiles < rows && tiles < 4 && 2 * tiles * (D / 4) <= kMostAccumulators) tiles *= 2;
+  return tiles;
 }
+// Waves a SIMD that a wave's registers have to allow: two, so that accumulators stay out of
+// the accumulation registers, or one where that leaves too few.
+constexpr int decode_waves(int tiles, int D) { return D == 256 || tiles * D >= 512 ? 1 : 2; }
 
 inline AttnPlan decode_plan(int q_heads, int kv_heads, int D, int n_seqs, int window_tokens,
                             int max_pages, int page_size, const moe_attn& a, int num_cus) {
   AttnPlan plan{};
   const int rows = window_tokens * (q_heads / kv_heads);
-  const Shape shape = window_shape(rows, D);
-  plan.tile_rows = 16 * shape.tiles * shape.groups;
+  const int wave_tiles = window_tiles(rows, D);
+  plan.tile_rows = 16 * wave_tiles;
   plan.row_tiles = (rows + plan.tile_rows - 1) / plan.tile_rows;
   // tiles of the longest possible sequence (of its visible part)
   long long tiles = ((long long)max_pages * page_size + kTile - 1) / kTile;
@@ -48,8 +40,8 @@ inline AttnPlan decode_plan(int q_heads, int kv_heads, int D, int n_seqs, int wi
     tiles = std::min(tiles, ((long long)a.window + window_tokens) / kTile + 2 +
                                 ((long long)a.sinks + kTile - 1) / kTile);
   const long long base = (long long)n_seqs * kv_heads * plan.row_tiles;
-  // workgroups that run at once: two a CU, one where a wave takes more than 256 registers
-  const long long at_once = (D == 256 && shape.tiles == 2 ? 1 : 2) * num_cus;
+  // workgroups that run at once: two a CU, one where a wave takes many more than 256 registers
+  const long long at_once = (wave_tiles * D >= 512 ? 1 : 2) * num_cus;
   const long long fill = (at_once + base - 1) / base;
   const long long even = (tiles + 63) / 64;  // 2048 keys, so that long sequences share out
   const long long most = tiles <= kUnsplitTiles ? 1 : std::max(1ll, tiles / kMinSplitTiles);
@@ -89,7 +81,7 @@ inline AttnPlan prefill_plan(int q_heads, int kv_heads, int D, int n_seqs, int n
   if (a.window > 0)
     keys = std::min(keys, (long long)a.window + n_tokens + a.sinks + 128);
   const long long most = std::max(1ll, keys / kMinSplitKeys);
-  const long long fill = num_cus / base;
+  const long long fill = (plan.tile_rows == 128 && D != 256 ? 2 : 1) * num_cus / base;
   plan.splits = (int)std::max(1ll, std::min<long long>({fill, most, kMaxSplits}));
   if (plan.splits > 1) {
     const size_t parts = (size_t)n_tokens * q_heads * plan.splits;
