@@ -176,18 +176,6 @@ struct Stage {
   }
 };
 
-// Whether one of the tile's pages up to the last visible key lies outside the cache.
-template <int KT>
-__device__ __forceinline__ bool bad_page(const PrefillParams& p, const int32_t* table, int key0,
-                                         int last_key) {
-  const int i0 = key0 >> p.page_shift;
-  const int i1 = min(key0 + KT - 1, last_key) >> p.page_shift;
-  bool bad = false;
-  for (int i = i0; i <= i1; ++i)
-    bad |= (unsigned)load_uniform(table + i) >= (unsigned)p.num_pages;
-  return bad;
-}
-
 #endif  // __HIP_DEVICE_COMPILE__
 
 template <typename A, int D, bool F8, int NW>
@@ -278,22 +266,34 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prefill(Pref
   // Tile i0 + j lies in buffer j % BUFS. While tile j is worked on, tile j + STEP is loaded;
   // it goes to a buffer that was last read before the last barrier.
   int flags = 0;  // bits 2 (j % BUFS), + 1: tile j is bad, an edge tile
-  auto note = [&](int j, int key0) {
-    const bool bad_tile = bad_page<KT>(p, table, key0, last_key);
+  auto note = [&](int j, int key0, int pages) {
+    const bool bad_tile =
+        __builtin_amdgcn_ballot_w64((unsigned)pages >= (unsigned)p.num_pages) != 0;
     const bool edge_tile = is_edge(bad_tile, key0);
     const int at = 2 * (j & (BUFS - 1));
     flags = (flags & ~(3 << at)) | (bad_tile ? 1 << at : 0) | (edge_tile ? 2 << at : 0);
     return edge_tile;
   };
+  // The tile's page numbers up to the last key that any row sees, one a lane. (Scalar loads
+  // would share their counter with the LDS reads and wait for both.)
+  auto tile_pages = [&](int j) {
+    const int first = t.keys.tile(min(i0 + j, i1 - 1)) * KT >> p.page_shift;
+    return table[min(first + min(lane, (KT - 1) >> p.page_shift), last_key >> p.page_shift)];
+  };
   const int count = i1 - i0;
-  if (count > 0) st.ids(p, table, t.keys.tile(i0) * KT, tid);
+  int pages = 0;  // of the next tile to load
+  if (count > 0) {
+    st.ids(p, table, t.keys.tile(i0) * KT, tid);
+    pages = tile_pages(0);
+  }
 #pragma unroll
   for (int j = 0; j < STEP; ++j) {
     if (j >= count) continue;
     const int key0 = t.keys.tile(i0 + j) * KT;
     st.load(p, kvh, key0, tid);
     if (j + 1 < count) st.ids(p, table, t.keys.tile(i0 + j + 1) * KT, tid);
-    const bool edge_tile = note(j, key0);
+    const bool edge_tile = note(j, key0, pages);
+    pages = tile_pages(j + 1);
     stage_store(j, edge_tile);
   }
   lds_barrier();
@@ -307,7 +307,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prefill(Pref
     if (more) {
       const int k1 = t.keys.tile(i0 + j + STEP) * KT;
       st.load(p, kvh, k1, tid);
-      edge_next = note(j + STEP, k1);
+      edge_next = note(j + STEP, k1, pages);
+      pages = tile_pages(j + STEP + 1);
       if (j + STEP + 1 < count) st.ids(p, table, t.keys.tile(i0 + j + STEP + 1) * KT, tid);
     }
     const bool sees = any && key0 <= pos_max &&
