@@ -329,7 +329,8 @@ typedef struct {
  *   pair i < rot_dim/2, a = position * inv_freq[i] (product and reduction in binary64):
  *   (y_p, y_q) -> (y_p cos a - y_q sin a, y_q cos a + y_p sin a), with p = i,
  *   q = i + rot_dim/2, or, interleaved, p = 2i, q = 2i + 1; elements from rot_dim on keep
- *   y. rot_dim: 0 (no rotation) or a multiple of 16 up to head_dim. */
+ *   y. rot_dim: 0 (no rotation) or a multiple of 16 up to head_dim. eps in 0..1,
+ *   weight_offset in -16..16. */
 typedef struct {
   const float* q_norm;   /* device fp32 [head_dim] or NULL                              */
   const float* k_norm;   /* device fp32 [head_dim] or NULL                              */

@@ -38,7 +38,7 @@ struct DecodeParams {
   float scale;     // times log2(e)
   KeyMask mask;
   int num_pages, page_shift, kv_heads, max_pages;
-  int group, T, splits, row_tiles;
+  int group, T, splits, fill, row_tiles;
 };
 
 // The key tiles of one sequence and how they are dealt to the splits: `per` tiles to each,
@@ -53,7 +53,11 @@ __device__ __forceinline__ SeqSplit seq_split(const DecodeParams& p, int seq) {
   const long long cap = (long long)p.max_pages << p.page_shift;
   s.len = (int)max(0ll, min((long long)p.kv_lens[seq], cap));
   s.tiles = visible_tiles<kTile>(p.mask, s.len - p.T, s.len - 1);
-  s.per = max(kMinSplitTiles, (s.tiles.count + p.splits - 1) / p.splits);
+  // as many even parts as fill the card, or as cut a long sequence; the table may be far wider
+  // than this one is long
+  const int parts = max(p.fill, (s.tiles.count + kLongSplitTiles - 1) / kLongSplitTiles);
+  const int most = min(parts, p.splits);
+  s.per = max(kMinSplitTiles, (s.tiles.count + most - 1) / most);
   s.live = (s.tiles.count + s.per - 1) / s.per;
   return s;
 }
@@ -170,9 +174,11 @@ __global__ __launch_bounds__(KW * kWave, decode_waves(NT, D)) void k_attn_decode
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int n16 = lane & 15, g = lane >> 4;
-  const int split = blockIdx.x;
-  const int kvh = blockIdx.y / p.row_tiles, rt = blockIdx.y % p.row_tiles;
-  const int seq = blockIdx.z;
+  // Splits outermost: a sequence's live splits are the first ones, and workgroups go to the 8
+  // XCDs in turn (64 sequences of 8192 keys with a page table 32 times as wide: 90 us; with
+  // the splits innermost, where the live ones share few XCDs, 449).
+  const int kvh = blockIdx.x / p.row_tiles, rt = blockIdx.x % p.row_tiles;
+  const int seq = blockIdx.y, split = blockIdx.z;
   const SeqSplit sp = seq_split(p, seq);
   const bool direct = sp.live <= 1;
   if (split >= sp.live && !(direct && split == 0)) return;
@@ -444,7 +450,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_attn_decode_join(DecodeParams 
 
 template <typename A, int D, bool F8, int NT, int KW = 4>
 hipError_t launch_one(const DecodeParams& p, int n_seqs, hipStream_t stream) {
-  k_attn_decode<A, D, F8, NT, KW><<<dim3(p.splits, p.kv_heads * p.row_tiles, n_seqs),
+  k_attn_decode<A, D, F8, NT, KW><<<dim3(p.kv_heads * p.row_tiles, n_seqs, p.splits),
                                     dim3(KW * kWave), 0, stream>>>(p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
@@ -506,6 +512,7 @@ hipError_t launch_attn_decode(const AttnArgs& a, const AttnPlan& plan) {
   p.group = a.q.heads / a.cache.kv_heads;
   p.T = a.window_tokens;
   p.splits = plan.splits;
+  p.fill = plan.fill;
   p.row_tiles = plan.row_tiles;
   return a.dtype == MOE_BF16
              ? launch_type<Bf16>(p, a.cache.head_dim, a.cache.dtype == MOE_E4M3,

@@ -251,6 +251,7 @@ struct AttnArgs {
 struct AttnPlan {
   int row_tiles;  // row tiles of one kv head (decode: per sequence; prefill: upper bound)
   int splits;
+  int fill;       // decode: splits of each sequence that fill the card
   int tile_rows;
   size_t partial, stats, total;  // workspace offsets and size
 };

@@ -13,6 +13,9 @@ constexpr int kTile = 32;  // keys of one step of a wave
 // more than it saves.
 constexpr int kUnsplitTiles = 32;
 constexpr int kMinSplitTiles = 8;
+// Sequences that fill the card anyway are cut at 4096 keys, so that long ones share out (64
+// sequences of 1 to 32768 keys at 8 bits: 367 us, cut at 8192 keys 386).
+constexpr int kLongSplitTiles = 128;
 
 // Row tiles (of 16 query rows) a wave takes: as many as the window has, while accumulators
 // (D/4 registers a row tile) fit beside a tile's keys and values (D/2 at 16 bits). More row
@@ -43,9 +46,10 @@ inline AttnPlan decode_plan(int q_heads, int kv_heads, int D, int n_seqs, int wi
   // workgroups that run at once: two a CU, one where a wave takes many more than 256 registers
   const long long at_once = (wave_tiles * D >= 512 ? 1 : 2) * num_cus;
   const long long fill = (at_once + base - 1) / base;
-  const long long even = (tiles + 63) / 64;  // 2048 keys, so that long sequences share out
+  const long long even = (tiles + kLongSplitTiles - 1) / kLongSplitTiles;
   const long long most = tiles <= kUnsplitTiles ? 1 : std::max(1ll, tiles / kMinSplitTiles);
   plan.splits = (int)std::min<long long>({std::max(fill, even), most, kMaxSplits});
+  plan.fill = (int)std::min<long long>(fill, kMaxSplits);
   if (plan.splits > 1) {
     const size_t parts = (size_t)n_seqs * window_tokens * q_heads * plan.splits;
     plan.partial = 0;
