@@ -26,12 +26,20 @@ constexpr float kNegInf = -__builtin_huge_valf();
 
 // 16-bit activation types: 8-element vectors, the matrix-core products and the expansion of
 // e4m3 codes (exact in either type).
+//
+// A row's probabilities are 2^(score - reference + kBias), where the reference moves to the
+// row's maximum only when that exceeds it by more than kLazy: sums are rescaled seldom. The
+// factor 2^kBias is in numerator and denominator alike. bf16 has the exponents of fp32 and
+// needs none. fp16 ends at 2^16 and has steps of 2^-24 below 2^-14: with probabilities up to
+// 2^15, and 2^11 for the reference itself, what is lost of a small one is at most 2^-36 of the
+// largest (without the factor 2^-25: a tail of 40000 keys at 2^-25 each vanished).
 struct Bf16 {
   typedef __bf16 T;
   typedef bf16x8 V8;
   typedef bf16x4 V4;
   typedef bf16x2 V2;
   static constexpr uint32_t kExpMask = 0x7f80u, kOne = 0x3f80u;
+  static constexpr float kLazy = 8.0f, kBias = 0.0f;
 #if defined(__HIP_DEVICE_COMPILE__)
   static __device__ __forceinline__ f32x4 mfma16(V8 a, V8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -52,6 +60,7 @@ struct F16 {
   typedef f16x4 V4;
   typedef f16x2 V2;
   static constexpr uint32_t kExpMask = 0x7c00u, kOne = 0x3c00u;
+  static constexpr float kLazy = 4.0f, kBias = 11.0f;
 #if defined(__HIP_DEVICE_COMPILE__)
   static __device__ __forceinline__ f32x4 mfma16(V8 a, V8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);

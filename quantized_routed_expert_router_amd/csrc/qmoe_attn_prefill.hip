@@ -12,8 +12,10 @@
 // The key rows of a 32-key half are dealt to the first product's rows (bits 2 and 3
 // exchanged) so that its accumulators 8u..8u+7 of a lane are 8 consecutive keys, which is
 // the second product's B operand: probabilities never leave the lane. Statistics and sums
-// are fp32; probabilities are rounded to the 16-bit type for the matrix cores (their
-// relative error, 2^-9 in bf16, is that of the output's own rounding).
+// are fp32; probabilities are rounded to the 16-bit type for the matrix cores (in bf16 by up
+// to 2^-8 of each, in fp16 by 2^-11, or 2^-36 of the row's largest where that is more: the
+// output's own rounding is as large; a second part as in decode would double the products of
+// a loop that they bound).
 #include <type_traits>
 
 #include "qmoe_attn_plan.h"
@@ -22,9 +24,6 @@ namespace qmoe {
 namespace {
 
 [[maybe_unused]] constexpr int kTileElems = 8192;  // keys x columns of one LDS tile: 16 KB each of keys and values
-// A row's reference maximum moves only when the new maximum exceeds it by this many powers
-// of two; probabilities then reach 2^8, which fp32 sums and both 16-bit types hold.
-[[maybe_unused]] constexpr float kLazy = 8.0f;
 
 struct PrefillParams {
   HeadView q;
@@ -347,7 +346,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prefill(Pref
 #pragma unroll
         for (int r = 0; r < 16; ++r) top = fmaxf(top, s[x][r]);
       top = fmaxf(top, __shfl_xor(top, 32)) * sc.scale;
-      const bool moves = top > m + kLazy;
+      const bool moves = top > m + A::kLazy;
       if (__builtin_amdgcn_ballot_w64(moves) != 0) {
         const float now = moves ? top : m;
         const float a = rescale(m - (now == kNegInf ? 0.0f : now));
@@ -356,7 +355,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prefill(Pref
         for (int dt = 0; dt < DT; ++dt) o[dt] *= a;
         m = now;
       }
-      const float base = m == kNegInf ? 0.0f : -m;
+      const float base = m == kNegInf ? 0.0f : A::kBias - m;
       V8 pr[2 * HALVES];
 #pragma unroll
       for (int x = 0; x < HALVES; ++x) {
