@@ -10,18 +10,15 @@
 // 8g..8g+7: the probabilities leave the first product where the second takes them, and
 // nothing goes through LDS until the waves' sums are joined. Softmax statistics and sums
 // are fp32; the probabilities enter the second product as a 16-bit value plus the 16-bit
-// rest (2^-16 relative and better), which costs matrix-core time that the memory-bound
-// loop has to spare.
+// rest, which costs matrix-core time that the memory-bound loop has to spare. What the two
+// parts leave of a probability: 2^-16 of it in bf16; in fp16 2^-22 of it, or 2^-36 of the
+// largest one that the wave has seen in the row, where that is more.
 #include <type_traits>
 
 #include "qmoe_attn_plan.h"
 
 namespace qmoe {
 namespace {
-
-// A row's reference maximum moves only when the new maximum exceeds it by this many powers
-// of two; probabilities then reach 2^8, which fp32 sums and both 16-bit types hold.
-[[maybe_unused]] constexpr float kLazy = 8.0f;
 
 struct DecodeParams {
   HeadView q;
@@ -306,7 +303,7 @@ __global__ __launch_bounds__(KW * kWave, decode_waves(NT, D)) void k_attn_decode
                           fmaxf(fmaxf(s[nt][1][0], s[nt][1][1]), fmaxf(s[nt][1][2], s[nt][1][3])));
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32)) * sc.scale;
-        const bool moves = top > m[nt] + kLazy;
+        const bool moves = top > m[nt] + A::kLazy;
         if (__builtin_amdgcn_ballot_w64(moves) != 0) {
           const float now = moves ? top : m[nt];
           const float a = rescale(m[nt] - (now == kNegInf ? 0.0f : now));
@@ -315,7 +312,7 @@ __global__ __launch_bounds__(KW * kWave, decode_waves(NT, D)) void k_attn_decode
           for (int dt = 0; dt < DT; ++dt) o[nt][dt] *= a;
           m[nt] = now;
         }
-        const float base = m[nt] == kNegInf ? 0.0f : -m[nt];
+        const float base = m[nt] == kNegInf ? 0.0f : A::kBias - m[nt];
         f32x8 pr;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {

@@ -103,3 +103,15 @@ def test_prefill_tail_behind_a_first_key(D, gap):
     got = att.attn_prefill(c.cache, c.q, torch.tensor([0, n], dtype=torch.int32).cuda(), c.table,
                            torch.tensor([L], dtype=torch.int32).cuda(), scale=1.0)
     c.check(got, [0, 777, n - 1], 2.0 ** -11, f"prefill, gap {gap}")
+
+
+@pytest.mark.parametrize("gap", [8, 14, 17, 18])
+@pytest.mark.parametrize("D,hq,hkv,n,L,cdtype", [
+    (64, 8, 2, 1, 700, HF), (64, 40, 1, 2, 700, HF), (128, 4, 2, 4, 900, HF), (256, 8, 1, 5, 700, HF),
+    (128, 16, 1, 4, 900, E4), (128, 8, 2, 2, 9000, HF),  # the last one with joined splits
+])
+def test_decode_tail(D, hq, hkv, n, L, cdtype, gap):
+    c = Tail(n, L, hq, hkv, D, gap, 32, cdtype)
+    got = att.attn_decode(c.cache, c.q, c.table, torch.tensor([L], dtype=torch.int32).cuda(),
+                          scale=1.0)
+    c.check(got, range(n), 2.0 ** -22, f"decode, gap {gap}")
