@@ -417,11 +417,15 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prefill(Pref
   }
 
   l += __shfl_xor(l, 32);
-  if (!real) return;
-  const long long at = (long long)token * hq + head;
-  if (direct) {
-    const float vs = p.v_scale ? p.v_scale[kvh] : 1.0f;
-    const float inv = l == 0.0f ? 0.0f : vs / l;
+  float zero = 0.0f;  // NaN where a sum is not finite
+#pragma unroll
+  for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) zero = __builtin_fmaf(o[dt][r], 0.0f, zero);
+  const long long at = (long long)token * hq + head, part = at * p.splits + split;
+  const float vs = p.v_scale ? p.v_scale[kvh] : 1.0f;
+  const float inv = l == 0.0f ? 0.0f : vs / l;
+  if (real && direct) {
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
@@ -432,8 +436,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prefill(Pref
         *reinterpret_cast<u32x2*>(p.out + 2 * (at * D + 32 * dt + 8 * r4 + 4 * h)) =
             bits_as<u32x2>(__builtin_convertvector(y, typename A::V4));
       }
-  } else {
-    const long long part = at * p.splits + split;
+  } else if (real) {
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
@@ -444,6 +447,55 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prefill(Pref
         *reinterpret_cast<f32x4*>(p.partial + part * D + 32 * dt + 8 * r4 + 4 * h) = y;
       }
     if (h == 0) p.stats[part] = make_float2(m, l);
+  }
+  if (__builtin_amdgcn_ballot_w64(real && !(zero == 0.0f)) == 0) return;
+
+  // A value that is not finite takes every row that sees it. But where the 16-bit type holds
+  // its key's probability as 0, the products above made NaN of an infinity. So a wave with
+  // such sums goes through its values once more, without scores, and writes the columns of
+  // the rows that see one again.
+#pragma unroll 1
+  for (int dt = 0; dt < DT; ++dt) {
+    f32x16 c[3];  // counts of each kind
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) c[i][r] = 0.0f;
+#pragma unroll 1
+    for (int j = 0; j < count * 2 * HALVES; ++j) {
+      const int from = t.keys.tile(i0 + j / (2 * HALVES)) * KT + 16 * (j % (2 * HALVES)) + 8 * h;
+      const int id = st.page_of(p, table, from);
+      uint32_t seen = 0;
+      if ((unsigned)id < (unsigned)p.num_pages) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) seen |= (uint32_t)key_visible(p.mask, from + k, pos) << k;
+      }
+      const long long word = st.row_of(p, id, kvh, from) * D + 8 * n32 + 256 * dt;
+      V8 a;
+      if constexpr (F8) {
+        const u32x2 w = *reinterpret_cast<const u32x2*>(p.cv + word);
+        a = expand_e4m3<A>(w[0], w[1]);
+      } else {
+        a = *reinterpret_cast<const V8*>(p.cv + 2 * word);
+      }
+      const V8 rows_seen = mask_elements<A>(seen);
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        c[i] = A::mfma32(non_finite<A>(a, non_finite_kind<A>(i)), rows_seen, c[i]);
+    }
+    if (!real) continue;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      float y = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) y += spread(c[i][r], non_finite_kind<A>(i));
+      if (y == 0.0f) continue;
+      const int col = 32 * dt + 8 * (r >> 2) + 4 * h + (r & 3);
+      if (direct)
+        reinterpret_cast<typename A::T*>(p.out)[at * D + col] = (typename A::T)(y * inv);
+      else
+        p.partial[part * D + col] = y;
+    }
   }
 #endif
 }
