@@ -135,15 +135,6 @@ moe_status check_attn(const moe_attn* a) {
   return MOE_OK;
 }
 
-// A window of 2^30 keys or more only ever hides keys that lie 2^30 back; it is cut there
-// so that position - window cannot wrap around.
-moe_attn bounded(const moe_attn& a) {
-  moe_attn b = a;
-  b.window = std::min(b.window, 1 << 30);
-  b.sinks = std::min(b.sinks, 1 << 30);
-  return b;
-}
-
 // Sizes that the workspace depends on.
 bool sizes_ok(const moe_kv_cache* cache, int q_heads, int n_seqs, int max_pages,
               const moe_attn* a) {
@@ -156,13 +147,13 @@ bool sizes_ok(const moe_kv_cache* cache, int q_heads, int n_seqs, int max_pages,
 AttnPlan plan_decode(const moe_kv_cache* c, int q_heads, int n_seqs, int t, int max_pages,
                      const moe_attn* a) {
   return decode_plan(q_heads, c->kv_heads, c->head_dim, n_seqs, t, max_pages, c->page_size,
-                     bounded(*a), device_cu_count());
+                     *a, device_cu_count());
 }
 
 AttnPlan plan_prefill(const moe_kv_cache* c, int q_heads, int n_seqs, int n, int max_pages,
                       const moe_attn* a) {
   return prefill_plan(q_heads, c->kv_heads, c->head_dim, n_seqs, n, max_pages, c->page_size,
-                      bounded(*a), device_cu_count());
+                      *a, device_cu_count());
 }
 
 // The checks that decode and prefill share, for n tokens (n > 0) and a workspace of need
@@ -331,7 +322,7 @@ moe_status moe_attn_decode(const moe_kv_cache* cache, const moe_heads* q, int dt
       plan_decode(cache, q->heads, pages->n_seqs, window_tokens, pages->max_pages, a);
   s = check_attention(cache, q, dtype, n, pages, out, ws, ws_bytes, plan.total, nullptr);
   if (s != MOE_OK) return s;
-  const AttnArgs args{view(q), dtype, *cache,     *pages,     bounded(*a), nullptr,
+  const AttnArgs args{view(q), dtype, *cache,     *pages,     *a, nullptr,
                       n,       window_tokens, (char*)out, (char*)ws,   (hipStream_t)stream};
   return launch_attn_decode(args, plan) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
@@ -356,7 +347,7 @@ moe_status moe_attn_prefill(const moe_kv_cache* cache, const moe_heads* q, int d
       plan_prefill(cache, q->heads, pages->n_seqs, n_tokens, pages->max_pages, a);
   s = check_attention(cache, q, dtype, n_tokens, pages, out, ws, ws_bytes, plan.total, q_starts);
   if (s != MOE_OK) return s;
-  const AttnArgs args{view(q),  dtype, *cache,     *pages,   bounded(*a),        q_starts,
+  const AttnArgs args{view(q),  dtype, *cache,     *pages,   *a,        q_starts,
                       n_tokens, 0,     (char*)out, (char*)ws, (hipStream_t)stream};
   return launch_attn_prefill(args, plan) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }

@@ -281,7 +281,7 @@ __global__ __launch_bounds__(KW * kWave, decode_waves(NT, D)) void k_attn_decode
 
       // all keys of the tile visible to all of the window's rows?
       const bool full = !careful && (page0 | page1) >= 0 && key0 + kTile - 1 <= first_pos &&
-                        (p.mask.window == 0 || key0 > sp.len - 1 - p.mask.window ||
+                        (p.mask.window == 0 || key0 > behind_window(p.mask, sp.len - 1) ||
                          key0 + kTile - 1 < p.mask.sinks);
       bool dirty = false;  // not full, with non-finite values somewhere
       const bool on_page = (g & 2 ? page1 : page0) >= 0;

@@ -275,8 +275,14 @@ struct KeyMask {
   int window, sinks;
 };
 
+// The last key behind the window of a query at pos. Windows go up to 2^31-1, and a position
+// may be negative (it sees no key at all), so it is held at 0 to keep the difference in range.
+__device__ __forceinline__ int behind_window(const KeyMask& m, int pos) {
+  return max(pos, 0) - m.window;
+}
+
 __device__ __forceinline__ bool key_visible(const KeyMask& m, int key, int pos) {
-  return key <= pos && (m.window == 0 || key > pos - m.window || key < m.sinks);
+  return key <= pos && (m.window == 0 || key > behind_window(m, pos) || key < m.sinks);
 }
 
 // The key tiles (of TILE keys) that queries at positions first..last can see: sink tiles
@@ -294,7 +300,7 @@ __device__ __forceinline__ TileList visible_tiles(const KeyMask& m, int first, i
     return t;
   }
   const int hi = last / TILE + 1;
-  const int from = m.window == 0 ? 0 : max(0, first - m.window + 1);
+  const int from = m.window == 0 ? 0 : max(0, behind_window(m, first) + 1);
   t.lo = from / TILE;
   t.ns = m.window == 0 ? 0 : min((int)(((long long)m.sinks + TILE - 1) / TILE), t.lo);
   t.count = t.ns + (hi - t.lo);

@@ -256,7 +256,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prefill(Pref
   // An edge tile: not all of the workgroup's rows see all of it.
   auto is_edge = [&](bool bad_tile, int key0) {
     return bad_tile || key0 + KT - 1 > first_key ||
-           (p.mask.window != 0 && key0 <= last_key - p.mask.window &&
+           (p.mask.window != 0 && key0 <= behind_window(p.mask, last_key) &&
             key0 + KT - 1 >= p.mask.sinks);
   };
   auto stage_store = [&](int buf, bool edge_tile) {
@@ -315,7 +315,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prefill(Pref
       if (j + STEP + 1 < count) st.ids(p, table, t.keys.tile(i0 + j + STEP + 1) * KT, tid);
     }
     const bool sees = any && key0 <= pos_max &&
-                      (p.mask.window == 0 || key0 + KT - 1 > pos_min - p.mask.window ||
+                      (p.mask.window == 0 || key0 + KT - 1 > behind_window(p.mask, pos_min) ||
                        key0 < p.mask.sinks);
     if (sees) {
       f32x16 s[HALVES];
@@ -333,7 +333,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prefill(Pref
       }
       // accumulator r of half x is key 32 x + 16 (r / 8) + 8 h + r % 8
       if (edge && (bad || key0 + KT - 1 > pos_min ||
-                   (p.mask.window != 0 && key0 <= pos_max - p.mask.window))) {
+                   (p.mask.window != 0 && key0 <= behind_window(p.mask, pos_max)))) {
 #pragma unroll
         for (int x = 0; x < HALVES; ++x)
 #pragma unroll
