@@ -365,7 +365,8 @@ typedef struct {
 /* Norm and rotation of the query and key heads of n_tokens tokens, one pass, out of place
  * or in place. q, k: input heads (either may have data == NULL); q_out, k_out: their
  * outputs, same head counts, heads that do not overlap each other. An output may be its
- * own input (same data and strides); any other overlap is rejected. dtype: MOE_BF16 or
+ * own input (same data and strides); any other overlap with what the call reads (rows,
+ * positions, weights, frequencies) is rejected. dtype: MOE_BF16 or
  * MOE_F16. positions: device int32 [n_tokens] (may be NULL when rot_dim == 0).
  * n_tokens <= MOE_MAX_PREFILL_TOKENS. */
 moe_status moe_qk_norm_rope(const moe_heads* q, const moe_heads* k, const int32_t* positions,
@@ -377,8 +378,10 @@ moe_status moe_qk_norm_rope(const moe_heads* q, const moe_heads* k, const int32_
  * the slot of each token; a slot outside the cache (negative for padding) stores nothing.
  * Slots inside the cache must differ from each other (of two equal ones, either token's
  * elements may stay). q (NULL or data == NULL: none): query heads normed and rotated into
- * q_out in the same launch, for every token. All other cache rows keep their contents. dtype is that of q,
- * k and v; a 16-bit cache has the same. n_tokens <= MOE_MAX_PREFILL_TOKENS. */
+ * q_out in the same launch, for every token. All other cache rows keep their contents. q_out
+ * may be q; any other overlap of the cache or q_out with what the call reads (slots and scales
+ * too) is rejected. dtype is that of q, k and v; a 16-bit cache has the same.
+ * n_tokens <= MOE_MAX_PREFILL_TOKENS. */
 moe_status moe_kv_append(const moe_kv_cache* cache, const moe_heads* k, const moe_heads* v,
                          const int32_t* slots, const int32_t* positions, int n_tokens,
                          int dtype, const moe_norm_rope* p, const moe_heads* q,

@@ -111,6 +111,16 @@ moe_status check_norm_rope(const moe_norm_rope* p, int D, const int32_t* positio
   return MOE_OK;
 }
 
+// Whether a written range holds nothing that norm and rotation read beside the rows.
+bool apart_from_parameters(const Range& written, const moe_norm_rope& p, int D,
+                           const int32_t* positions, int n) {
+  const size_t row = 4 * (size_t)D;
+  return disjoint(written, range(positions, positions ? 4 * (size_t)n : 0)) &&
+         disjoint(written, range(p.q_norm, p.q_norm ? row : 0)) &&
+         disjoint(written, range(p.k_norm, p.k_norm ? row : 0)) &&
+         disjoint(written, range(p.inv_freq, 2 * (size_t)p.rot_dim));
+}
+
 HeadView view(const moe_heads* h) {
   if (!has(h)) return HeadView{nullptr, 0, 0, 0};
   return HeadView{(char*)h->data, h->token_stride, h->head_stride, h->heads};
@@ -231,6 +241,9 @@ moe_status moe_qk_norm_rope(const moe_heads* q, const moe_heads* k, const int32_
         !views_apart(*k_out, *q, n, D))
       return MOE_ERR_INVALID_ARGUMENT;
   }
+  if ((has(q) && !apart_from_parameters(range(*q_out, n, D), *p, D, positions, n)) ||
+      (has(k) && !apart_from_parameters(range(*k_out, n, D), *p, D, positions, n)))
+    return MOE_ERR_INVALID_ARGUMENT;
   if (!has(q) && !has(k)) return MOE_OK;
   RowsArgs a{};
   a.q = view(q);
@@ -273,13 +286,17 @@ moe_status moe_kv_append(const moe_kv_cache* cache, const moe_heads* k, const mo
   if (s != MOE_OK) return s;
   // no input of the call lies in what it writes
   const Range kc = k_range(cache), vc = v_range(cache);
-  const Range inputs[] = {range(*k, n, D), range(*v, n, D), range(slots, 4 * (size_t)n),
-                          range(positions, positions ? 4 * (size_t)n : 0),
-                          has(q) ? range(*q, n, D) : Range{0, 0},
-                          has(q) ? range(*q_out, n, D) : Range{0, 0}};
-  if (!disjoint(kc, vc)) return MOE_ERR_INVALID_ARGUMENT;
+  const Range qo = has(q) ? range(*q_out, n, D) : Range{0, 0};
+  const Range inputs[] = {range(*k, n, D), range(*v, n, D), has(q) ? range(*q, n, D) : Range{0, 0}};
+  const Range kscale = range(cache->k_scale, cache->k_scale ? 4 * (size_t)cache->kv_heads : 0);
+  const Range vscale = range(cache->v_scale, cache->v_scale ? 4 * (size_t)cache->kv_heads : 0);
+  if (!disjoint(kc, vc) || !disjoint(kc, qo) || !disjoint(vc, qo)) return MOE_ERR_INVALID_ARGUMENT;
   for (const Range& in : inputs)
     if (!disjoint(kc, in) || !disjoint(vc, in)) return MOE_ERR_INVALID_ARGUMENT;
+  for (const Range& out : {kc, vc, qo})
+    if (!disjoint(out, range(slots, 4 * (size_t)n)) || !disjoint(out, kscale) ||
+        !disjoint(out, vscale) || !apart_from_parameters(out, *p, D, positions, n))
+      return MOE_ERR_INVALID_ARGUMENT;
   if (has(q) && (!views_apart(*q_out, *k, n, D) || !views_apart(*q_out, *v, n, D)))
     return MOE_ERR_INVALID_ARGUMENT;
   RowsArgs a{};
