@@ -7,6 +7,7 @@
 // not MOE_OK, and the outputs otherwise.
 #include <Python.h>
 
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
@@ -151,8 +152,10 @@ moe_heads dense(const Tensor& t) {
   return moe_heads{t.data_ptr(), t.size(1) * t.size(2), t.size(2), (int32_t)t.size(1)};
 }
 
+// Errors of torch (an allocation that fails) become the exceptions that torch's own calls raise.
 template <typename F>
 PyObject* guarded(PyObject* const* args, Py_ssize_t n, F body) {
+  HANDLE_TH_ERRORS
   try {
     const long device = n > 0 ? PyLong_AsLong(args[0]) : -1;
     if (PyErr_Occurred()) PyErr_Clear();
@@ -161,10 +164,8 @@ PyObject* guarded(PyObject* const* args, Py_ssize_t n, F body) {
     return body(a);
   } catch (const Mismatch&) {
     Py_RETURN_NONE;
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
-    return nullptr;
   }
+  END_HANDLE_TH_ERRORS
 }
 
 // (device, q, k, positions, q_norm, k_norm, inv_freq, eps, weight_offset, interleaved, stream)

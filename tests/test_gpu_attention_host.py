@@ -1,0 +1,43 @@
+"""What a call of the attention half does to the Python program around it: the error of an
+allocation that fails."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from quantized_routed_expert_router_amd import attention as att
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32).cuda()
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_out_of_memory_is_torchs_error(given):
+    # with and without an output given: the two marshalling paths
+    n, heads, D = 8192, 64, 128
+    q = torch.zeros((n, heads, D), dtype=BF, device="cuda")
+    k = torch.zeros((n, 1, D), dtype=BF, device="cuda")
+    cache = att.KVCache.empty(1, 1, 16, D)
+    slots, p = torch.full((n,), -1, dtype=torch.int32, device="cuda"), att.NormRope()
+    k_out = torch.empty_like(k)
+    table, lens, starts = _i32([[0]]), _i32([16]), _i32([0, 16])
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    room = torch.cuda.memory_reserved() + (32 << 20)
+    torch.cuda.set_per_process_memory_fraction(room / torch.cuda.get_device_properties(0).total_memory)
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            att.qk_norm_rope(q, k, None, p, k_out=k_out if given else None)
+        with pytest.raises(torch.OutOfMemoryError):
+            att.attn_prefill(cache, q, starts, table, lens, ws=ws if given else None)
+        if not given:
+            with pytest.raises(torch.OutOfMemoryError):
+                att.kv_append(cache, k, k, slots, None, p, q=q)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
