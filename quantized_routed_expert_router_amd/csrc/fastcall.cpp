@@ -144,6 +144,19 @@ moe_norm_rope norm_rope_of(Args& a, int64_t D) {
   return p;
 }
 
+// Other Python threads run meanwhile: an allocation may have to wait for the device, a launch
+// for room in the stream's queue. Held around everything from the first allocation to the
+// launch; no Python object is made or read inside.
+class WithoutGil {
+ public:
+  WithoutGil() : state_(PyEval_SaveThread()) {}
+  ~WithoutGil() { PyEval_RestoreThread(state_); }
+  WithoutGil(const WithoutGil&) = delete;
+
+ private:
+  PyThreadState* state_;
+};
+
 Tensor new_like(const Tensor& t) {
   return at::empty(t.sizes(), t.options(), at::MemoryFormat::Contiguous);
 }
@@ -177,10 +190,16 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const int32_t* positions = (const int32_t*)a.vector(at::kInt, q.size(0));
     const moe_norm_rope p = norm_rope_of(a, q.size(2));
     void* stream = a.stream();
-    Tensor qo = new_like(q), ko = new_like(k);
-    const moe_heads qos = dense(qo), kos = dense(ko);
-    const moe_status s = moe_qk_norm_rope(&qs, &ks, positions, (int)q.size(0), dtype_of(q),
-                                          (int)q.size(2), &p, &qos, &kos, stream);
+    Tensor qo, ko;
+    moe_status s;
+    {
+      const WithoutGil free;
+      qo = new_like(q);
+      ko = new_like(k);
+      const moe_heads qos = dense(qo), kos = dense(ko);
+      s = moe_qk_norm_rope(&qs, &ks, positions, (int)q.size(0), dtype_of(q), (int)q.size(2), &p,
+                           &qos, &kos, stream);
+    }
     if (s != MOE_OK) return PyLong_FromLong(s);
     PyObject* pair = PyTuple_New(2);
     if (!pair) return nullptr;
@@ -205,10 +224,15 @@ PyObject* kv_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const Tensor& q = a.required();
     const moe_heads qs = heads_of(q, &k, false);
     void* stream = a.stream();
-    Tensor qo = new_like(q);
-    const moe_heads qos = dense(qo);
-    const moe_status s = moe_kv_append(&c, &ks, &vs, slots, positions, (int)k.size(0), dtype_of(k),
-                                       &p, &qs, &qos, stream);
+    Tensor qo;
+    moe_status s;
+    {
+      const WithoutGil free;
+      qo = new_like(q);
+      const moe_heads qos = dense(qo);
+      s = moe_kv_append(&c, &ks, &vs, slots, positions, (int)k.size(0), dtype_of(k), &p, &qs, &qos,
+                        stream);
+    }
     if (s != MOE_OK) return PyLong_FromLong(s);
     return THPVariable_Wrap(std::move(qo));
   });
@@ -245,14 +269,19 @@ PyObject* attend(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const size_t need =
         starts ? moe_attn_prefill_workspace_bytes(&c, heads, b, tokens, pages.max_pages, &p)
                : moe_attn_decode_workspace_bytes(&c, heads, b, tokens / b, pages.max_pages, &p);
-    Tensor out = new_like(q), ws;
-    if (need) ws = at::empty({(int64_t)need}, q.options().dtype(at::kByte));
-    void* room = need ? ws.data_ptr() : nullptr;
-    const moe_status s =
-        starts ? moe_attn_prefill(&c, &qs, dtype_of(q), (const int32_t*)starts->data_ptr(), tokens,
-                                  &pages, &p, out.data_ptr(), room, need, stream)
-               : moe_attn_decode(&c, &qs, dtype_of(q), &pages, tokens / b, &p, out.data_ptr(),
-                                 room, need, stream);
+    Tensor out;
+    moe_status s;
+    {
+      const WithoutGil free;
+      Tensor ws;
+      out = new_like(q);
+      if (need) ws = at::empty({(int64_t)need}, q.options().dtype(at::kByte));
+      void* room = need ? ws.data_ptr() : nullptr;
+      s = starts ? moe_attn_prefill(&c, &qs, dtype_of(q), (const int32_t*)starts->data_ptr(),
+                                    tokens, &pages, &p, out.data_ptr(), room, need, stream)
+                 : moe_attn_decode(&c, &qs, dtype_of(q), &pages, tokens / b, &p, out.data_ptr(),
+                                   room, need, stream);
+    }
     if (s != MOE_OK) return PyLong_FromLong(s);
     return THPVariable_Wrap(std::move(out));
   });

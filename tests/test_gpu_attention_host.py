@@ -1,6 +1,9 @@
 """What a call of the attention half does to the Python program around it: the error of an
-allocation that fails."""
+allocation that fails, and other threads while a launch waits for room in the stream's queue."""
 from __future__ import annotations
+
+import threading
+import time
 
 import pytest
 import torch
@@ -41,3 +44,48 @@ def test_out_of_memory_is_torchs_error(given):
                 att.kv_append(cache, k, k, slots, None, p, q=q)
     finally:
         torch.cuda.set_per_process_memory_fraction(1.0)
+
+
+def test_other_threads_run_while_a_launch_waits():
+    # more calls than a stream's queue holds, behind a spin: the launch waits for room, and
+    # another thread goes on meanwhile
+    cache = att.KVCache.empty(1, 1, 16, 64)
+    q = torch.zeros((1, 1, 64), dtype=BF, device="cuda")
+    k = torch.zeros((1, 1, 64), dtype=BF, device="cuda")
+    table, lens, slots, p = _i32([[0]]), _i32([4]), _i32([3]), att.NormRope()
+    att.kv_append(cache, k, k, slots, None, p, q=q)
+    att.attn_decode(cache, q, table, lens)
+    att.qk_norm_rope(q, k, None, p)
+    torch.cuda.synchronize()
+    start = torch.cuda.Event(enable_timing=True)
+    end = torch.cuda.Event(enable_timing=True)
+    cycles = 20_000_000
+    start.record()
+    torch.cuda._sleep(cycles)
+    end.record()
+    torch.cuda.synchronize()
+    cycles = int(cycles * 2000 / start.elapsed_time(end))  # two seconds
+    gaps, done = [], threading.Event()
+
+    def tick():
+        last = time.perf_counter()
+        while not done.is_set():
+            time.sleep(0.002)
+            now = time.perf_counter()
+            gaps.append(now - last)
+            last = now
+
+    for call in (lambda: att.attn_decode(cache, q, table, lens), lambda: att.qk_norm_rope(q, k, None, p),
+                 lambda: att.kv_append(cache, k, k, slots, None, p, q=q)):
+        done.clear()
+        gaps.clear()
+        t = threading.Thread(target=tick)
+        t.start()
+        torch.cuda._sleep(cycles)
+        for _ in range(24000):
+            call()
+        done.set()
+        t.join()
+        torch.cuda.synchronize()
+        print(f"longest pause of the other thread {max(gaps):.3f} s", flush=True)
+        assert max(gaps) < 0.5
