@@ -16,6 +16,12 @@ constexpr int kMinSplitTiles = 8;
 // Sequences that fill the card anyway are cut at 4096 keys, so that long ones share out (64
 // sequences of 1 to 32768 keys at 8 bits: 367 us, cut at 8192 keys 386).
 constexpr int kLongSplitTiles = 128;
+// Partial sums of one call, in bytes, at most. The page table's width says how long a sequence
+// may be, not how long any is, and every token and head has room for as many splits: without a
+// bound 32 sequences behind a table of a million keys asked for 17 GB. Splits that fill the
+// card need 17 MB of it at most (512 sequences of 300 keys behind such a table, 64 heads of 128:
+// 161 us, unbounded 904; 64 x 8 tokens over 1 to 262144 keys: 3.40 ms, unbounded 3.48).
+constexpr size_t kMostPartialBytes = (size_t)256 << 20;
 
 // Row tiles (of 16 query rows) a wave takes: as many as the window has, while accumulators
 // (D/4 registers a row tile) fit beside a tile's keys and values (D/2 at 16 bits). More row
@@ -46,7 +52,12 @@ inline AttnPlan decode_plan(int q_heads, int kv_heads, int D, int n_seqs, int wi
   // workgroups that run at once: two a CU, one where a wave takes many more than 256 registers
   const long long at_once = (wave_tiles * D >= 512 ? 1 : 2) * num_cus;
   const long long fill = (at_once + base - 1) / base;
-  const long long even = (tiles + kLongSplitTiles - 1) / kLongSplitTiles;
+  // no more even cuts than fill the card for a sequence alone, or than the workspace holds
+  const long long alone = (at_once * n_seqs + base - 1) / base;
+  const size_t split_bytes =
+      (size_t)n_seqs * window_tokens * q_heads * (D * sizeof(float) + sizeof(float2));
+  const long long even = std::min({(tiles + kLongSplitTiles - 1) / kLongSplitTiles, alone,
+                                   (long long)(kMostPartialBytes / split_bytes)});
   const long long most = tiles <= kUnsplitTiles ? 1 : std::max(1ll, tiles / kMinSplitTiles);
   plan.splits = (int)std::min<long long>({std::max(fill, even), most, kMaxSplits});
   plan.fill = (int)std::min<long long>(fill, kMaxSplits);
