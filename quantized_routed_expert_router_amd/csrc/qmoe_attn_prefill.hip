@@ -82,6 +82,10 @@ __device__ __forceinline__ RowTile row_tile(const PrefillParams& p, int seq, int
   return t;
 }
 
+// 8 waves are taken when row tiles fill the card by themselves, so they never split the keys.
+template <int NW>
+constexpr bool kWhole = NW == 8;
+
 #if defined(__HIP_DEVICE_COMPILE__)
 
 // The last sequence s for which at_or_before(s, q_starts[s]) holds (it does for a first part
@@ -204,7 +208,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prefill(Pref
   const RowTile t = row_tile<BM, KT>(p, seq, index);
   if ((long long)index * BM >= t.rows) return;
   const int split = blockIdx.y;
-  const bool direct = t.live <= 1;
+  const bool direct = kWhole<NW> || t.live <= 1;
   if (split >= t.live && !(direct && split == 0)) return;
   const int i0 = split * t.per, i1 = min(i0 + t.per, t.keys.count);
 
@@ -520,13 +524,17 @@ __global__ __launch_bounds__(kJoinThreads) void k_attn_prefill_join(PrefillParam
 
 template <typename A, int D, bool F8, int NW>
 hipError_t launch_one(const PrefillParams& p, hipStream_t stream) {
+  if (kWhole<NW> && p.splits != 1) return hipErrorInvalidValue;
   k_attn_prefill<A, D, F8, NW><<<dim3((unsigned)(p.slots * p.kv_heads), p.splits),
                                  dim3(64 * NW), 0, stream>>>(p);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || p.splits == 1) return e;
-  k_attn_prefill_join<A, D, NW><<<dim3((unsigned)(p.n * p.kv_heads * p.group), D / kJoinCols),
-                                  dim3(kJoinThreads), 0, stream>>>(p);
-  return hipGetLastError();
+  if constexpr (!kWhole<NW>) {
+    if (e != hipSuccess || p.splits == 1) return e;
+    k_attn_prefill_join<A, D, NW><<<dim3((unsigned)(p.n * p.kv_heads * p.group), D / kJoinCols),
+                                    dim3(kJoinThreads), 0, stream>>>(p);
+    e = hipGetLastError();
+  }
+  return e;
 }
 
 template <typename A, int D, bool F8>

@@ -40,6 +40,20 @@ def test_splits_of_usual_calls():
     assert round(parts(64, 1, 32, 8, 128, 1 << 18)) == 64
 
 
+@pytest.mark.parametrize("kv_heads,group", [(1, 8), (2, 8), (8, 4), (8, 12), (3, 1)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_large_prompt_chunks_take_no_workspace(kv_heads, group, D):
+    # chunks of 256 rows a workgroup fill the card and never split their keys
+    cache = att._KVCache(0, 0, 0, 0, 0, 4, 64, kv_heads, D)
+    a = att._Attn(1.0, 0, 0)
+    heads = kv_heads * group
+    for n in (-(-65536 // heads), 8192):
+        for seqs in (1, 5, 300, 8192):
+            if n * heads >= 65536 and n <= 8192:
+                assert lib.moe_attn_prefill_workspace_bytes(ctypes.byref(cache), heads, seqs, n,
+                                                            1 << 14, ctypes.byref(a)) == 0
+
+
 @pytest.mark.gpu
 def test_long_sequence_in_a_batch_at_the_bound():
     g = torch.Generator().manual_seed(11)
