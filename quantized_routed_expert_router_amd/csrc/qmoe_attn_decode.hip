@@ -89,7 +89,8 @@ struct ValueRegs {
   u32x4 w[N];
 };
 
-// Each cache line is used once a call: non-temporal loads read 7.1 TB/s here, plain ones 6.2.
+// Each cache line is used once a call (by windows of more rows than a wave takes, once for
+// every row tile): non-temporal loads read 7.1 TB/s here, plain ones 6.2.
 __device__ __forceinline__ u32x4 stream_load(const char* p) {
   return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
 }
@@ -312,7 +313,7 @@ __global__ __launch_bounds__(KW * kWave, decode_waves(NT, D)) void k_attn_decode
           for (int dt = 0; dt < DT; ++dt) o[nt][dt] *= a;
           m[nt] = now;
         }
-        const float base = m[nt] == kNegInf ? 0.0f : A::kBias - m[nt];
+        const float base = exponent_base<A>(m[nt]);
         f32x8 pr;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -397,7 +398,7 @@ __global__ __launch_bounds__(KW * kWave, decode_waves(NT, D)) void k_attn_decode
         }
       }
       __syncthreads();
-      constexpr int PER = DC / (4 * kWaves);  // columns a thread: 4 or 8
+      constexpr int PER = DC / (4 * kWaves);  // columns a thread: 2, 4 or 8
       const int r = threadIdx.x / (4 * kWaves), col = (threadIdx.x % (4 * kWaves)) * PER;
       const int row = row0 + nt * 16 + r;
       if (row < rows) {
@@ -467,7 +468,7 @@ hipError_t launch_tiles(const DecodeParams& p, int n_seqs, hipStream_t stream) {
   }
   if (nt == 2) return launch_one<A, D, F8, 2>(p, n_seqs, stream);
   // A short context on few workgroups is a chain of latencies, which twice the waves halve
-  // (517 keys: 10.7 us against 8.3 and a joining launch of 3.9); on many, four waves run
+  // (517 keys: 10.8 us against 7.2 and a joining launch of 3.8); on many, four waves run
   // nearer to the memory's rate (64 sequences at 8 bits: 370 us, with eight 447).
   if constexpr (D != 256) {
     if (p.splits == 1 && (long long)n_seqs * p.kv_heads * p.row_tiles <= device_cu_count())

@@ -217,6 +217,14 @@ __device__ __forceinline__ ScaleSplit split_scale(float scale) {
           scale == 0.0f ? 0u : 0xffffffffu};
 }
 
+// What is added to a row's scaled scores for its probabilities' exponents, with m its
+// reference. (Without a bias a bare negation, which costs no instruction.)
+template <typename A>
+__device__ __forceinline__ float exponent_base(float m) {
+  const float base = A::kBias == 0.0f ? -m : A::kBias - m;
+  return m == kNegInf ? 0.0f : base;
+}
+
 // 2^x for rescaling sums: never 0, so that an infinite sum stays infinite.
 __device__ __forceinline__ float rescale(float x) { return fmaxf(exp2_fast(x), 1e-38f); }
 #endif

@@ -183,8 +183,8 @@ struct Stage {
 
 // Bound by the matrix cores and the vector unit, which the two waves of a SIMD use in turn: a
 // tile's products and its exponentials, maxima and rounding cost about the same. 8192 tokens,
-// 32 query and 8 kv heads of 128, bf16: 592-616 us, 893-929 TFLOP/s (a large library product
-// reaches 1260); 4096 tokens of 16 heads of 256: 317 us, 434 TFLOP/s, one wave a SIMD.
+// 32 query and 8 kv heads of 128, bf16: 592-621 us, 885-929 TFLOP/s (a large library product
+// reaches 1260); 4096 tokens of 16 heads of 256: 290-317 us, 434-474 TFLOP/s, one wave a SIMD.
 template <typename A, int D, bool F8, int NW>
 __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prefill(PrefillParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -229,6 +229,9 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prefill(Pref
   const int pos_max = t.first_pos + (min(wrow + 32, t.rows) - 1) / p.group;
   const int first_key = t.first_pos + t.row0 / p.group;  // positions of the workgroup's rows
   const int last_key = t.first_pos + (min(t.row0 + BM, t.rows) - 1) / p.group;
+  // the last keys behind the windows of the wave's first and last rows, of the workgroup's last
+  const int low_min = behind_window(p.mask, pos_min), low_max = behind_window(p.mask, pos_max);
+  const int low_last = behind_window(p.mask, last_key);
   auto visible = [&](int key, bool bad_tile) {
     bool ok = key_visible(p.mask, key, pos);
     if (bad_tile && ok) ok = (unsigned)table[key >> p.page_shift] < (unsigned)p.num_pages;
@@ -260,7 +263,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prefill(Pref
   // An edge tile: not all of the workgroup's rows see all of it.
   auto is_edge = [&](bool bad_tile, int key0) {
     return bad_tile || key0 + KT - 1 > first_key ||
-           (p.mask.window != 0 && key0 <= behind_window(p.mask, last_key) &&
+           (p.mask.window != 0 && key0 <= low_last &&
             key0 + KT - 1 >= p.mask.sinks);
   };
   auto stage_store = [&](int buf, bool edge_tile) {
@@ -319,7 +322,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prefill(Pref
       if (j + STEP + 1 < count) st.ids(p, table, t.keys.tile(i0 + j + STEP + 1) * KT, tid);
     }
     const bool sees = any && key0 <= pos_max &&
-                      (p.mask.window == 0 || key0 + KT - 1 > behind_window(p.mask, pos_min) ||
+                      (p.mask.window == 0 || key0 + KT - 1 > low_min ||
                        key0 < p.mask.sinks);
     if (sees) {
       f32x16 s[HALVES];
@@ -337,7 +340,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prefill(Pref
       }
       // accumulator r of half x is key 32 x + 16 (r / 8) + 8 h + r % 8
       if (edge && (bad || key0 + KT - 1 > pos_min ||
-                   (p.mask.window != 0 && key0 <= behind_window(p.mask, pos_max)))) {
+                   (p.mask.window != 0 && key0 <= low_max))) {
 #pragma unroll
         for (int x = 0; x < HALVES; ++x)
 #pragma unroll
@@ -359,7 +362,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prefill(Pref
         for (int dt = 0; dt < DT; ++dt) o[dt] *= a;
         m = now;
       }
-      const float base = m == kNegInf ? 0.0f : A::kBias - m;
+      const float base = exponent_base<A>(m);
       V8 pr[2 * HALVES];
 #pragma unroll
       for (int x = 0; x < HALVES; ++x) {
@@ -421,11 +424,11 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prefill(Pref
   }
 
   l += __shfl_xor(l, 32);
-  float zero = 0.0f;  // NaN where a sum is not finite
+  float all = 0.0f;  // NaN where a sum is
 #pragma unroll
   for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) zero = __builtin_fmaf(o[dt][r], 0.0f, zero);
+    for (int r = 0; r < 16; ++r) all += o[dt][r];
   const long long at = (long long)token * hq + head, part = at * p.splits + split;
   const float vs = p.v_scale ? p.v_scale[kvh] : 1.0f;
   const float inv = l == 0.0f ? 0.0f : vs / l;
@@ -452,12 +455,12 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prefill(Pref
       }
     if (h == 0) p.stats[part] = make_float2(m, l);
   }
-  if (__builtin_amdgcn_ballot_w64(real && !(zero == 0.0f)) == 0) return;
+  if (__builtin_amdgcn_ballot_w64(real && __builtin_isnan(all)) == 0) return;
 
   // A value that is not finite takes every row that sees it. But where the 16-bit type holds
   // its key's probability as 0, the products above made NaN of an infinity. So a wave with
-  // such sums goes through its values once more, without scores, and writes the columns of
-  // the rows that see one again.
+  // such sums goes through its values once more, without scores, 32 columns at a time, and
+  // writes the columns of the rows that see one again.
 #pragma unroll 1
   for (int dt = 0; dt < DT; ++dt) {
     f32x16 c[3];  // counts of each kind
@@ -466,26 +469,43 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prefill(Pref
 #pragma unroll
       for (int r = 0; r < 16; ++r) c[i][r] = 0.0f;
 #pragma unroll 1
-    for (int j = 0; j < count * 2 * HALVES; ++j) {
-      const int from = t.keys.tile(i0 + j / (2 * HALVES)) * KT + 16 * (j % (2 * HALVES)) + 8 * h;
-      const int id = st.page_of(p, table, from);
-      uint32_t seen = 0;
-      if ((unsigned)id < (unsigned)p.num_pages) {
+    for (int j = 0; j < count; ++j) {
+      const int from = t.keys.tile(i0 + j) * KT + 8 * h;
+      int id[2 * HALVES];
+      u32x4 w[2 * HALVES];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) seen |= (uint32_t)key_visible(p.mask, from + k, pos) << k;
-      }
-      const long long word = st.row_of(p, id, kvh, from) * D + 8 * n32 + 256 * dt;
-      V8 a;
-      if constexpr (F8) {
-        const u32x2 w = *reinterpret_cast<const u32x2*>(p.cv + word);
-        a = expand_e4m3<A>(w[0], w[1]);
-      } else {
-        a = *reinterpret_cast<const V8*>(p.cv + 2 * word);
-      }
-      const V8 rows_seen = mask_elements<A>(seen);
+      for (int ks = 0; ks < 2 * HALVES; ++ks) id[ks] = st.page_of(p, table, from + 16 * ks);
+      bool some = false;
 #pragma unroll
-      for (int i = 0; i < 3; ++i)
-        c[i] = A::mfma32(non_finite<A>(a, non_finite_kind<A>(i)), rows_seen, c[i]);
+      for (int ks = 0; ks < 2 * HALVES; ++ks) {
+        const long long word = st.row_of(p, id[ks], kvh, from + 16 * ks) * D + 8 * n32 + 256 * dt;
+        if constexpr (F8) {
+          const u32x2 x = *reinterpret_cast<const u32x2*>(p.cv + word);
+          w[ks] = bits_as<u32x4>(expand_e4m3<A>(x[0], x[1]));
+        } else {
+          w[ks] = *reinterpret_cast<const u32x4*>(p.cv + 2 * word);
+        }
+      }
+#pragma unroll
+      for (int ks = 0; ks < 2 * HALVES; ++ks) {
+        V8 finite = bits_as<V8>(w[ks]);
+        some |= clear_nonfinite<A>(finite);
+      }
+      if (__builtin_amdgcn_ballot_w64(some) == 0) continue;
+#pragma unroll
+      for (int ks = 0; ks < 2 * HALVES; ++ks) {
+        uint32_t seen = 0;
+        if ((unsigned)id[ks] < (unsigned)p.num_pages) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            seen |= (uint32_t)key_visible(p.mask, from + 16 * ks + k, pos) << k;
+        }
+        const V8 rows_seen = mask_elements<A>(seen);
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          c[i] = A::mfma32(non_finite<A>(bits_as<V8>(w[ks]), non_finite_kind<A>(i)), rows_seen,
+                           c[i]);
+      }
     }
     if (!real) continue;
 #pragma unroll
