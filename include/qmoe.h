@@ -341,8 +341,9 @@ typedef struct {
 
 /* Pages and lengths of the sequences of one attention call, in device memory:
  *   table    int32 [n_seqs][table_stride], entry (s, i) is the page that holds rows
- *            i * page_size .. of sequence s; max_pages entries of a row may be read. Pages
- *            without a visible key are not read, and their entries may hold anything;
+ *            i * page_size .. of sequence s; max_pages entries of a row may be read.
+ *            Entries of pages without a visible key may hold anything (such a page may
+ *            still be read, where its number is one of the cache's, without effect);
  *            keys on a page number outside [0, num_pages) count as not visible.
  *   kv_lens  int32 [n_seqs], keys of each sequence, the call's own tokens included (they
  *            have been appended before); clamped to [0, max_pages * page_size]. */
@@ -356,7 +357,15 @@ typedef struct {
 /* softmax(scale * q.k) over the visible keys. A query at position p sees key j when
  * j <= p and (window == 0 or j > p - window or j < sinks). A query that sees no key (or
  * whose visible scores are all -inf) gets zeros. Query head h reads kv head
- * h / (heads / kv_heads). */
+ * h / (heads / kv_heads). window and sinks: 0..2^31-1. A row that sees an infinite (NaN)
+ * value is infinite (NaN) in that column, however small its probability; values that a row
+ * does not see never reach it.
+ *
+ * Scores, maxima and sums are fp32; outputs are rounded once. In the second product the
+ * decode calls hold a probability as a 16-bit value and its 16-bit rest (what is left out:
+ * 2^-16 of it in bf16; 2^-22 in fp16), the prefill calls as one 16-bit value, which is off by
+ * up to half a step (2^-8 of it in bf16, 2^-11 in fp16) beside the output's own rounding. In
+ * fp16 both also lose up to 2^-36 of the row's largest probability of each. */
 typedef struct {
   float scale;
   int32_t window, sinks;
@@ -394,8 +403,10 @@ moe_status moe_kv_append(const moe_kv_cache* cache, const moe_heads* k, const mo
  * q's heads: a multiple of kv_heads. window_tokens 1..MOE_MAX_WINDOW_TOKENS and
  * n_seqs * window_tokens <= MOE_MAX_DECODE_TOKENS. A 16-bit cache has q's type. ws: device
  * workspace of moe_attn_decode_workspace_bytes bytes, 256-byte aligned, no initialisation
- * needed (NULL when that is 0). out overlaps none of the inputs. Keys are split over
- * workgroups and joined; results do not depend on timing. */
+ * needed (NULL when that is 0; at most 256 MB and alignment, whatever max_pages is). out
+ * overlaps none of the inputs. Keys are split over workgroups and joined; results do not
+ * depend on timing, but their last bits may on max_pages, n_seqs and the card, which the
+ * split follows. */
 size_t moe_attn_decode_workspace_bytes(const moe_kv_cache* cache, int q_heads, int n_seqs,
                                        int window_tokens, int max_pages, const moe_attn* a);
 moe_status moe_attn_decode(const moe_kv_cache* cache, const moe_heads* q, int dtype,

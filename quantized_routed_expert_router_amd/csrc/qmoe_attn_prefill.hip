@@ -183,7 +183,7 @@ struct Stage {
 
 // Bound by the matrix cores and the vector unit, which the two waves of a SIMD use in turn: a
 // tile's products and its exponentials, maxima and rounding cost about the same. 8192 tokens,
-// 32 query and 8 kv heads of 128, bf16: 592-621 us, 885-929 TFLOP/s (a large library product
+// 32 query and 8 kv heads of 128, bf16: 592-628 us, 875-929 TFLOP/s (a large library product
 // reaches 1260); 4096 tokens of 16 heads of 256: 290-317 us, 434-474 TFLOP/s, one wave a SIMD.
 template <typename A, int D, bool F8, int NW>
 __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prefill(PrefillParams p) {
