@@ -282,7 +282,7 @@ __global__ __launch_bounds__(KW * kWave, decode_waves(NT, D)) void k_attn_decode
 
       // all keys of the tile visible to all of the window's rows?
       const bool full = !careful && (page0 | page1) >= 0 && key0 + kTile - 1 <= first_pos &&
-                        (p.mask.window == 0 || key0 > behind_window(p.mask, sp.len - 1) ||
+                        (key0 > behind_window(p.mask, sp.len - 1) ||
                          key0 + kTile - 1 < p.mask.sinks);
       bool dirty = false;  // not full, with non-finite values somewhere
       const bool on_page = (g & 2 ? page1 : page0) >= 0;
@@ -505,7 +505,7 @@ hipError_t launch_attn_decode(const AttnArgs& a, const AttnPlan& plan) {
   p.partial = (float*)(a.ws + plan.partial);
   p.stats = (float2*)(a.ws + plan.stats);
   p.scale = a.a.scale * kLog2e;
-  p.mask = KeyMask{a.a.window, a.a.sinks};
+  p.mask = key_mask(a.a);
   p.num_pages = a.cache.num_pages;
   while ((1 << p.page_shift) < a.cache.page_size) ++p.page_shift;
   p.kv_heads = a.cache.kv_heads;

@@ -283,14 +283,19 @@ struct KeyMask {
   int window, sinks;
 };
 
-// The last key behind the window of a query at pos. Windows go up to 2^31-1, and a position
-// may be negative (it sees no key at all), so it is held at 0 to keep the difference in range.
+// No window is one of 2^31-1 keys: positions are below that.
+inline KeyMask key_mask(const moe_attn& a) {
+  return {a.window == 0 ? 0x7fffffff : a.window, a.sinks};
+}
+
+// The last key behind the window of a query at pos, negative if there is none. A position may be
+// negative (it sees no key at all): it is held at 0 to keep the difference in range.
 __device__ __forceinline__ int behind_window(const KeyMask& m, int pos) {
   return max(pos, 0) - m.window;
 }
 
 __device__ __forceinline__ bool key_visible(const KeyMask& m, int key, int pos) {
-  return key <= pos && (m.window == 0 || key > behind_window(m, pos) || key < m.sinks);
+  return key <= pos && (key > behind_window(m, pos) || key < m.sinks);
 }
 
 // The key tiles (of TILE keys) that queries at positions first..last can see: sink tiles
@@ -308,9 +313,8 @@ __device__ __forceinline__ TileList visible_tiles(const KeyMask& m, int first, i
     return t;
   }
   const int hi = last / TILE + 1;
-  const int from = m.window == 0 ? 0 : max(0, behind_window(m, first) + 1);
-  t.lo = from / TILE;
-  t.ns = m.window == 0 ? 0 : min((int)(((long long)m.sinks + TILE - 1) / TILE), t.lo);
+  t.lo = max(0, behind_window(m, first) + 1) / TILE;
+  t.ns = min((int)(((long long)m.sinks + TILE - 1) / TILE), t.lo);
   t.count = t.ns + (hi - t.lo);
   return t;
 }

@@ -263,8 +263,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prefill(Pref
   // An edge tile: not all of the workgroup's rows see all of it.
   auto is_edge = [&](bool bad_tile, int key0) {
     return bad_tile || key0 + KT - 1 > first_key ||
-           (p.mask.window != 0 && key0 <= low_last &&
-            key0 + KT - 1 >= p.mask.sinks);
+           (key0 <= low_last && key0 + KT - 1 >= p.mask.sinks);
   };
   auto stage_store = [&](int buf, bool edge_tile) {
     if (edge_tile) {
@@ -322,8 +321,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prefill(Pref
       if (j + STEP + 1 < count) st.ids(p, table, t.keys.tile(i0 + j + STEP + 1) * KT, tid);
     }
     const bool sees = any && key0 <= pos_max &&
-                      (p.mask.window == 0 || key0 + KT - 1 > low_min ||
-                       key0 < p.mask.sinks);
+                      (key0 + KT - 1 > low_min || key0 < p.mask.sinks);
     if (sees) {
       f32x16 s[HALVES];
       const int krow = (n32 & 19) | ((n32 & 4) << 1) | ((n32 & 8) >> 1);
@@ -339,8 +337,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prefill(Pref
         }
       }
       // accumulator r of half x is key 32 x + 16 (r / 8) + 8 h + r % 8
-      if (edge && (bad || key0 + KT - 1 > pos_min ||
-                   (p.mask.window != 0 && key0 <= low_max))) {
+      if (edge && (bad || key0 + KT - 1 > pos_min || key0 <= low_max)) {
 #pragma unroll
         for (int x = 0; x < HALVES; ++x)
 #pragma unroll
@@ -593,7 +590,7 @@ hipError_t launch_attn_prefill(const AttnArgs& a, const AttnPlan& plan) {
   p.partial = (float*)(a.ws + plan.partial);
   p.stats = (float2*)(a.ws + plan.stats);
   p.scale = a.a.scale * kLog2e;
-  p.mask = KeyMask{a.a.window, a.a.sinks};
+  p.mask = key_mask(a.a);
   p.num_pages = a.cache.num_pages;
   while ((1 << p.page_shift) < a.cache.page_size) ++p.page_shift;
   p.kv_heads = a.cache.kv_heads;
