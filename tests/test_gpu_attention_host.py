@@ -34,7 +34,11 @@ def test_out_of_memory_is_torchs_error(given):
     torch.cuda.empty_cache()
     room = torch.cuda.memory_reserved() + (32 << 20)
     torch.cuda.set_per_process_memory_fraction(room / torch.cuda.get_device_properties(0).total_memory)
+    held = []
     try:
+        with pytest.raises(torch.OutOfMemoryError):  # what the allocator has left of its own
+            while True:
+                held.append(torch.empty(32 << 20, dtype=torch.uint8, device="cuda"))
         with pytest.raises(torch.OutOfMemoryError):
             att.qk_norm_rope(q, k, None, p, k_out=k_out if given else None)
         with pytest.raises(torch.OutOfMemoryError):
@@ -88,4 +92,4 @@ def test_other_threads_run_while_a_launch_waits():
         t.join()
         torch.cuda.synchronize()
         print(f"longest pause of the other thread {max(gaps):.3f} s", flush=True)
-        assert max(gaps) < 0.5
+        assert max(gaps) < 1.0  # held up by the launch it would be the spin, nearly
