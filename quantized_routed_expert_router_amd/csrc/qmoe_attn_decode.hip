@@ -468,7 +468,7 @@ hipError_t launch_tiles(const DecodeParams& p, int n_seqs, hipStream_t stream) {
   }
   if (nt == 2) return launch_one<A, D, F8, 2>(p, n_seqs, stream);
   // A short context on few workgroups is a chain of latencies, which twice the waves halve
-  // (517 keys: 11.0 us against 8.2 and a joining launch of 3.8); on many, four waves run
+  // (517 keys: 10.6 us against 7.2 and a joining launch of 3.8); on many, four waves run
   // nearer to the memory's rate (64 sequences at 8 bits: 370 us, with eight 447).
   if constexpr (D != 256) {
     if (p.splits == 1 && (long long)n_seqs * p.kv_heads * p.row_tiles <= device_cu_count())
