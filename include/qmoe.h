@@ -425,6 +425,116 @@ moe_status moe_attn_prefill(const moe_kv_cache* cache, const moe_heads* q, int d
                             const moe_attn* a, void* out, void* ws, size_t ws_bytes,
                             void* stream);
 
+/* ---------------------------------------------------------------------------------
+ * Routing by a rule, for routers whose scores are not the softmax of the selected logits.
+ * (The engine explainer, "Architecture overview": each token keeps the experts its router
+ * picks. The pages give moe_route's rule; this one is the library's own.) */
+#define MOE_F32 3 /* fp32, beside MOE_BF16 and MOE_F16, where a call says so             */
+
+#define MOE_SCORE_SIGMOID 0
+#define MOE_SCORE_SOFTMAX 1 /* over all E experts                                      */
+#define MOE_GROUP_MAX 0
+#define MOE_GROUP_TOP2 1
+#define MOE_MAX_ROUTE_GROUPS 64
+
+/* score s_e = 1 / (1 + exp(-l_e)), or exp(l_e) / sum_i exp(l_i); pick c_e = s_e + bias_e.
+ * Group g holds experts g * E / groups ..; it is worth its largest c, or the sum of its two
+ * largest (a group of one: its c). The top_groups worthiest groups stay, of equal ones the
+ * lower; of their experts the k with the largest c are taken, of equal ones the lower id.
+ * Slot order is the order of c. w = scale * s, or with renormalize scale * s / sum of the k
+ * taken (0 where that sum is 0). All in binary64, w rounded once to fp32.
+ * A logit that is NaN or a c that is NaN or -inf ranks last, whatever its group (such experts
+ * by lower id), and has weight 0; where every logit is -inf, softmax scores are 0. In a
+ * softmax, +inf logits share the weight. */
+typedef struct {
+  int32_t score;       /* MOE_SCORE_SIGMOID or MOE_SCORE_SOFTMAX                       */
+  const float* bias;   /* device fp32 [E], 4-byte aligned, or NULL                     */
+  int32_t groups;      /* 1..MOE_MAX_ROUTE_GROUPS, a divisor of E                      */
+  int32_t top_groups;  /* 1..groups, with top_groups * E / groups >= k                 */
+  int32_t group_score; /* MOE_GROUP_MAX or MOE_GROUP_TOP2                              */
+  int32_t renormalize; /* 0 or 1                                                       */
+  float scale;         /* finite                                                       */
+} moe_route_rule;
+
+/* moe_route by a rule. logits: device [n][E] of dtype MOE_F32, MOE_BF16 or MOE_F16, aligned to
+ * their size. out, ws, limits and errors as moe_route (the workspace is
+ * moe_route_workspace_bytes); MOE_ERR_INVALID_ARGUMENT for a rule outside the ranges above. */
+moe_status moe_route_scored(const void* logits, int dtype, int n_tokens, int n_experts, int top_k,
+                            const moe_route_rule* rule, const moe_routing* out, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * Microscaled 4-bit floats (the OCP microscaling format MXFP4) and products in them.
+ *
+ * A matrix of `rows` rows and `cols` columns, cols a multiple of 32:
+ *   codes   uint8 [rows][cols/2]    e2m1 (sign, 2 exponent bits, 1 fraction bit: 0, .5, 1, 1.5,
+ *                                   2, 3, 4, 6), column 2i in the low half of byte i
+ *   scales  uint8 [rows][cols/32]   e8m0: the factor 2^(byte - 127) of 32 columns; 255: NaN
+ * Both 16-byte aligned. E experts' matrices follow each other. */
+typedef struct {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  int32_t rows, cols;
+} moe_mx_matrix;
+
+#define MOE_MX_MAX_COLS 65536      /* columns (reduction axis) of a matrix              */
+#define MOE_MX_MAX_ROWS (1 << 24)  /* rows of one matrix                                */
+
+/* Rows to 4 bits: for each block of 32 values, scale byte = max(floor(log2 max|x|) - 2, -127)
+ * + 127 (a block of zeros: 0), codes = x / scale rounded to nearest even, magnitudes beyond 6
+ * to 6. A block with an infinity or a NaN gets scale 255 and codes 0. x: device, `rows` rows
+ * of `cols` values of dtype MOE_F32, MOE_BF16 or MOE_F16, row_stride elements apart; 16-byte
+ * aligned, rows too. codes and scales as above; they overlap neither x nor each other. */
+moe_status moe_mx_quantize(const void* x, int dtype, int64_t rows, int cols, int64_t row_stride,
+                           uint8_t* codes, uint8_t* scales, void* stream);
+
+/* Values of `rows` rows (m->rows is not read), rounded once to dtype (exact in fp32 and bf16
+ * below the type's largest value; beyond: infinity); a block of scale 255: NaN. out: device,
+ * contiguous, 16-byte aligned. */
+moe_status moe_mx_dequantize(const moe_mx_matrix* m, int64_t rows, int dtype, void* out,
+                             void* stream);
+
+/* out[t][r] = sum_c Q(x)[t][c] * w[r][c] with Q as moe_mx_quantize: products and scales exact,
+ * sums fp32, rounded once to out_dtype. x: n_tokens rows as in moe_mx_quantize (cols = w->cols).
+ * out: device, w->rows values a row, rows out_stride elements apart, aligned to their size,
+ * overlapping none of the inputs. n_tokens <= MOE_MAX_ROUTE_TOKENS. ws: device workspace of
+ * moe_mx_linear_workspace_bytes bytes, 256-byte aligned, no initialisation needed (NULL when
+ * that is 0). */
+size_t moe_mx_linear_workspace_bytes(int n_tokens, int cols);
+moe_status moe_mx_linear(const void* x, int dtype, int64_t row_stride, int n_tokens,
+                         const moe_mx_matrix* w, void* out, int out_dtype, int64_t out_stride,
+                         void* ws, size_t ws_bytes, void* stream);
+
+/* The same for rows that are quantized already: x->rows rows; one quantization then serves
+ * several products. No workspace. */
+moe_status moe_mx_linear_quantized(const moe_mx_matrix* x, const moe_mx_matrix* w, void* out,
+                                   int out_dtype, int64_t out_stride, void* stream);
+
+/* A routed-expert layer with microscaled weights: gate and up [E][d_ff][d_model], down
+ * [E][d_model][d_ff] (rows and cols those of one expert). */
+typedef struct {
+  int32_t d_model;   /* d: multiple of 32, at most 8192                            */
+  int32_t d_ff;      /* f: multiple of 32, at most 8192                            */
+  int32_t n_experts; /* E: 1..MOE_MAX_EXPERTS                                      */
+  int32_t top_k;     /* k: 1..min(E, MOE_MAX_TOP_K)                                */
+  moe_mx_matrix gate, up, down;
+} moe_mx_layer;
+
+/* out[t] = residual[t] + sum_j w[t][j] * y_j (slot order), with, for the expert of slot j,
+ * g = Q(x) gate^T and u = Q(x) up^T (fp32 sums), h = g / (1 + exp(-g)) * u, y = Q(h) down^T
+ * (fp32 sums). h and its 4-bit form are those of the binary64 value for the given g and u; the
+ * weighted sum is binary64 and is rounded once. x: n_tokens rows of d values as in
+ * moe_mx_quantize. residual: device fp32 [n][d] or NULL (zeros); out: device fp32 [n][d], which
+ * may be residual; both 16-byte aligned, and otherwise out overlaps no input. r: routing of
+ * moe_route or moe_route_scored for the same n, E and k. ws: device workspace of
+ * moe_mx_ffn_workspace_bytes bytes, 256-byte aligned, no initialisation needed. One entry
+ * point serves single tokens, verify windows and prefill chunks. n_tokens <=
+ * MOE_MAX_PREFILL_TOKENS; n_tokens == 0 enqueues nothing. */
+size_t moe_mx_ffn_workspace_bytes(const moe_mx_layer* L, int n_tokens);
+moe_status moe_mx_ffn(const moe_mx_layer* L, const void* x, int dtype, int64_t row_stride,
+                      int n_tokens, const moe_routing* r, const float* residual, float* out,
+                      void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -39,7 +39,8 @@ COMMON_FLAGS = [
 LIBS = {
     "libqmoe.so": ["qmoe.hip", "qmoe_route.hip", "qmoe_decode.hip", "qmoe_prefill.hip",
                    "qmoe_attn.hip", "qmoe_rows.hip", "qmoe_attn_decode.hip",
-                   "qmoe_attn_prefill.hip"],
+                   "qmoe_attn_prefill.hip", "qmoe_route_rule.hip", "qmoe_mx.hip",
+                   "qmoe_mx_quant.hip", "qmoe_mx_window.hip", "qmoe_mx_gemm.hip"],
     "libqmoe_synth.so": ["synth.hip"],
 }
 

@@ -274,6 +274,13 @@ hipError_t launch_route(const float* logits, int n, int E, int k, const moe_rout
 // The spread top-k alone (one wave a token): expert ids and routing weights, no grouping.
 hipError_t launch_route_topk(const float* logits, int n, int E, int k, int32_t* ids, float* w,
                              hipStream_t stream);
+// The grouping alone: offsets and pair list of P expert ids (more than kFusedRouteTokens
+// tokens' pairs; ws as for launch_route).
+hipError_t launch_route_group(const int32_t* ids, int P, int E, const moe_routing* out, void* ws,
+                              hipStream_t stream);
+hipError_t launch_route_scored(const void* logits, int dtype, int n, int E, int k,
+                               const moe_route_rule& rule, const moe_routing* out, void* ws,
+                               hipStream_t stream);
 hipError_t launch_decode(const DecodeArgs& a);
 hipError_t launch_prefill(const PrefillArgs& a);
 

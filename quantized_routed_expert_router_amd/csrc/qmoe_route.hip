@@ -178,24 +178,28 @@ hipError_t launch_route_kpl(const float* logits, int n, int E, int k, const moe_
   }
   hipError_t err = launch_route_topk(logits, n, E, k, out->topk_ids, out->topk_w, stream);
   if (err != hipSuccess) return err;
-  const int P = n * k;
+  return launch_route_group(out->topk_ids, n * k, E, out, ws, stream);
+}
+
+}  // namespace
+
+hipError_t launch_route_group(const int32_t* ids, int P, int E, const moe_routing* out, void* ws,
+                              hipStream_t stream) {
   if (P <= kSingleGroupPairs) {
-    hipLaunchKernelGGL(k_route_group, dim3(1), dim3(kGroupThreads), 0, stream, out->topk_ids, P,
+    hipLaunchKernelGGL(k_route_group, dim3(1), dim3(kGroupThreads), 0, stream, ids, P,
                        E, out->expert_offsets, out->pair_index);
     return hipGetLastError();
   }
   const int nchunks = (P + kChunkPairs - 1) / kChunkPairs;
   int* hist = static_cast<int*>(ws);
   hipLaunchKernelGGL(k_group_count, dim3(nchunks), dim3(kScatterThreads), 0, stream,
-                     out->topk_ids, P, E, hist);
-  err = hipGetLastError();
+                     ids, P, E, hist);
+  const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   hipLaunchKernelGGL(k_group_scatter, dim3(nchunks), dim3(kScatterThreads), 0, stream,
-                     out->topk_ids, P, E, nchunks, hist, out->expert_offsets, out->pair_index);
+                     ids, P, E, nchunks, hist, out->expert_offsets, out->pair_index);
   return hipGetLastError();
 }
-
-}  // namespace
 
 hipError_t launch_route_topk(const float* logits, int n, int E, int k, int32_t* ids, float* w,
                              hipStream_t stream) {

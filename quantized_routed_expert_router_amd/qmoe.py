@@ -29,7 +29,10 @@ EXPORTS = ("moe_status_string", "moe_route_workspace_bytes", "moe_route",
            "moe_layer_decode", "moe_layer_decode_stages", "moe_layer_decode_noalloc",
            "moe_expert_ffn_prefill", "moe_expert_ffn_prefill_stages",
            "moe_qk_norm_rope", "moe_kv_append", "moe_attn_decode_workspace_bytes",
-           "moe_attn_decode", "moe_attn_prefill_workspace_bytes", "moe_attn_prefill")
+           "moe_attn_decode", "moe_attn_prefill_workspace_bytes", "moe_attn_prefill",
+           "moe_route_scored", "moe_mx_quantize", "moe_mx_dequantize",
+           "moe_mx_linear_workspace_bytes", "moe_mx_linear", "moe_mx_linear_quantized",
+           "moe_mx_ffn_workspace_bytes", "moe_mx_ffn")
 
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
@@ -61,6 +64,12 @@ class _Routing(ctypes.Structure):
                 ("expert_offsets", ctypes.c_void_p), ("pair_index", ctypes.c_void_p)]
 
 
+class _RouteRule(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("bias", ctypes.c_void_p), ("groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_score", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 DEBUG_FIELDS = ("xq", "xs", "gate_dots", "up_dots", "g", "u", "h", "hq", "hs", "down_dots", "y",
                 "logits")
 
@@ -80,6 +89,8 @@ def _load():
     L.moe_route_workspace_bytes.argtypes = [i32, i32, i32]
     L.moe_route_workspace_bytes.restype = sz
     L.moe_route.argtypes = [vp, i32, i32, i32, ctypes.POINTER(_Routing), vp, sz, vp]
+    L.moe_route_scored.argtypes = [vp, i32, i32, i32, i32, ctypes.POINTER(_RouteRule),
+                                   ctypes.POINTER(_Routing), vp, sz, vp]
     L.moe_ffn_workspace_bytes.argtypes = [ctypes.POINTER(_Layer), i32, i32]
     L.moe_ffn_workspace_bytes.restype = sz
     L.moe_expert_ffn_decode.argtypes = [ctypes.POINTER(_Layer), vp, i32, ctypes.POINTER(_Routing),
@@ -145,6 +156,7 @@ I32 = (torch.int32,)
 TWO_BYTE = (torch.int16, torch.bfloat16, torch.float16, torch.uint16)
 WORDS = (torch.int32, torch.uint32)
 BYTES = (torch.uint8, torch.int8)
+FLOATS = {torch.float32: 3, torch.bfloat16: 0, torch.float16: 1}  # MOE_F32, MOE_BF16, MOE_F16
 
 
 def _stream(stream) -> int:
@@ -284,6 +296,73 @@ def route(logits: torch.Tensor, top_k: int, out: Routing | None = None, stream=N
                        0 if ws is None else ws.numel(), _stream(stream))
     if rc != MOE_OK:
         raise MoeError("moe_route", rc)
+    return out
+
+
+SCORES = {"sigmoid": 0, "softmax": 1}
+GROUP_SCORES = {"max": 0, "top2": 1}
+
+
+@dataclass
+class RouteRule:
+    """How route_scored picks and weighs experts (see moe_route_rule): scores by "sigmoid" or
+    "softmax" over all experts; `bias` fp32 [E] (or None) added for the selection alone;
+    experts in `groups` equal groups of neighbours, of which the `top_groups` (None: all) with
+    the largest score ("max") or sum of the two largest ("top2") stay; weights divided by
+    their sum with `renormalize`, and times `scale`."""
+    score: str = "sigmoid"
+    bias: torch.Tensor | None = None
+    groups: int = 1
+    top_groups: int | None = None
+    group_score: str = "top2"
+    renormalize: bool = True
+    scale: float = 1.0
+
+    def _struct(self) -> _RouteRule:
+        if self.score not in SCORES:
+            raise ValueError(f"score: {self.score!r}, expected one of {tuple(SCORES)}")
+        if self.group_score not in GROUP_SCORES:
+            raise ValueError(f"group_score: {self.group_score!r}, expected one of "
+                             f"{tuple(GROUP_SCORES)}")
+        keep = self.groups if self.top_groups is None else self.top_groups
+        return _RouteRule(SCORES[self.score], _ptr(self.bias), self.groups, keep,
+                          GROUP_SCORES[self.group_score], 1 if self.renormalize else 0, self.scale)
+
+
+def route_scored(logits: torch.Tensor, top_k: int, rule: RouteRule, out: Routing | None = None,
+                 stream=None, ws: torch.Tensor | None = None) -> Routing:
+    """moe_route_scored: experts, weights and grouping of `logits` [n, E] (fp32, bf16 or fp16)
+    by `rule`. Works on the GPU of its tensors, on that GPU's current stream or on `stream`;
+    what it allocates belongs to that stream."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise ValueError(f"logits: expected [n, E], got {getattr(logits, 'shape', type(logits))}")
+    if stream is not None:
+        if logits.is_cuda and stream.device != logits.device:
+            raise ValueError(f"stream: on {stream.device}, the tensors on {logits.device}")
+        with torch.cuda.stream(stream):
+            return route_scored(logits, top_k, rule, out, None, ws)
+    n, E = logits.shape
+    args = _Args()
+    args.need(logits, "logits", tuple(FLOATS))
+    if rule.bias is not None:
+        args.need(rule.bias, "bias", F32, shape=(E,))
+    if out is not None:
+        out.check(n, E, top_k, args)
+    if ws is not None:
+        args.need(ws, "ws", BYTES)
+    args.on_gpu()
+    st = rule._struct()
+    with torch.cuda.device(logits.device):
+        if out is None:
+            out = Routing.empty(n, E, max(top_k, 0), logits.device)
+        if ws is None:
+            ws = route_workspace(n, E, top_k, logits.device)
+        rs = out._struct()
+        rc = lib.moe_route_scored(_ptr(logits), FLOATS[logits.dtype], n, E, top_k, ctypes.byref(st),
+                                  ctypes.byref(rs), _ptr(ws), 0 if ws is None else ws.numel(),
+                                  _stream(None))
+    if rc != MOE_OK:
+        raise MoeError("moe_route_scored", rc)
     return out
 
 
