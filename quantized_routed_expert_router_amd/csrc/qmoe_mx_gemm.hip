@@ -11,14 +11,14 @@ namespace qmoe {
 namespace {
 
 typedef __attribute__((address_space(3))) void* lptr_t;
-typedef const __attribute__((address_space(1))) void* gptr_t;
+typedef __attribute__((address_space(3))) float lds_float;
+typedef __attribute__((address_space(3))) mx_f32x4 lds_f32x4;
+
+__device__ __forceinline__ uint32_t lds_address(void* p) { return (uint32_t)(uintptr_t)(lptr_t)p; }
 
 constexpr int kThreads = 256;
+constexpr int kTileRows = 256;  // most weight rows, and rows of x, of a tile
 constexpr int kStepBytes = 64;  // codes of a row in one stage: 128 values, 4 blocks
-
-// Blocks past the end of the reduction axis are read from here: codes of 0 under scale 1.
-__device__ __align__(16) const uint8_t mx_zero_block[16] = {};
-__device__ const uint8_t mx_unit_scale[4] = {127, 127, 127, 127};
 
 enum Mode { kLinear, kGateUp, kDown };
 
@@ -38,6 +38,11 @@ struct GemmArgs {
   uint8_t *hq, *hs;  // gate and up: codes and scales of h [P]
 };
 
+// Buffers are declared 2^31 bytes long: every offset is kept inside the tensor by construction,
+// and an offset of 2^31 reads zeros.
+constexpr uint32_t kBufferBytes = 0x80000000u;
+constexpr int kOutside = (int)0x80000000u;
+
 __device__ __forceinline__ int swz(int row, int seg) { return seg ^ ((row >> 2) & 3); }
 
 // One stage of the ring in LDS: 128 values of the reduction axis. Row r's four 16-byte blocks
@@ -45,33 +50,58 @@ __device__ __forceinline__ int swz(int row, int seg) { return seg ^ ((row >> 2) 
 // different banks; its four scales are one word (TAIL: a word a scale).
 template <int BN, int BM, bool TAIL>
 struct Stage {
-  static constexpr int kXRows = BM < 64 ? 64 : BM;  // a direct load brings in 64 rows
   uint4 w[BN * 4];
-  uint4 x[kXRows * 4];
-  uint32_t ws[TAIL ? 4 : 1][kThreads];
-  uint32_t xs[TAIL ? 4 : 1][kThreads];
+  uint4 x[(BM < 64 ? 64 : BM) * 4];
+  uint32_t ws[TAIL ? 4 : 1][kTileRows];
+  uint32_t xs[TAIL ? 4 : 1][kTileRows];
 };
 
-// A workgroup of 4 waves multiplies BM rows of x by BN weight rows. The waves lie WM by 4 / WM
-// over the tile; a wave holds NW x NX accumulators of 32 x 32 (weight rows by rows of x, so
-// that a lane holds 16 weight rows of one row of x: half of a block of h). A ring of SLOTS
-// stages is filled by direct loads into LDS. A stage is two instructions deep: while the first
-// half multiplies, the second half's operands are read, and while the second multiplies, those
-// of the next stage. Between them the stage's reads are complete and its slot is refilled.
-template <int WM, int NW, int NX, int SLOTS, bool TAIL, int MODE>
+// The ring's slots by name: an array of them would be kept in memory.
+template <class S, int N>
+struct Slots {
+  static constexpr int kCount = N;
+  S *s0, *s1, *s2, *s3;
+  template <int I>
+  __device__ __forceinline__ S* get() const {
+    if constexpr (I == 0) return s0;
+    else if constexpr (I == 1) return s1;
+    else if constexpr (I == 2) return s2;
+    else return s3;
+  }
+};
+
+// A workgroup of WM x WN waves multiplies BM rows of x by BN weight rows; a wave holds NW x NX accumulators of 32 x 32 (weight rows by rows of x, so
+// that a lane holds 16 weight rows of one row of x: half of a block of h). For gate and up the
+// first half of the tile's weight rows are gate, the second the same rows of up, and a wave
+// holds both of its rows.
+//
+// A ring of SLOTS stages is filled by direct loads into LDS; the offset of a lane never changes
+// and the stage is a scalar offset, so a load costs no arithmetic. Every slot is an LDS variable
+// of its own: the compiler then sees that the slots being filled are not the one being read, and
+// adds no wait for them. A stage is two instructions deep: while the first half multiplies, the
+// second half's operands are read, and while the second multiplies, those of the next stage.
+// Between them the stage's reads are complete and its slot is refilled.
+//
+// TAIL: K is not a multiple of 128. Blocks past K are read as zeros (codes and scales), and
+// scales come a byte at a time, since their rows are not whole words.
+template <class S, int WM, int WN, int NW, int NX, int SLOTS, bool TAIL, int MODE>
 struct Tile {
-  static constexpr int WN = 4 / WM;
+  static constexpr int NT = kWave * WM * WN;  // threads: each load brings in NT / 4 rows
   static constexpr int BN = 32 * NW * WN, BM = 32 * NX * WM;
   static constexpr int kGroupsW = NW, kGroupsX = NX;  // 32-row groups a wave
-  typedef Stage<BN, BM, TAIL> S;
-  static constexpr int kWLoads = BN / 64, kXLoads = S::kXRows / 64;
-  static constexpr int kOps = kWLoads + kXLoads + (TAIL ? 8 : 2);
-  static_assert(BN >= 64 && BN <= kThreads && BM <= kThreads, "one scale word a thread");
+  static constexpr int kRows = NT / 4;
+  static constexpr int kWLoads = BN / kRows, kXLoads = BM < kRows ? 1 : BM / kRows;
+  // 4 waves bring in both kinds of scales one after the other, 8 waves each half its own
+  static constexpr int kKinds = NT == 2 * kTileRows ? 1 : 2;
+  static constexpr int kOps = kWLoads + kXLoads + (TAIL ? 4 : 1) * kKinds;
+  static_assert(NT == kTileRows || NT == 2 * kTileRows, "a scale word a thread and kind");
+  static_assert(BN >= kRows && BN <= kTileRows && BM <= kTileRows, "whole loads");
+  static_assert(MODE != kGateUp || (BN == 256 && NT == 256), "gate rows and up rows in loads of their own");
 
-  S* ring;
-  const uint8_t* wp[kWLoads];  // this thread's weight rows, at its block of stage 0
-  const uint8_t* xp[kXLoads];
-  const uint8_t *wsp, *xsp;  // its scale words at stage 0
+  Slots<S, SLOTS> st;
+  __amdgpu_buffer_rsrc_t wbuf[MODE == kGateUp ? 2 : 1], xbuf, sbuf[kKinds];
+  int woff[kWLoads], xoff[kXLoads], soff[kKinds];  // byte offsets of this thread at stage 0
+  int to;  // kKinds == 1: words from the stage's weight scales to this wave's
   int tid, lane, wave, wm, wn, nk, nb;
   mx_f32x16 acc[NW][NX];
 
@@ -84,81 +114,85 @@ struct Tile {
 
   __device__ __forceinline__ int block_of() const { return swz(tid >> 2, tid & 3); }
 
-  __device__ __forceinline__ void load(int stage, int slot) const {
+  // SIZE bytes a lane, into LDS in the order of the lanes (1: a word a byte)
+  template <int SIZE>
+  __device__ __forceinline__ void bring(__amdgpu_buffer_rsrc_t b, void* lds, int off, int at) const {
+    if constexpr (SIZE == 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lptr_t)lds, 16, off, at, 0, 0);
+    if constexpr (SIZE == 4) __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lptr_t)lds, 4, off, at, 0, 0);
+    if constexpr (SIZE == 1) __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lptr_t)lds, 1, off, at, 0, 0);
+  }
+
+  template <int SLOT>
+  __device__ __forceinline__ void load(int stage) const {
     const int s = min(stage, nk - 1);
-    S& st = ring[slot];
-    const int b = 4 * s + block_of();
-    const size_t off = (size_t)s * kStepBytes;
+    S& g = *st.template get<SLOT>();
+    const bool in = !TAIL || 4 * s + block_of() < nb;
 #pragma unroll
-    for (int i = 0; i < kWLoads; ++i) {
-      const uint8_t* p = wp[i] + off;
-      if (TAIL && b >= nb) p = mx_zero_block;
-      __builtin_amdgcn_global_load_lds((gptr_t)p, (lptr_t)(st.w + kThreads * i + kWave * wave), 16, 0, 0);
-    }
+    for (int i = 0; i < kWLoads; ++i)
+      bring<16>(wbuf[MODE == kGateUp ? i / 2 : 0], g.w + NT * i + kWave * wave, in ? woff[i] : kOutside,
+                s * kStepBytes);
 #pragma unroll
-    for (int i = 0; i < kXLoads; ++i) {
-      const uint8_t* p = xp[i] + off;
-      if (TAIL && b >= nb) p = mx_zero_block;
-      __builtin_amdgcn_global_load_lds((gptr_t)p, (lptr_t)(st.x + kThreads * i + kWave * wave), 16, 0, 0);
-    }
-    if constexpr (TAIL) {
+    for (int i = 0; i < kXLoads; ++i)
+      bring<16>(xbuf, g.x + NT * i + kWave * wave, in ? xoff[i] : kOutside, s * kStepBytes);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bool in = 4 * s + j < nb;
-        __builtin_amdgcn_global_load_lds((gptr_t)(in ? wsp + 4 * s + j : mx_unit_scale),
-                                         (lptr_t)(st.ws[j] + kWave * wave), 1, 0, 0);
-        __builtin_amdgcn_global_load_lds((gptr_t)(in ? xsp + 4 * s + j : mx_unit_scale),
-                                         (lptr_t)(st.xs[j] + kWave * wave), 1, 0, 0);
+    for (int t = 0; t < kKinds; ++t) {
+#pragma unroll
+      for (int j = 0; j < (TAIL ? 4 : 1); ++j) {
+        uint32_t* words = kKinds == 1 ? g.ws[j] + to : (t == 0 ? g.ws[j] : g.xs[j]) + kWave * wave;
+        if constexpr (TAIL)
+          bring<1>(sbuf[t], words, 4 * s + j < nb ? soff[t] + j : kOutside, 4 * s);
+        else
+          bring<4>(sbuf[t], words, soff[t], 4 * s);
       }
-    } else {
-      __builtin_amdgcn_global_load_lds((gptr_t)(wsp + 4 * s), (lptr_t)(st.ws[0] + kWave * wave), 4, 0, 0);
-      __builtin_amdgcn_global_load_lds((gptr_t)(xsp + 4 * s), (lptr_t)(st.xs[0] + kWave * wave), 4, 0, 0);
     }
   }
+
+  // Tile row of weight group q of this wave
+  __device__ __forceinline__ int wrow(int q) const {
+    const int r = lane & 31;
+    if constexpr (MODE == kGateUp) {
+      constexpr int NG = NW / 2;
+      return (q / NG) * (BN / 2) + (wn * NG + q % NG) * 32 + r;
+    }
+    return (wn * NW + q) * 32 + r;
+  }
+  __device__ __forceinline__ int xrow(int i) const { return (wm * NX + i) * 32 + (lane & 31); }
 
   // Lane l of the half h = l / 32 takes blocks 2h (first instruction) and 2h + 1 (second).
-  __device__ __forceinline__ Ops read(int slot, int half) const {
-    const S& st = ring[slot];
-    const int r = lane & 31, b = 2 * (lane >> 5) + half;
-    Ops o;
+  template <int SLOT, int HALF>
+  __device__ __forceinline__ void read(Ops& o) const {
+    const S& g = *st.template get<SLOT>();
+    const int b = 2 * (lane >> 5) + HALF;
 #pragma unroll
-    for (int q = 0; q < NW; ++q) {
-      const int row = (wn * NW + q) * 32 + r;
-      __builtin_memcpy(&o.w[q], &st.w[4 * row + swz(row, b)], 16);
-    }
+    for (int i = 0; i < NX; ++i)
+      __builtin_memcpy(&o.x[i], &g.x[4 * xrow(i) + swz(lane & 31, b)], 16);
 #pragma unroll
-    for (int i = 0; i < NX; ++i) {
-      const int row = (wm * NX + i) * 32 + r;
-      __builtin_memcpy(&o.x[i], &st.x[4 * row + swz(row, b)], 16);
-    }
-    return o;
+    for (int q = 0; q < NW; ++q)
+      __builtin_memcpy(&o.w[q], &g.w[4 * wrow(q) + swz(lane & 31, b)], 16);
   }
 
-  __device__ __forceinline__ Scales scales(int slot) const {
-    const S& st = ring[slot];
-    const int r = lane & 31, h = lane >> 5;
-    Scales o;
+  template <int SLOT>
+  __device__ __forceinline__ void scales(Scales& o) const {
+    const S& g = *st.template get<SLOT>();
+    [[maybe_unused]] const int h = lane >> 5;
 #pragma unroll
     for (int q = 0; q < NW; ++q) {
-      const int row = (wn * NW + q) * 32 + r;
       if constexpr (TAIL) {
-        o.w[0][q] = (int)st.ws[2 * h][row];
-        o.w[1][q] = (int)st.ws[2 * h + 1][row];
+        o.w[0][q] = (int)g.ws[2 * h][wrow(q)];
+        o.w[1][q] = (int)g.ws[2 * h + 1][wrow(q)];
       } else {
-        o.w[0][q] = (int)(st.ws[0][row] >> (16 * h));
+        o.w[0][q] = (int)g.ws[0][wrow(q)];
       }
     }
 #pragma unroll
     for (int i = 0; i < NX; ++i) {
-      const int row = (wm * NX + i) * 32 + r;
       if constexpr (TAIL) {
-        o.x[0][i] = (int)st.xs[2 * h][row];
-        o.x[1][i] = (int)st.xs[2 * h + 1][row];
+        o.x[0][i] = (int)g.xs[2 * h][xrow(i)];
+        o.x[1][i] = (int)g.xs[2 * h + 1][xrow(i)];
       } else {
-        o.x[0][i] = (int)(st.xs[0][row] >> (16 * h));
+        o.x[0][i] = (int)g.xs[0][xrow(i)];
       }
     }
-    return o;
   }
 
   template <int HALF>
@@ -171,6 +205,83 @@ struct Tile {
                                               s.x[TAIL ? HALF : 0][i]);
   }
 
+  // The two scales of this lane's half to the lower half of each word (where the words are used,
+  // not where they are read: that would wait for them).
+  __device__ __forceinline__ void halve(Scales& o) const {
+    if constexpr (!TAIL) {
+      const int sh = (lane >> 5) * 16;
+#pragma unroll
+      for (int q = 0; q < NW; ++q) o.w[0][q] = (int)((uint32_t)o.w[0][q] >> sh);
+#pragma unroll
+      for (int i = 0; i < NX; ++i) o.x[0][i] = (int)((uint32_t)o.x[0][i] >> sh);
+    }
+  }
+
+  // The operands are in registers at this point: without it the loads of the next stage are
+  // moved behind the loop's branch, in front of the products that need them.
+  __device__ __forceinline__ static void pin(Ops& o) {
+#pragma unroll
+    for (int i = 0; i < NX; ++i) asm volatile("" : "+v"(o.x[i]));
+#pragma unroll
+    for (int q = 0; q < NW; ++q) asm volatile("" : "+v"(o.w[q]));
+  }
+  __device__ __forceinline__ static void pin(Scales& o) {
+#pragma unroll
+    for (int t = 0; t < (TAIL ? 2 : 1); ++t) {
+#pragma unroll
+      for (int i = 0; i < NX; ++i) asm volatile("" : "+v"(o.x[t][i]));
+#pragma unroll
+      for (int q = 0; q < NW; ++q) asm volatile("" : "+v"(o.w[t][q]));
+    }
+  }
+
+  // One product, then up to one LDS read and one direct load: the four waves' reads and loads
+  // are spread over the stage and do not hold up the matrix cores.
+  template <int READS, int LOADS>
+  __device__ __forceinline__ static void interleave() {
+    constexpr int M = NW * NX;
+    constexpr int R = (READS + M - 1) / M, L = (LOADS + M - 1) / M;
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a matrix-core op
+      __builtin_amdgcn_sched_group_barrier(0x100, R, 0);  // LDS reads
+      if (LOADS) __builtin_amdgcn_sched_group_barrier(0x020, L, 0);  // direct loads
+      __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);  // VALU
+    }
+  }
+
+  // Stage s in slot SLOT: its first half's operands and its scales are in a and sc.
+  template <int SLOT>
+  __device__ __forceinline__ void step(int s, Ops& a, Scales& sc) {
+    constexpr int NEXT = (SLOT + 1) % SLOTS;
+    Ops b;
+    halve(sc);
+    read<SLOT, 1>(b);
+    multiply<0>(a, sc);
+    interleave<NW + NX, 0>();
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's reads of the stage are done
+    wait_vmcnt<(SLOTS - 2) * kOps>();    // and its loads of the next one
+    barrier_after_lds_dma();
+    __builtin_amdgcn_sched_barrier(0);
+    load<SLOT>(s + SLOTS);
+    Scales next;
+    scales<NEXT>(next);
+    read<NEXT, 0>(a);
+    multiply<1>(b, sc);
+    interleave<2 * (NW + NX), kOps>();
+    __builtin_amdgcn_sched_barrier(0);
+    pin(a);
+    pin(next);
+    sc = next;
+  }
+
+  template <int SLOT>
+  __device__ __forceinline__ void first_loads() const {
+    load<SLOT>(SLOT);
+    if constexpr (SLOT + 1 < SLOTS) first_loads<SLOT + 1>();
+  }
+
   __device__ __forceinline__ void run() {
 #pragma unroll
     for (int q = 0; q < NW; ++q)
@@ -178,33 +289,40 @@ struct Tile {
       for (int i = 0; i < NX; ++i)
 #pragma unroll
         for (int j = 0; j < 16; ++j) acc[q][i][j] = 0.0f;
-#pragma unroll
-    for (int s = 0; s < SLOTS; ++s) load(s, s);
+    first_loads<0>();
     wait_vmcnt<(SLOTS - 1) * kOps>();
     barrier_after_lds_dma();
-    Ops a = read(0, 0);
-    Scales sc = scales(0);
-    int slot = 0;
-    for (int s = 0; s < nk; ++s) {
-      const Ops b = read(slot, 1);
-      multiply<0>(a, sc);
-      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's reads of the stage are done
-      wait_vmcnt<(SLOTS - 2) * kOps>();    // and its loads of the next one
-      barrier_after_lds_dma();
-      load(s + SLOTS, slot);
-      slot = slot + 1 == SLOTS ? 0 : slot + 1;
-      const Scales next = scales(slot);
-      a = read(slot, 0);
-      multiply<1>(b, sc);
-      sc = next;
+    Ops a;
+    Scales sc;
+    read<0, 0>(a);
+    scales<0>(sc);
+    pin(a);
+    pin(sc);
+    // whole rounds of the ring, then the rest: leaving the loop in the middle of a round would
+    // make the compiler drain the ring at the loop's head
+    static_assert(SLOTS >= 2 && SLOTS <= 4, "the steps below");
+    int s = 0;
+    for (; s + SLOTS <= nk; s += SLOTS) {
+      step<0>(s, a, sc);
+      step<1>(s + 1, a, sc);
+      if constexpr (SLOTS > 2) step<2 % SLOTS>(s + 2, a, sc);
+      if constexpr (SLOTS > 3) step<3 % SLOTS>(s + 3, a, sc);
+    }
+    if (s < nk) {
+      step<0>(s, a, sc);
+      if (SLOTS > 2 && s + 1 < nk) {
+        step<1>(s + 1, a, sc);
+        if (SLOTS > 3 && s + 2 < nk) step<2 % SLOTS>(s + 2, a, sc);
+      }
     }
     wait_vmcnt<0>();  // the loads past the last stage have landed
   }
 
   // e: expert (its weights); n0: first weight row (gate and up: first row of f); m0, rows: this
-  // tile's rows of x (gate and up: grouped pairs; down: grouped pairs; linear: rows)
-  __device__ __forceinline__ void init(S* ring_, const GemmArgs& a, int e, int n0, int m0, int rows) {
-    ring = ring_;
+  // tile's rows of x (gate and up, down: grouped pairs)
+  __device__ __forceinline__ void init(const Slots<S, SLOTS>& slots, const GemmArgs& a, int e, int n0,
+                                       int m0, int rows) {
+    st = slots;
     tid = threadIdx.x;
     lane = tid & (kWave - 1);
     wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -212,49 +330,52 @@ struct Tile {
     wn = wave / WM;
     nb = a.K / kMxBlock;
     nk = (nb + 3) / 4;
-    const size_t codes = (size_t)a.K / 2;
-    auto weight = [&](int tr, const uint8_t*& c, const uint8_t*& s) {
-      // tile row tr: 32-row group tr / 32 of wave column tr / (32 NW)
-      int row = n0 + tr;
-      bool up = false;
-      if constexpr (MODE == kGateUp) {
-        // a wave's groups: NW / 2 of gate, then the same rows of up
-        const int group = tr / 32, q = group % NW;
-        up = q >= NW / 2;
-        row = n0 + ((group / NW) * (NW / 2) + q % (NW / 2)) * 32 + tr % 32;
-      }
-      // past the matrix: its last row, never stored
-      const size_t at = (size_t)e * a.N + min(row, a.N - 1);
-      c = (up ? a.w1 : a.w0) + at * codes;
-      s = (up ? a.s1 : a.s0) + at * nb;
-    };
-    auto source = [&](int i) -> size_t {
-      const int g = m0 + min(i, rows - 1);
-      return MODE == kGateUp ? (size_t)(a.pair_index[g] / a.k) : (size_t)g;
-    };
-    const uint8_t* unused;
+    const int codes = a.K / 2;
+    // weights: a buffer from the tile's first row; rows past the matrix: its last, never stored
+    const size_t first = (size_t)e * a.N + n0;
+    const int last = a.N - 1 - n0;
+    wbuf[0] = buffer_rsrc(a.w0 + first * codes, kBufferBytes);
+    if constexpr (MODE == kGateUp) wbuf[1] = buffer_rsrc(a.w1 + first * codes, kBufferBytes);
+    constexpr int kOwn = MODE == kGateUp ? BN / 2 : BN;  // tile rows of one matrix
 #pragma unroll
-    for (int i = 0; i < kWLoads; ++i) {
-      weight(64 * i + (tid >> 2), wp[i], unused);
-      wp[i] += 16 * block_of();
+    for (int i = 0; i < kWLoads; ++i)
+      woff[i] = min((kRows * i + (tid >> 2)) % kOwn, last) * codes + 16 * block_of();
+    // rows of x: those of the pairs' tokens (gate and up), or the tile's own from its first
+    const size_t x0 = MODE == kGateUp ? 0 : (size_t)m0;
+    xbuf = buffer_rsrc(a.xq + x0 * codes, kBufferBytes);
+    auto source = [&](int i) {
+      const int j = min(i, rows - 1);
+      return MODE == kGateUp ? a.pair_index[m0 + j] / a.k : j;
+    };
+#pragma unroll
+    for (int i = 0; i < kXLoads; ++i) xoff[i] = source(kRows * i + (tid >> 2)) * codes + 16 * block_of();
+    const uint8_t* ws = (MODE == kGateUp && wave >= 2 ? a.s1 : a.s0) + first * nb;
+    const uint8_t* xs = a.xs + x0 * nb;
+    if constexpr (kKinds == 1) {
+      const bool x = wave >= 4;
+      const int row = tid % kTileRows;
+      sbuf[0] = buffer_rsrc(x ? xs : ws, kBufferBytes);
+      soff[0] = (x ? source(min(row, BM - 1)) : min(row % kOwn, last)) * nb;
+      to = (x ? (int)((sizeof(S::ws)) / 4) : 0) + kWave * (wave % 4);
+    } else {
+      sbuf[0] = buffer_rsrc(ws, kBufferBytes);
+      soff[0] = min(tid % kOwn, last) * nb;
+      sbuf[1] = buffer_rsrc(xs, kBufferBytes);
+      soff[1] = source(min(tid, BM - 1)) * nb;
+      to = 0;
     }
-    weight(min(tid, BN - 1), unused, wsp);
-#pragma unroll
-    for (int i = 0; i < kXLoads; ++i)
-      xp[i] = a.xq + source(64 * i + (tid >> 2)) * codes + 16 * block_of();
-    xsp = a.xs + source(min(tid, BM - 1)) * nb;
   }
 };
 
 // The four pieces and the scale of a block of h from its 64-bit values. The gate and up sums of
 // the block lie in LDS as gu[value][lane], gate first; lanes l and l + 32 hold its two halves.
 // Rolled loops: taken by a block in some two hundred.
-__device__ __forceinline__ void hidden_block64(float* gu, int lane, uint32_t (&pieces)[4], uint32_t& scale) {
+__device__ __forceinline__ void hidden_block64(lds_float* gu, int lane, uint32_t (&pieces)[4], uint32_t& scale) {
   double m = 0.0;
   bool bad = false;
 #pragma unroll 1
   for (int j = 0; j < 16; ++j) {
-    float *lo = gu + j * kWave + lane, *hi = lo + 16 * kWave;
+    lds_float *lo = gu + j * kWave + lane, *hi = lo + 16 * kWave;
     const double h = mx_silu_up64(*lo, *hi);
     bad |= !(fabs(h) < __builtin_inf());
     m = fmax(m, fabs(h));
@@ -268,7 +389,7 @@ __device__ __forceinline__ void hidden_block64(float* gu, int lane, uint32_t (&p
   uint64_t all = 0;
 #pragma unroll 1
   for (int j = 0; j < 16; ++j) {
-    const float *lo = gu + j * kWave + lane, *hi = lo + 16 * kWave;
+    const lds_float *lo = gu + j * kWave + lane, *hi = lo + 16 * kWave;
     const uint64_t bits = (uint64_t)__float_as_uint(*hi) << 32 | __float_as_uint(*lo);
     const uint64_t c = bad ? 0u : mx_code64(__longlong_as_double((int64_t)bits), scale);
     all |= c << (4 * j);
@@ -321,7 +442,7 @@ __device__ __forceinline__ void hidden_block(const mx_f32x16& g, const mx_f32x16
   some |= __shfl_xor((int)some, 32) != 0;
   redo = redo && (some || m != 0.0f);
   if (__ballot(redo)) {
-    float* gu = stage();
+    lds_float* gu = stage();
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       gu[j * kWave + lane] = g[j];
@@ -333,19 +454,33 @@ __device__ __forceinline__ void hidden_block(const mx_f32x16& g, const mx_f32x16
   }
 }
 
+// LDS that a wave has for itself once the ring is free: WAVES / SLOTS waves (rounded up, at least
+// two) share a slot.
+template <class S, int WAVES, int SLOTS>
+struct WaveLds {
+  static constexpr int kShare = (WAVES + SLOTS - 1) / SLOTS < 2 ? 2 : (WAVES + SLOTS - 1) / SLOTS;
+  static constexpr size_t kBytes = sizeof(S) / kShare / 16 * 16;
+  __device__ static __forceinline__ lds_float* of(const Slots<S, SLOTS>& slots, int wave) {
+    uint32_t at = lds_address(slots.s0);
+    if (wave / kShare == 1) at = lds_address(slots.s1);
+    if (SLOTS > 2 && wave / kShare == 2) at = lds_address(slots.s2);
+    if (SLOTS > 3 && wave / kShare == 3) at = lds_address(slots.s3);
+    return reinterpret_cast<lds_float*>(at + wave % kShare * (uint32_t)kBytes);
+  }
+};
+
 template <class T>
 __device__ __forceinline__ void gateup_epilogue(T& c, const GemmArgs& a, int n0, int g0, int rows,
-                                                float* lds) {
+                                                lds_float* lds) {
   constexpr int NG = T::kGroupsW / 2, NX = T::kGroupsX;  // gate groups a wave, groups of pairs
   __syncthreads();  // every wave is done with the ring
-  const int lane = c.lane, r = lane & 31, half = lane >> 5;
-  float* mine = lds + c.wave * (32 * kWave);
+  const int lane = c.lane, half = lane >> 5;
 #pragma unroll
   for (int i = 0; i < NX; ++i)
 #pragma unroll
     for (int q = 0; q < NG; ++q) {
       uint32_t pc[4], scale;
-      hidden_block(c.acc[q][i], c.acc[NG + q][i], lane, pc, scale, [&] { return mine; });
+      hidden_block(c.acc[q][i], c.acc[NG + q][i], lane, pc, scale, [&] { return lds; });
       // piece p holds rows 8p + 4 half .. + 3 of the block: word p is piece p of the lower half
       // and then of the upper; each half stores two words
       const uint32_t mine0 = half ? pc[2] : pc[0], mine1 = half ? pc[3] : pc[1];
@@ -355,7 +490,7 @@ __device__ __forceinline__ void gateup_epilogue(T& c, const GemmArgs& a, int n0,
       uint2 word;
       word.x = half ? (g0w | mine0 << 16) : (mine0 | g0w << 16);
       word.y = half ? (g1w | mine1 << 16) : (mine1 | g1w << 16);
-      const int row = (c.wm * NX + i) * 32 + r;
+      const int row = c.xrow(i);
       const int f0 = n0 + (c.wn * NG + q) * 32;
       if (row < rows && f0 < a.N) {
         const size_t g = (size_t)(g0 + row);
@@ -366,53 +501,100 @@ __device__ __forceinline__ void gateup_epilogue(T& c, const GemmArgs& a, int n0,
 }
 
 // Lane l holds, of row l % 32 of x, the outputs 8p + 4 (l / 32) .. + 3, p = 0..3, of each group.
+// 32 rows at a time go through LDS, so that a row's outputs of the wave leave side by side, 16
+// bytes a lane; where out's rows or its last columns are not whole 16-byte words, a value a lane.
 template <class T, int MODE>
-__device__ __forceinline__ void rows_epilogue(T& c, const GemmArgs& a, int n0, int m0, int rows) {
-  constexpr int NX = T::kGroupsX, NW = T::kGroupsW;
-  const int lane = c.lane, r = lane & 31, half = lane >> 5;
+__device__ __forceinline__ void rows_epilogue(T& c, const GemmArgs& a, int n0, int m0, int rows, lds_float* lds) {
+  constexpr int NX = T::kGroupsX, NW = T::kGroupsW, kCols = 32 * NW, kPitch = kCols + 4;
+  __syncthreads();  // every wave is done with the ring
+  const int lane = c.lane, half = lane >> 5;
+  const int col0 = n0 + c.wn * kCols;
+  const bool words = MODE == kDown || (a.out_stride % 8 == 0 && a.N % 8 == 0 &&
+                                       (reinterpret_cast<uintptr_t>(a.out) & 15) == 0);
 #pragma unroll
   for (int i = 0; i < NX; ++i) {
-    const int row = (c.wm * NX + i) * 32 + r;
-    if (row >= rows) continue;
-    const size_t at = MODE == kDown ? (size_t)a.pair_index[m0 + row] : (size_t)(m0 + row);
+    const int first = (c.wm * NX + i) * 32;
+    if (first >= rows) break;
 #pragma unroll
     for (int q = 0; q < NW; ++q)
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
-        const int col = n0 + (c.wn * NW + q) * 32 + 8 * p + 4 * half;
-        const float v0 = c.acc[q][i][4 * p], v1 = c.acc[q][i][4 * p + 1], v2 = c.acc[q][i][4 * p + 2],
-                    v3 = c.acc[q][i][4 * p + 3];
-        if constexpr (MODE == kDown) {
-          if (col < a.N) {  // a multiple of 32
-            const mx_f32x4 v = {v0, v1, v2, v3};
-            __builtin_nontemporal_store(
-                v, reinterpret_cast<mx_f32x4*>(static_cast<float*>(a.out) + at * a.N + col));
-          }
-        } else {
-          const float v[4] = {v0, v1, v2, v3};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (col + j >= a.N) break;
-            const int64_t o = (int64_t)at * a.out_stride + col + j;
-            if (a.out_dtype == MOE_F32) static_cast<float*>(a.out)[o] = v[j];
-            else if (a.out_dtype == MOE_BF16) static_cast<__bf16*>(a.out)[o] = (__bf16)v[j];
-            else static_cast<_Float16*>(a.out)[o] = (_Float16)v[j];
-          }
-        }
+        const mx_f32x4 v = {c.acc[q][i][4 * p], c.acc[q][i][4 * p + 1], c.acc[q][i][4 * p + 2],
+                            c.acc[q][i][4 * p + 3]};
+        *reinterpret_cast<lds_f32x4*>(lds + (lane & 31) * kPitch + 32 * q + 8 * p + 4 * half) = v;
       }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    const int count = min(32, rows - first);
+    if (words && (MODE == kDown || a.out_dtype == MOE_F32)) {
+      constexpr int kLanes = kCols / 4, kStep = kWave / kLanes;  // lanes a row, rows at once
+      const int col = 4 * (lane % kLanes);
+#pragma unroll
+      for (int j = 0; j < 32 / kStep; ++j) {
+        const int r = j * kStep + lane / kLanes;
+        if (r >= count || col0 + col >= a.N) continue;
+        const mx_f32x4 v = *reinterpret_cast<const lds_f32x4*>(lds + r * kPitch + col);
+        const size_t at = MODE == kDown ? (size_t)a.pair_index[m0 + first + r] * a.N
+                                        : (size_t)(m0 + first + r) * a.out_stride;
+        __builtin_nontemporal_store(
+            v, reinterpret_cast<mx_f32x4*>(static_cast<float*>(a.out) + at + col0 + col));
+      }
+    } else if (words) {
+      constexpr int kLanes = kCols / 8, kStep = kWave / kLanes;
+      const int col = 8 * (lane % kLanes);
+#pragma unroll
+      for (int j = 0; j < 32 / kStep; ++j) {
+        const int r = j * kStep + lane / kLanes;
+        if (r >= count || col0 + col >= a.N) continue;
+        const mx_f32x4 v = *reinterpret_cast<const lds_f32x4*>(lds + r * kPitch + col);
+        const mx_f32x4 w = *reinterpret_cast<const lds_f32x4*>(lds + r * kPitch + col + 4);
+        i32x4 o;
+        if (a.out_dtype == MOE_BF16) {
+          typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+          const bf16x8 h = {(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3],
+                            (__bf16)w[0], (__bf16)w[1], (__bf16)w[2], (__bf16)w[3]};
+          __builtin_memcpy(&o, &h, 16);
+        } else {
+          typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
+          const f16x8 h = {(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3],
+                           (_Float16)w[0], (_Float16)w[1], (_Float16)w[2], (_Float16)w[3]};
+          __builtin_memcpy(&o, &h, 16);
+        }
+        *reinterpret_cast<i32x4*>(static_cast<uint16_t*>(a.out) +
+                                  (size_t)(m0 + first + r) * a.out_stride + col0 + col) = o;
+      }
+    } else {
+      for (int j = lane; j < count * kCols; j += kWave) {
+        const int r = j / kCols, col = j % kCols;
+        if (col0 + col >= a.N) continue;
+        const float v = lds[r * kPitch + col];
+        const size_t at = (size_t)(m0 + first + r) * a.out_stride + col0 + col;
+        if (a.out_dtype == MOE_F32) static_cast<float*>(a.out)[at] = v;
+        else if (a.out_dtype == MOE_BF16) static_cast<__bf16*>(a.out)[at] = (__bf16)v;
+        else static_cast<_Float16*>(a.out)[at] = (_Float16)v;
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
-template <int WM, int NW, int NX, int SLOTS, bool TAIL, int MODE>
-__device__ __forceinline__ void tile(char* lds, const GemmArgs& a, int e, int n0, int m0, int rows) {
-  typedef Tile<WM, NW, NX, SLOTS, TAIL, MODE> T;
+template <class S, int WM, int WN, int NW, int NX, int SLOTS, bool TAIL, int MODE>
+__device__ __forceinline__ void tile(const Slots<S, SLOTS>& slots, const GemmArgs& a, int e, int n0, int m0,
+                                     int rows) {
+  typedef Tile<S, WM, WN, NW, NX, SLOTS, TAIL, MODE> T;
+  typedef WaveLds<S, WM * WN, SLOTS> Lds;
   T c;
-  c.init(reinterpret_cast<typename T::S*>(lds), a, e, n0, m0, rows);
+  c.init(slots, a, e, n0, m0, rows);
   c.run();
-  if constexpr (MODE == kGateUp)
-    gateup_epilogue(c, a, n0, m0, rows, reinterpret_cast<float*>(lds));
-  else
-    rows_epilogue<T, MODE>(c, a, n0, m0, rows);
+  lds_float* lds = Lds::of(slots, c.wave);
+  if constexpr (MODE == kGateUp) {
+    static_assert(Lds::kBytes >= 32 * kWave * 4, "a block's gate and up sums");
+    gateup_epilogue(c, a, n0, m0, rows, lds);
+  } else {
+    static_assert(Lds::kBytes >= 32 * (32 * NW + 4) * 4, "32 rows of the wave's outputs");
+    rows_epilogue<T, MODE>(c, a, n0, m0, rows, lds);
+  }
 }
 
 // M-tile mt of the list runs on XCD mt % 8, which takes its column tiles one after another (they
@@ -426,30 +608,47 @@ __device__ __forceinline__ bool list_tile(int ntiles, int ntn, int& mt, int& nt)
 
 // The grouped product: 256 weight rows by up to 128 pairs.
 template <bool TAIL, int MODE>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_mx_grouped(GemmArgs a) {
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(TAIL ? 1 : 2, 2))) void k_mx_grouped(GemmArgs a) {
+  typedef Stage<256, 128, TAIL> S;
   constexpr int SLOTS = TAIL ? 2 : 3;
-  __shared__ __attribute__((aligned(16))) char lds[sizeof(Stage<256, 128, TAIL>) * SLOTS];
+  __shared__ S slot0, slot1;
+  Slots<S, SLOTS> slots{&slot0, &slot1, nullptr, nullptr};
+  if constexpr (SLOTS == 3) {
+    __shared__ S slot2;
+    slots.s2 = &slot2;
+  }
   constexpr int kN = MODE == kGateUp ? 128 : 256;  // rows of f, or of d, a workgroup
   const int ntn = (a.N + kN - 1) / kN;
   int mt, nt;
   if (!list_tile(load_uniform(a.ntiles), ntn, mt, nt)) return;
   const int4 t = load_uniform(a.tiles + mt);
   if (t.z <= 32)
-    tile<1, 2, 1, SLOTS, TAIL, MODE>(lds, a, t.x, nt * kN, t.y, t.z);
+    tile<S, 1, 4, 2, 1, SLOTS, TAIL, MODE>(slots, a, t.x, nt * kN, t.y, t.z);
   else if (t.z <= 64)
-    tile<1, 2, 2, SLOTS, TAIL, MODE>(lds, a, t.x, nt * kN, t.y, t.z);
+    tile<S, 1, 4, 2, 2, SLOTS, TAIL, MODE>(slots, a, t.x, nt * kN, t.y, t.z);
   else
-    tile<1, 2, 4, SLOTS, TAIL, MODE>(lds, a, t.x, nt * kN, t.y, t.z);
+    tile<S, 1, 4, 2, 4, SLOTS, TAIL, MODE>(slots, a, t.x, nt * kN, t.y, t.z);
 }
 
-template <int WM, int NW, int NX, int SLOTS, bool TAIL>
-__global__ __launch_bounds__(kThreads) void k_mx_linear(GemmArgs a) {
-  typedef Tile<WM, NW, NX, SLOTS, TAIL, kLinear> T;
-  __shared__ __attribute__((aligned(16))) char lds[sizeof(typename T::S) * SLOTS];
-  const int ntn = (a.N + T::BN - 1) / T::BN;
+template <int WM, int WN, int NW, int NX, int SLOTS, bool TAIL>
+__global__ __launch_bounds__(kWave * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_mx_linear(
+    GemmArgs a) {
+  constexpr int BN = 32 * NW * WN, BM = 32 * NX * WM;
+  typedef Stage<BN, BM, TAIL> S;
+  __shared__ S slot0, slot1;
+  Slots<S, SLOTS> slots{&slot0, &slot1, nullptr, nullptr};
+  if constexpr (SLOTS > 2) {
+    __shared__ S slot2;
+    slots.s2 = &slot2;
+  }
+  if constexpr (SLOTS > 3) {
+    __shared__ S slot3;
+    slots.s3 = &slot3;
+  }
+  const int ntn = (a.N + BN - 1) / BN;
   int mt, nt;
-  if (!list_tile((a.rows + T::BM - 1) / T::BM, ntn, mt, nt)) return;
-  tile<WM, NW, NX, SLOTS, TAIL, kLinear>(lds, a, 0, nt * T::BN, mt * T::BM, min(T::BM, a.rows - mt * T::BM));
+  if (!list_tile((a.rows + BM - 1) / BM, ntn, mt, nt)) return;
+  tile<S, WM, WN, NW, NX, SLOTS, TAIL, kLinear>(slots, a, 0, nt * BN, mt * BM, min(BM, a.rows - mt * BM));
 }
 
 // ---------------------------------------------------------------- work list
@@ -530,14 +729,14 @@ __global__ __launch_bounds__(1024) void k_mx_combine(const float* __restrict__ y
 
 inline int list_grid(int max_mt, int ntn) { return (max_mt + 7) / 8 * 8 * ntn; }
 
-template <int WM, int NW, int NX, int SLOTS, int TSLOTS>
+template <int WM, int WN, int NW, int NX, int SLOTS, int TSLOTS>
 void linear(const GemmArgs& g, hipStream_t stream) {
-  constexpr int BN = 32 * NW * (4 / WM), BM = 32 * NX * WM;
-  const dim3 grid(list_grid((g.rows + BM - 1) / BM, (g.N + BN - 1) / BN));
+  constexpr int BN = 32 * NW * WN, BM = 32 * NX * WM;
+  const dim3 grid(list_grid((g.rows + BM - 1) / BM, (g.N + BN - 1) / BN)), block(kWave * WM * WN);
   if (g.K % 128 == 0)
-    hipLaunchKernelGGL((k_mx_linear<WM, NW, NX, SLOTS, false>), grid, dim3(kThreads), 0, stream, g);
+    hipLaunchKernelGGL((k_mx_linear<WM, WN, NW, NX, SLOTS, false>), grid, block, 0, stream, g);
   else
-    hipLaunchKernelGGL((k_mx_linear<WM, NW, NX, TSLOTS, true>), grid, dim3(kThreads), 0, stream, g);
+    hipLaunchKernelGGL((k_mx_linear<WM, WN, NW, NX, TSLOTS, true>), grid, block, 0, stream, g);
 }
 
 }  // namespace
@@ -566,9 +765,9 @@ hipError_t launch_mx_linear(const MxLinearArgs& a, hipStream_t stream) {
     g.xs = xs;
   }
   if ((long long)a.n * a.N <= 1024ll * 1024)
-    linear<1, 1, 2, 4, 3>(g, stream);
+    linear<1, 4, 1, 2, 4, 3>(g, stream);
   else
-    linear<2, 4, 4, 4, 2>(g, stream);
+    linear<2, 4, 2, 4, 4, 3>(g, stream);
   return hipGetLastError();
 }
 
