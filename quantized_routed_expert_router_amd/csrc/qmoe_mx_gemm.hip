@@ -28,7 +28,11 @@ struct GemmArgs {
   const uint8_t *xq, *xs;  // codes and scales of the rows to multiply
   const int32_t* pair_index;
   const int4* tiles;
-  const int* ntiles;
+  const int* xcd_first;  // [kXcds + 1] first tile of each XCD
+  int xcd_m, xcd_n;      // linear: column of XCDs over rows of x, tiles of an XCD: xcd_rm x xcd_rn,
+  int xcd_rm, xcd_rn;    // taken in panels of `panel` column tiles
+  int panel;
+  int64_t wrows, xrows;  // rows of the weights' and of x's tensors
   int rows;   // linear: rows of x
   int N, K;   // weight rows (of one expert) and the reduction axis
   int k;      // top_k
@@ -47,20 +51,28 @@ __device__ __forceinline__ int swz(int row, int seg) { return seg ^ ((row >> 2) 
 
 // One stage of the ring in LDS: 128 values of the reduction axis. Row r's four 16-byte blocks
 // sit at positions swz(r, block), so that 16 neighbouring rows' reads of one block fall into
-// different banks; its four scales are one word (TAIL: a word a scale).
-template <int BN, int BM, bool TAIL>
+// different banks.
+template <int BN, int BM>
 struct Stage {
   uint4 w[BN * 4];
   uint4 x[(BM < 64 ? 64 : BM) * 4];
-  uint32_t ws[TAIL ? 4 : 1][kTileRows];
-  uint32_t xs[TAIL ? 4 : 1][kTileRows];
+};
+
+// Scales of two rounds of ROUND stages: a word (four blocks) a row and stage.
+template <int BN, int BM, int ROUND>
+struct ScaleRing {
+  static constexpr int kRound = ROUND;
+  uint32_t s[2][ROUND][BN + BM];
 };
 
 // The ring's slots by name: an array of them would be kept in memory.
-template <class S, int N>
+template <class S, class SC, int N>
 struct Slots {
+  typedef S Slot;
+  typedef SC Scale;
   static constexpr int kCount = N;
   S *s0, *s1, *s2, *s3;
+  SC* scales;
   template <int I>
   __device__ __forceinline__ S* get() const {
     if constexpr (I == 0) return s0;
@@ -82,26 +94,37 @@ struct Slots {
 // second half's operands are read, and while the second multiplies, those of the next stage.
 // Between them the stage's reads are complete and its slot is refilled.
 //
-// TAIL: K is not a multiple of 128. Blocks past K are read as zeros (codes and scales), and
-// scales come a byte at a time, since their rows are not whole words.
-template <class S, int WM, int WN, int NW, int NX, int SLOTS, bool TAIL, int MODE>
+// Scales come through registers, ROUND stages of a row at once: a word a row and stage would
+// cost the memory path as many requests as the codes do (a line a lane), and rows of scales need
+// not be whole words. They are requested a round ahead and go to LDS a word a stage.
+//
+// TAIL: K is not a whole number of rounds. Codes and scales past K are zeros.
+template <class R, int WM, int WN, int NW, int NX, bool TAIL, int MODE>
 struct Tile {
+  typedef typename R::Slot S;
+  typedef typename R::Scale SC;
+  static constexpr int SLOTS = R::kCount, ROUND = SC::kRound;
   static constexpr int NT = kWave * WM * WN;  // threads: each load brings in NT / 4 rows
   static constexpr int BN = 32 * NW * WN, BM = 32 * NX * WM;
   static constexpr int kGroupsW = NW, kGroupsX = NX;  // 32-row groups a wave
   static constexpr int kRows = NT / 4;
   static constexpr int kWLoads = BN / kRows, kXLoads = BM < kRows ? 1 : BM / kRows;
-  // 4 waves bring in both kinds of scales one after the other, 8 waves each half its own
+  static constexpr int kOps = kWLoads + kXLoads;  // direct loads a thread and stage
+  // rows of scales a thread fetches: with 8 waves, each half those of one matrix
   static constexpr int kKinds = NT == 2 * kTileRows ? 1 : 2;
-  static constexpr int kOps = kWLoads + kXLoads + (TAIL ? 4 : 1) * kKinds;
-  static_assert(NT == kTileRows || NT == 2 * kTileRows, "a scale word a thread and kind");
+  static_assert(NT == kTileRows || NT == 2 * kTileRows, "a row of scales a thread and kind");
   static_assert(BN >= kRows && BN <= kTileRows && BM <= kTileRows, "whole loads");
   static_assert(MODE != kGateUp || (BN == 256 && NT == 256), "gate rows and up rows in loads of their own");
 
-  Slots<S, SLOTS> st;
-  __amdgpu_buffer_rsrc_t wbuf[MODE == kGateUp ? 2 : 1], xbuf, sbuf[kKinds];
-  int woff[kWLoads], xoff[kXLoads], soff[kKinds];  // byte offsets of this thread at stage 0
-  int to;  // kKinds == 1: words from the stage's weight scales to this wave's
+  R st;
+  __amdgpu_buffer_rsrc_t wbuf[MODE == kGateUp ? 2 : 1], xbuf;
+  int woff[kWLoads], xoff[kXLoads];  // byte offsets of this thread at stage 0
+  const uint8_t* sbase[kKinds];      // scales: the tensor from the tile's first row on,
+  int soff[kKinds], send[kKinds];    // this thread's row in it, and its last 4 ROUND bytes (before
+                                     // its start where it is shorter: only in the workspace)
+  int srow[kKinds];                  // its place in the scale ring (-1: none)
+  uint32_t held[kKinds][ROUND];      // the round that is requested
+  int held_by[kKinds];               // bytes that its words lie further on
   int tid, lane, wave, wm, wn, nk, nb;
   mx_f32x16 acc[NW][NX];
 
@@ -109,17 +132,14 @@ struct Tile {
     i32x4 w[NW], x[NX];
   };
   struct Scales {
-    int w[TAIL ? 2 : 1][NW], x[TAIL ? 2 : 1][NX];
+    int w[NW], x[NX];
   };
 
   __device__ __forceinline__ int block_of() const { return swz(tid >> 2, tid & 3); }
 
-  // SIZE bytes a lane, into LDS in the order of the lanes (1: a word a byte)
-  template <int SIZE>
+  // 16 bytes a lane, into LDS in the order of the lanes
   __device__ __forceinline__ void bring(__amdgpu_buffer_rsrc_t b, void* lds, int off, int at) const {
-    if constexpr (SIZE == 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lptr_t)lds, 16, off, at, 0, 0);
-    if constexpr (SIZE == 4) __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lptr_t)lds, 4, off, at, 0, 0);
-    if constexpr (SIZE == 1) __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lptr_t)lds, 1, off, at, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lptr_t)lds, 16, off, at, 0, 0);
   }
 
   template <int SLOT>
@@ -129,21 +149,40 @@ struct Tile {
     const bool in = !TAIL || 4 * s + block_of() < nb;
 #pragma unroll
     for (int i = 0; i < kWLoads; ++i)
-      bring<16>(wbuf[MODE == kGateUp ? i / 2 : 0], g.w + NT * i + kWave * wave, in ? woff[i] : kOutside,
-                s * kStepBytes);
+      bring(wbuf[MODE == kGateUp ? i / 2 : 0], g.w + NT * i + kWave * wave, in ? woff[i] : kOutside,
+            s * kStepBytes);
 #pragma unroll
     for (int i = 0; i < kXLoads; ++i)
-      bring<16>(xbuf, g.x + NT * i + kWave * wave, in ? xoff[i] : kOutside, s * kStepBytes);
+      bring(xbuf, g.x + NT * i + kWave * wave, in ? xoff[i] : kOutside, s * kStepBytes);
+  }
+
+  // Requests this thread's scales of a round (TAIL: the last bytes of the tensor from where a
+  // whole request ends with them).
+  __device__ __forceinline__ void fetch(int round) {
 #pragma unroll
     for (int t = 0; t < kKinds; ++t) {
+      const int want = soff[t] + 4 * ROUND * min(round, (nk - 1) / ROUND);
+      const int at = TAIL ? min(want, send[t]) : want;
+      if constexpr (TAIL) held_by[t] = want - at;
+      __builtin_memcpy(held[t], sbase[t] + at, 4 * ROUND);
+    }
+  }
+
+  // Stores the requested round.
+  __device__ __forceinline__ void keep(int round) {
 #pragma unroll
-      for (int j = 0; j < (TAIL ? 4 : 1); ++j) {
-        uint32_t* words = kKinds == 1 ? g.ws[j] + to : (t == 0 ? g.ws[j] : g.xs[j]) + kWave * wave;
-        if constexpr (TAIL)
-          bring<1>(sbuf[t], words, 4 * s + j < nb ? soff[t] + j : kOutside, 4 * s);
-        else
-          bring<4>(sbuf[t], words, soff[t], 4 * s);
+    for (int t = 0; t < kKinds; ++t) {
+      if constexpr (TAIL) {
+        static_assert(!TAIL || ROUND == 2, "a round is one 64-bit word");
+        const int there = nb - 8 * round;  // scales of the row from this round on
+        const uint64_t mask = there >= 8 ? ~0ull : there <= 0 ? 0ull : (1ull << (8 * there)) - 1ull;
+        const uint64_t v = ((uint64_t)held[t][1] << 32 | held[t][0]) >> (8 * held_by[t]) & mask;
+        held[t][0] = (uint32_t)v;
+        held[t][1] = (uint32_t)(v >> 32);
       }
+#pragma unroll
+      for (int j = 0; j < ROUND; ++j)
+        if (srow[t] >= 0) st.scales->s[round & 1][j][srow[t]] = held[t][j];
     }
   }
 
@@ -171,28 +210,12 @@ struct Tile {
       __builtin_memcpy(&o.w[q], &g.w[4 * wrow(q) + swz(lane & 31, b)], 16);
   }
 
-  template <int SLOT>
-  __device__ __forceinline__ void scales(Scales& o) const {
-    const S& g = *st.template get<SLOT>();
-    [[maybe_unused]] const int h = lane >> 5;
+  __device__ __forceinline__ void scales(int stage, Scales& o) const {
+    const uint32_t* p = st.scales->s[stage / ROUND & 1][stage % ROUND];
 #pragma unroll
-    for (int q = 0; q < NW; ++q) {
-      if constexpr (TAIL) {
-        o.w[0][q] = (int)g.ws[2 * h][wrow(q)];
-        o.w[1][q] = (int)g.ws[2 * h + 1][wrow(q)];
-      } else {
-        o.w[0][q] = (int)g.ws[0][wrow(q)];
-      }
-    }
+    for (int q = 0; q < NW; ++q) o.w[q] = (int)p[wrow(q)];
 #pragma unroll
-    for (int i = 0; i < NX; ++i) {
-      if constexpr (TAIL) {
-        o.x[0][i] = (int)g.xs[2 * h][xrow(i)];
-        o.x[1][i] = (int)g.xs[2 * h + 1][xrow(i)];
-      } else {
-        o.x[0][i] = (int)g.xs[0][xrow(i)];
-      }
-    }
+    for (int i = 0; i < NX; ++i) o.x[i] = (int)p[BN + xrow(i)];
   }
 
   template <int HALF>
@@ -201,20 +224,17 @@ struct Tile {
     for (int i = 0; i < NX; ++i)
 #pragma unroll
       for (int q = 0; q < NW; ++q)
-        acc[q][i] = mx_mma32<TAIL ? 0 : HALF>(o.w[q], o.x[i], acc[q][i], s.w[TAIL ? HALF : 0][q],
-                                              s.x[TAIL ? HALF : 0][i]);
+        acc[q][i] = mx_mma32<HALF>(o.w[q], o.x[i], acc[q][i], s.w[q], s.x[i]);
   }
 
   // The two scales of this lane's half to the lower half of each word (where the words are used,
   // not where they are read: that would wait for them).
   __device__ __forceinline__ void halve(Scales& o) const {
-    if constexpr (!TAIL) {
-      const int sh = (lane >> 5) * 16;
+    const int sh = (lane >> 5) * 16;
 #pragma unroll
-      for (int q = 0; q < NW; ++q) o.w[0][q] = (int)((uint32_t)o.w[0][q] >> sh);
+    for (int q = 0; q < NW; ++q) o.w[q] = (int)((uint32_t)o.w[q] >> sh);
 #pragma unroll
-      for (int i = 0; i < NX; ++i) o.x[0][i] = (int)((uint32_t)o.x[0][i] >> sh);
-    }
+    for (int i = 0; i < NX; ++i) o.x[i] = (int)((uint32_t)o.x[i] >> sh);
   }
 
   // The operands are in registers at this point: without it the loads of the next stage are
@@ -227,12 +247,9 @@ struct Tile {
   }
   __device__ __forceinline__ static void pin(Scales& o) {
 #pragma unroll
-    for (int t = 0; t < (TAIL ? 2 : 1); ++t) {
+    for (int i = 0; i < NX; ++i) asm volatile("" : "+v"(o.x[i]));
 #pragma unroll
-      for (int i = 0; i < NX; ++i) asm volatile("" : "+v"(o.x[t][i]));
-#pragma unroll
-      for (int q = 0; q < NW; ++q) asm volatile("" : "+v"(o.w[t][q]));
-    }
+    for (int q = 0; q < NW; ++q) asm volatile("" : "+v"(o.w[q]));
   }
 
   // One product, then up to one LDS read and one direct load: the four waves' reads and loads
@@ -240,21 +257,27 @@ struct Tile {
   template <int READS, int LOADS>
   __device__ __forceinline__ static void interleave() {
     constexpr int M = NW * NX;
-    constexpr int R = (READS + M - 1) / M, L = (LOADS + M - 1) / M;
+    constexpr int kReads = (READS + M - 1) / M, kLoads = (LOADS + M - 1) / M;
 #pragma unroll
     for (int i = 0; i < M; ++i) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a matrix-core op
-      __builtin_amdgcn_sched_group_barrier(0x100, R, 0);  // LDS reads
-      if (LOADS) __builtin_amdgcn_sched_group_barrier(0x020, L, 0);  // direct loads
+      __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);  // LDS reads
+      if (LOADS) __builtin_amdgcn_sched_group_barrier(0x020, kLoads, 0);  // direct loads
       __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);  // VALU
     }
   }
 
-  // Stage s in slot SLOT: its first half's operands and its scales are in a and sc.
-  template <int SLOT>
+  // Stage s, s modulo SLOTS = I: its first half's operands and its scales are in a and sc.
+  template <int I>
   __device__ __forceinline__ void step(int s, Ops& a, Scales& sc) {
-    constexpr int NEXT = (SLOT + 1) % SLOTS;
+    constexpr int SLOT = I % SLOTS, NEXT = (I + 1) % SLOTS;
     Ops b;
+    if (SLOTS % ROUND == 0 ? I % ROUND == ROUND - 1 : (s + 1) % ROUND == 0) {
+      // the last stage of a round: the next one to LDS, the one after it requested (before this
+      // stage's barrier, behind which the next stage's scales are read)
+      keep((s + 1) / ROUND);
+      fetch((s + 1) / ROUND + 1);
+    }
     halve(sc);
     read<SLOT, 1>(b);
     multiply<0>(a, sc);
@@ -266,7 +289,7 @@ struct Tile {
     __builtin_amdgcn_sched_barrier(0);
     load<SLOT>(s + SLOTS);
     Scales next;
-    scales<NEXT>(next);
+    scales(s + 1, next);
     read<NEXT, 0>(a);
     multiply<1>(b, sc);
     interleave<2 * (NW + NX), kOps>();
@@ -274,6 +297,18 @@ struct Tile {
     pin(a);
     pin(next);
     sc = next;
+  }
+
+  template <int I>
+  __device__ __forceinline__ void steps(int s, Ops& a, Scales& sc) {
+    step<I>(s + I, a, sc);
+    if constexpr (I + 1 < SLOTS) steps<I + 1>(s, a, sc);
+  }
+  template <int I>
+  __device__ __forceinline__ void rest(int s, Ops& a, Scales& sc) {
+    if (s + I >= nk) return;
+    step<I>(s + I, a, sc);
+    if constexpr (I + 2 < SLOTS) rest<I + 1>(s, a, sc);
   }
 
   template <int SLOT>
@@ -289,39 +324,30 @@ struct Tile {
       for (int i = 0; i < NX; ++i)
 #pragma unroll
         for (int j = 0; j < 16; ++j) acc[q][i][j] = 0.0f;
+    fetch(0);
     first_loads<0>();
+    keep(0);
+    fetch(1);
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the scales are in LDS
     wait_vmcnt<(SLOTS - 1) * kOps>();
     barrier_after_lds_dma();
     Ops a;
     Scales sc;
     read<0, 0>(a);
-    scales<0>(sc);
+    scales(0, sc);
     pin(a);
     pin(sc);
-    // whole rounds of the ring, then the rest: leaving the loop in the middle of a round would
-    // make the compiler drain the ring at the loop's head
-    static_assert(SLOTS >= 2 && SLOTS <= 4, "the steps below");
+    // SLOTS stages at a time, so that slots and places in a round are known, then the rest:
+    // leaving the loop in its middle would make the compiler drain the ring at the loop's head
     int s = 0;
-    for (; s + SLOTS <= nk; s += SLOTS) {
-      step<0>(s, a, sc);
-      step<1>(s + 1, a, sc);
-      if constexpr (SLOTS > 2) step<2 % SLOTS>(s + 2, a, sc);
-      if constexpr (SLOTS > 3) step<3 % SLOTS>(s + 3, a, sc);
-    }
-    if (s < nk) {
-      step<0>(s, a, sc);
-      if (SLOTS > 2 && s + 1 < nk) {
-        step<1>(s + 1, a, sc);
-        if (SLOTS > 3 && s + 2 < nk) step<2 % SLOTS>(s + 2, a, sc);
-      }
-    }
+    for (; s + SLOTS <= nk; s += SLOTS) steps<0>(s, a, sc);
+    rest<0>(s, a, sc);
     wait_vmcnt<0>();  // the loads past the last stage have landed
   }
 
   // e: expert (its weights); n0: first weight row (gate and up: first row of f); m0, rows: this
   // tile's rows of x (gate and up, down: grouped pairs)
-  __device__ __forceinline__ void init(const Slots<S, SLOTS>& slots, const GemmArgs& a, int e, int n0,
-                                       int m0, int rows) {
+  __device__ __forceinline__ void init(const R& slots, const GemmArgs& a, int e, int n0, int m0, int rows) {
     st = slots;
     tid = threadIdx.x;
     lane = tid & (kWave - 1);
@@ -349,20 +375,24 @@ struct Tile {
     };
 #pragma unroll
     for (int i = 0; i < kXLoads; ++i) xoff[i] = source(kRows * i + (tid >> 2)) * codes + 16 * block_of();
+    auto row_of_scales = [&](int t, const uint8_t* base, int64_t tensor_rows, int row, int place) {
+      sbase[t] = base;
+      soff[t] = row * nb;
+      send[t] = (int)min((int64_t)1 << 30, tensor_rows * nb - 4 * ROUND);
+      srow[t] = place;
+    };
     const uint8_t* ws = (MODE == kGateUp && wave >= 2 ? a.s1 : a.s0) + first * nb;
     const uint8_t* xs = a.xs + x0 * nb;
+    const int64_t wleft = a.wrows - (int64_t)first, xleft = a.xrows - (int64_t)x0;
+    const int row = tid % kTileRows;
+    const int wplace = row < BN ? row : -1, xplace = row < BM ? BN + row : -1;
+    const int wr = min(row % kOwn, last), xr = source(min(row, BM - 1));
     if constexpr (kKinds == 1) {
-      const bool x = wave >= 4;
-      const int row = tid % kTileRows;
-      sbuf[0] = buffer_rsrc(x ? xs : ws, kBufferBytes);
-      soff[0] = (x ? source(min(row, BM - 1)) : min(row % kOwn, last)) * nb;
-      to = (x ? (int)((sizeof(S::ws)) / 4) : 0) + kWave * (wave % 4);
+      if (wave < 4) row_of_scales(0, ws, wleft, wr, wplace);
+      else row_of_scales(0, xs, xleft, xr, xplace);
     } else {
-      sbuf[0] = buffer_rsrc(ws, kBufferBytes);
-      soff[0] = min(tid % kOwn, last) * nb;
-      sbuf[1] = buffer_rsrc(xs, kBufferBytes);
-      soff[1] = source(min(tid, BM - 1)) * nb;
-      to = 0;
+      row_of_scales(0, ws, wleft, wr, wplace);
+      row_of_scales(1, xs, xleft, xr, xplace);
     }
   }
 };
@@ -456,11 +486,13 @@ __device__ __forceinline__ void hidden_block(const mx_f32x16& g, const mx_f32x16
 
 // LDS that a wave has for itself once the ring is free: WAVES / SLOTS waves (rounded up, at least
 // two) share a slot.
-template <class S, int WAVES, int SLOTS>
+template <class R, int WAVES>
 struct WaveLds {
+  typedef typename R::Slot S;
+  static constexpr int SLOTS = R::kCount;
   static constexpr int kShare = (WAVES + SLOTS - 1) / SLOTS < 2 ? 2 : (WAVES + SLOTS - 1) / SLOTS;
   static constexpr size_t kBytes = sizeof(S) / kShare / 16 * 16;
-  __device__ static __forceinline__ lds_float* of(const Slots<S, SLOTS>& slots, int wave) {
+  __device__ static __forceinline__ lds_float* of(const R& slots, int wave) {
     uint32_t at = lds_address(slots.s0);
     if (wave / kShare == 1) at = lds_address(slots.s1);
     if (SLOTS > 2 && wave / kShare == 2) at = lds_address(slots.s2);
@@ -579,15 +611,14 @@ __device__ __forceinline__ void rows_epilogue(T& c, const GemmArgs& a, int n0, i
   }
 }
 
-template <class S, int WM, int WN, int NW, int NX, int SLOTS, bool TAIL, int MODE>
-__device__ __forceinline__ void tile(const Slots<S, SLOTS>& slots, const GemmArgs& a, int e, int n0, int m0,
-                                     int rows) {
-  typedef Tile<S, WM, WN, NW, NX, SLOTS, TAIL, MODE> T;
-  typedef WaveLds<S, WM * WN, SLOTS> Lds;
+template <class R, int WM, int WN, int NW, int NX, bool TAIL, int MODE>
+__device__ __forceinline__ void tile(const R& ring, const GemmArgs& a, int e, int n0, int m0, int rows) {
+  typedef Tile<R, WM, WN, NW, NX, TAIL, MODE> T;
+  typedef WaveLds<R, WM * WN> Lds;
   T c;
-  c.init(slots, a, e, n0, m0, rows);
+  c.init(ring, a, e, n0, m0, rows);
   c.run();
-  lds_float* lds = Lds::of(slots, c.wave);
+  lds_float* lds = Lds::of(ring, c.wave);
   if constexpr (MODE == kGateUp) {
     static_assert(Lds::kBytes >= 32 * kWave * 4, "a block's gate and up sums");
     gateup_epilogue(c, a, n0, m0, rows, lds);
@@ -597,100 +628,132 @@ __device__ __forceinline__ void tile(const Slots<S, SLOTS>& slots, const GemmArg
   }
 }
 
-// M-tile mt of the list runs on XCD mt % 8, which takes its column tiles one after another (they
-// share the rows of x in that XCD's L2).
-__device__ __forceinline__ bool list_tile(int ntiles, int ntn, int& mt, int& nt) {
-  const int slot = (int)(blockIdx.x / 8);
-  mt = (int)(blockIdx.x % 8) + 8 * (slot / ntn);
+// Workgroups are dealt to the 8 XCDs round robin. Each XCD has a run of the tile list, whose
+// tiles of one expert are neighbours, and takes a tile's column tiles one after another: the
+// tiles of an expert then read its weights, and a tile's workgroups its rows of x, through one
+// L2. (Dealt out tile by tile, every tile fetched its weights from the memory-side cache, which
+// bounded the product at about 4.6 TB/s: gate and up of 64 experts with 1024 rows each, 197 us.)
+constexpr int kXcds = 8;
+
+__device__ __forceinline__ bool list_tile(const int* xcd_first, int ntn, int& mt, int& nt) {
+  const int x = (int)blockIdx.x % kXcds, slot = (int)blockIdx.x / kXcds;
+  mt = load_uniform(xcd_first + x) + slot / ntn;
   nt = slot % ntn;
-  return mt < ntiles;
+  return mt < load_uniform(xcd_first + x + 1);
 }
 
-// The grouped product: 256 weight rows by up to 128 pairs.
+// Linear: an XCD has a rectangle of tiles and takes it in panels, so that the workgroups that
+// run at once share rows and columns about evenly.
+__device__ __forceinline__ bool grid_tile(const GemmArgs& a, int mtiles, int ntiles, int& mt, int& nt) {
+  const int x = (int)blockIdx.x % kXcds;
+  int slot = (int)blockIdx.x / kXcds;
+  const int per = a.xcd_rm * a.panel, p = slot / per;
+  slot -= p * per;
+  const int width = min(a.panel, a.xcd_rn - p * a.panel);
+  mt = x % a.xcd_m * a.xcd_rm + slot / width;
+  nt = x / a.xcd_m * a.xcd_rn + p * a.panel + slot % width;
+  return mt < mtiles && nt < ntiles;
+}
+
+// The grouped product: 256 weight rows by up to 128 pairs. Two workgroups a CU: 80 KB of LDS.
 template <bool TAIL, int MODE>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(TAIL ? 1 : 2, 2))) void k_mx_grouped(GemmArgs a) {
-  typedef Stage<256, 128, TAIL> S;
-  constexpr int SLOTS = TAIL ? 2 : 3;
-  __shared__ S slot0, slot1;
-  Slots<S, SLOTS> slots{&slot0, &slot1, nullptr, nullptr};
-  if constexpr (SLOTS == 3) {
-    __shared__ S slot2;
-    slots.s2 = &slot2;
-  }
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_mx_grouped(GemmArgs a) {
+  typedef Stage<256, 128> S;
+  typedef ScaleRing<256, 128, 2> SC;
+  __shared__ S slot0, slot1, slot2;
+  __shared__ SC scales;
+  const Slots<S, SC, 3> ring{&slot0, &slot1, &slot2, nullptr, &scales};
   constexpr int kN = MODE == kGateUp ? 128 : 256;  // rows of f, or of d, a workgroup
   const int ntn = (a.N + kN - 1) / kN;
   int mt, nt;
-  if (!list_tile(load_uniform(a.ntiles), ntn, mt, nt)) return;
+  if (!list_tile(a.xcd_first, ntn, mt, nt)) return;
   const int4 t = load_uniform(a.tiles + mt);
   if (t.z <= 32)
-    tile<S, 1, 4, 2, 1, SLOTS, TAIL, MODE>(slots, a, t.x, nt * kN, t.y, t.z);
+    tile<Slots<S, SC, 3>, 1, 4, 2, 1, TAIL, MODE>(ring, a, t.x, nt * kN, t.y, t.z);
   else if (t.z <= 64)
-    tile<S, 1, 4, 2, 2, SLOTS, TAIL, MODE>(slots, a, t.x, nt * kN, t.y, t.z);
+    tile<Slots<S, SC, 3>, 1, 4, 2, 2, TAIL, MODE>(ring, a, t.x, nt * kN, t.y, t.z);
   else
-    tile<S, 1, 4, 2, 4, SLOTS, TAIL, MODE>(slots, a, t.x, nt * kN, t.y, t.z);
+    tile<Slots<S, SC, 3>, 1, 4, 2, 4, TAIL, MODE>(ring, a, t.x, nt * kN, t.y, t.z);
 }
 
-template <int WM, int WN, int NW, int NX, int SLOTS, bool TAIL>
+template <int WM, int WN, int NW, int NX, bool TAIL>
 __global__ __launch_bounds__(kWave * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_mx_linear(
     GemmArgs a) {
   constexpr int BN = 32 * NW * WN, BM = 32 * NX * WM;
-  typedef Stage<BN, BM, TAIL> S;
-  __shared__ S slot0, slot1;
-  Slots<S, SLOTS> slots{&slot0, &slot1, nullptr, nullptr};
-  if constexpr (SLOTS > 2) {
-    __shared__ S slot2;
-    slots.s2 = &slot2;
-  }
-  if constexpr (SLOTS > 3) {
-    __shared__ S slot3;
-    slots.s3 = &slot3;
-  }
+  typedef Stage<BN, BM> S;
+  typedef ScaleRing<BN, BM, TAIL ? 2 : 4> SC;
+  __shared__ S slot0, slot1, slot2, slot3;
+  __shared__ SC scales;
+  const Slots<S, SC, 4> ring{&slot0, &slot1, &slot2, &slot3, &scales};
   const int ntn = (a.N + BN - 1) / BN;
   int mt, nt;
-  if (!list_tile((a.rows + BM - 1) / BM, ntn, mt, nt)) return;
-  tile<S, WM, WN, NW, NX, SLOTS, TAIL, kLinear>(slots, a, 0, nt * BN, mt * BM, min(BM, a.rows - mt * BM));
+  if (!grid_tile(a, (a.rows + BM - 1) / BM, ntn, mt, nt)) return;
+  tile<Slots<S, SC, 4>, WM, WN, NW, NX, TAIL, kLinear>(ring, a, 0, nt * BN, mt * BM,
+                                                              min(BM, a.rows - mt * BM));
 }
 
 // ---------------------------------------------------------------- work list
 
-// One workgroup, one thread an expert: every full tile in expert order, then the partly filled
-// ones by the rows they compute (128, 64, 32), so that the longest start first.
-__global__ __launch_bounds__(1024) void k_mx_tiles(const int32_t* __restrict__ offsets, int E,
-                                                   int4* __restrict__ tiles, int* __restrict__ ntiles) {
-  __shared__ int s_wsum[16];
-  __shared__ int s_total;
+// A tile costs its weights (4) and its groups of 32 rows (1 each), in the units of the split of
+// the list over the XCDs. Both are read from the measured times of 64 experts with full tiles and
+// of 490 experts with a few rows each.
+constexpr int kTileCost = 4;
+
+// Inclusive scan over the workgroup (1024 threads) of two values at once.
+__device__ __forceinline__ int2 block_scan(int2 v, int2* wsum) {
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-  const int beg = tid < E ? offsets[tid] : 0;
-  const int m = tid < E ? offsets[tid + 1] - beg : 0;
-  const int nfull = m / kMxBM, rem = m - nfull * kMxBM;
-  const int cls = rem == 0 ? -1 : rem > 64 ? 0 : rem > 32 ? 1 : 2;
-  int start = 0;
-  auto place = [&](int v) {
-    int incl = v;
 #pragma unroll
-    for (int off = 1; off < kWave; off <<= 1) {
-      const int o = __shfl_up(incl, off);
-      if (lane >= off) incl += o;
-    }
-    if (lane == kWave - 1) s_wsum[wave] = incl;
-    __syncthreads();
-    int base = incl - v;
-    for (int w = 0; w < wave; ++w) base += s_wsum[w];
-    if (tid == 1023) s_total = base + v;
-    __syncthreads();
-    const int pos = start + base;
-    start += s_total;
-    __syncthreads();
-    return pos;
-  };
-  const int fb = place(nfull);
-  for (int i = 0; i < nfull; ++i) tiles[fb + i] = make_int4(tid, beg + i * kMxBM, kMxBM, 0);
-#pragma unroll
-  for (int c = 0; c < 3; ++c) {
-    const int pb = place(cls == c ? 1 : 0);
-    if (cls == c) tiles[pb] = make_int4(tid, beg + nfull * kMxBM, rem, 0);
+  for (int off = 1; off < kWave; off <<= 1) {
+    const int a = __shfl_up(v.x, off), b = __shfl_up(v.y, off);
+    if (lane >= off) v.x += a, v.y += b;
   }
-  if (tid == 0) *ntiles = start;
+  if (lane == kWave - 1) wsum[wave] = v;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) v.x += wsum[w].x, v.y += wsum[w].y;
+  __syncthreads();
+  return v;
+}
+
+// One workgroup: tiles in expert order, and the XCDs' shares of their cost. A thread finds an
+// expert's first tile; then the threads write the tiles, each looking its expert up.
+__global__ __launch_bounds__(1024) void k_mx_tiles(const int32_t* __restrict__ offsets, int E,
+                                                   int4* __restrict__ tiles, int* __restrict__ xcd_first) {
+  __shared__ int2 s_wsum[16];
+  __shared__ int s_first[1024], s_cost[1024], s_beg[1025];
+  __shared__ int2 s_total;
+  const int tid = threadIdx.x;
+  const int beg = offsets[min(tid, E)];
+  const int m = tid < E ? offsets[tid + 1] - beg : 0;
+  const int count = (m + kMxBM - 1) / kMxBM;
+  const int2 mine = make_int2(count, kTileCost * count + (m + 31) / 32);
+  const int2 incl = block_scan(mine, s_wsum);
+  s_first[tid] = incl.x - mine.x;
+  s_cost[tid] = incl.y - mine.y;
+  s_beg[tid] = beg;
+  if (tid == 1023) s_total = incl, s_beg[1024] = offsets[E];
+  __syncthreads();
+  const int ntiles = s_total.x, total = s_total.y;
+  for (int j = tid; j < ntiles; j += 1024) {
+    int lo = 0, hi = E - 1;  // the last expert whose first tile is not behind j
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (s_first[mid] <= j) lo = mid;
+      else hi = mid - 1;
+    }
+    const int i = j - s_first[lo], g0 = s_beg[lo] + i * kMxBM;
+    const int rows = min(kMxBM, s_beg[lo + 1] - g0);
+    tiles[j] = make_int4(lo, g0, rows, 0);
+    // XCD x starts at the first tile whose cost before it is x / 8 of the whole or more
+    const int cost = s_cost[lo] + i * (kTileCost + kMxBM / 32);
+    const int next = cost + kTileCost + (rows + 31) / 32;
+#pragma unroll
+    for (int x = 0; x < kXcds; ++x) {
+      const long long at = (long long)x * total;
+      if (at == (long long)cost * kXcds) xcd_first[x] = j;
+      else if (at > (long long)cost * kXcds && at < (long long)next * kXcds) xcd_first[x] = j + 1;
+    }
+  }
+  if (tid <= kXcds && (tid == kXcds || ntiles == 0)) xcd_first[tid] = ntiles;
 }
 
 // ---------------------------------------------------------------- combine
@@ -727,29 +790,52 @@ __global__ __launch_bounds__(1024) void k_mx_combine(const float* __restrict__ y
   }
 }
 
-inline int list_grid(int max_mt, int ntn) { return (max_mt + 7) / 8 * 8 * ntn; }
+// Workgroups that cover the tiles of any XCD: its share of the cost is at most an eighth of the
+// whole and one tile, a tile costs kTileCost + 1 to kTileCost + 4.
+inline int list_grid(int max_mt, int ntn) {
+  const int most = ((kTileCost + 4) * ((max_mt + kXcds - 1) / kXcds + 1)) / (kTileCost + 1) + 2;
+  return kXcds * std::min(max_mt, most) * ntn;
+}
 
-template <int WM, int WN, int NW, int NX, int SLOTS, int TSLOTS>
-void linear(const GemmArgs& g, hipStream_t stream) {
+// Splits the tiles over the XCDs: the split that leaves the largest share smallest, of those the
+// one whose shares are the most square.
+template <int WM, int WN, int NW, int NX>
+void linear(GemmArgs g, hipStream_t stream) {
   constexpr int BN = 32 * NW * WN, BM = 32 * NX * WM;
-  const dim3 grid(list_grid((g.rows + BM - 1) / BM, (g.N + BN - 1) / BN)), block(kWave * WM * WN);
-  if (g.K % 128 == 0)
-    hipLaunchKernelGGL((k_mx_linear<WM, WN, NW, NX, SLOTS, false>), grid, block, 0, stream, g);
+  const int mt = (g.rows + BM - 1) / BM, nt = (g.N + BN - 1) / BN;
+  long long best = 0, border = 0;
+  for (int m = 1; m <= kXcds; m *= 2) {
+    const long long rm = (mt + m - 1) / m, rn = (nt + kXcds / m - 1) / (kXcds / m);
+    if (best == 0 || rm * rn < best || (rm * rn == best && rm * BM + rn * BN < border)) {
+      best = rm * rn;
+      border = rm * BM + rn * BN;
+      g.xcd_m = m;
+      g.xcd_rm = (int)rm;
+      g.xcd_rn = (int)rn;
+    }
+  }
+  // about 32 workgroups of an XCD run at once
+  g.panel = std::max(1, std::min(g.xcd_rn, (32 + g.xcd_rm - 1) / g.xcd_rm));
+  const dim3 grid((unsigned)(kXcds * best)), block(kWave * WM * WN);
+  if (g.K % 512 == 0)
+    hipLaunchKernelGGL((k_mx_linear<WM, WN, NW, NX, false>), grid, block, 0, stream, g);
   else
-    hipLaunchKernelGGL((k_mx_linear<WM, WN, NW, NX, TSLOTS, true>), grid, block, 0, stream, g);
+    hipLaunchKernelGGL((k_mx_linear<WM, WN, NW, NX, true>), grid, block, 0, stream, g);
 }
 
 }  // namespace
 
 hipError_t launch_mx_linear(const MxLinearArgs& a, hipStream_t stream) {
   if (a.n == 0) return hipSuccess;
-  if (mx_linear_window(a.n, a.K)) return launch_mx_linear_window(a, stream);
+  if (mx_linear_window(a.n, a.N, a.K)) return launch_mx_linear_window(a, stream);
   GemmArgs g{};
   g.w0 = a.w;
   g.s0 = a.ws;
   g.xq = a.xq;
   g.xs = a.xs;
   g.rows = a.n;
+  g.wrows = a.N;
+  g.xrows = a.n;
   g.N = a.N;
   g.K = a.K;
   g.out = a.out;
@@ -765,9 +851,9 @@ hipError_t launch_mx_linear(const MxLinearArgs& a, hipStream_t stream) {
     g.xs = xs;
   }
   if ((long long)a.n * a.N <= 1024ll * 1024)
-    linear<1, 4, 1, 2, 4, 3>(g, stream);
+    linear<1, 4, 1, 2>(g, stream);
   else
-    linear<2, 4, 2, 4, 4, 3>(g, stream);
+    linear<2, 4, 2, 4>(g, stream);
   return hipGetLastError();
 }
 
@@ -783,8 +869,9 @@ hipError_t launch_mx_ffn(const MxFfnArgs& a, hipStream_t stream) {
   uint8_t* hs = reinterpret_cast<uint8_t*>(a.work + W.hs);
   float* y = reinterpret_cast<float*>(a.work + W.y);
   int4* tiles = reinterpret_cast<int4*>(a.work + W.tiles);
-  int* ntiles = reinterpret_cast<int*>(a.work + W.ntiles);
-  hipLaunchKernelGGL(k_mx_tiles, dim3(1), dim3(1024), 0, stream, a.r->expert_offsets, E, tiles, ntiles);
+  int* xcd_first = reinterpret_cast<int*>(a.work + W.xcd_first);
+  hipLaunchKernelGGL(k_mx_tiles, dim3(1), dim3(1024), 0, stream, a.r->expert_offsets, E, tiles,
+                     xcd_first);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   err = launch_mx_quantize(MxQuantArgs{a.x, a.dtype, n, a.row_stride, d, xq, xs}, stream);
@@ -794,7 +881,7 @@ hipError_t launch_mx_ffn(const MxFfnArgs& a, hipStream_t stream) {
   GemmArgs g{};
   g.pair_index = a.r->pair_index;
   g.tiles = tiles;
-  g.ntiles = ntiles;
+  g.xcd_first = xcd_first;
   g.k = k;
   g.w0 = L.gate.codes;
   g.s0 = L.gate.scales;
@@ -804,10 +891,12 @@ hipError_t launch_mx_ffn(const MxFfnArgs& a, hipStream_t stream) {
   g.xs = xs;
   g.N = f;
   g.K = d;
+  g.wrows = (int64_t)E * f;
+  g.xrows = n;
   g.hq = hq;
   g.hs = hs;
   const dim3 gu(list_grid(max_mt, (f + 127) / 128));
-  if (d % 128 == 0)
+  if (d % 256 == 0)
     hipLaunchKernelGGL((k_mx_grouped<false, kGateUp>), gu, dim3(kThreads), 0, stream, g);
   else
     hipLaunchKernelGGL((k_mx_grouped<true, kGateUp>), gu, dim3(kThreads), 0, stream, g);
@@ -820,9 +909,11 @@ hipError_t launch_mx_ffn(const MxFfnArgs& a, hipStream_t stream) {
   g.xs = hs;
   g.N = d;
   g.K = f;
+  g.wrows = (int64_t)E * d;
+  g.xrows = P;
   g.out = y;
   const dim3 dn(list_grid(max_mt, (d + 255) / 256));
-  if (f % 128 == 0)
+  if (f % 256 == 0)
     hipLaunchKernelGGL((k_mx_grouped<false, kDown>), dn, dim3(kThreads), 0, stream, g);
   else
     hipLaunchKernelGGL((k_mx_grouped<true, kDown>), dn, dim3(kThreads), 0, stream, g);

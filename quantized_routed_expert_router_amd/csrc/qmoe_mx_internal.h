@@ -219,11 +219,15 @@ constexpr int kMxWindowPairs = 256;
 inline bool mx_window(int n, int k) { return n <= kMxWindowTokens && n * k <= kMxWindowPairs; }
 
 // Whether a linear product runs on the window kernel: the rows to multiply are then quantized in
-// LDS (up to 70 KB at 16 rows of 8192) and need no workspace.
-inline bool mx_linear_window(int n, int K) { return n <= kMxWindowTokens && K <= 8192; }
+// LDS (up to 70 KB at 16 rows of 8192) and need no workspace. Weights with fewer than 16 scales
+// in all run there too: the tiles fetch 16 at once.
+inline bool mx_linear_window(int n, int N, int K) {
+  return (n <= kMxWindowTokens && K <= 8192) || (int64_t)N * (K / kMxBlock) < 16;
+}
 
+// Workspace of a linear product: the same for every N, which the query is not told.
 inline size_t mx_linear_ws(int n, int K) {
-  if (n == 0 || mx_linear_window(n, K)) return 0;
+  if (n == 0 || (n <= kMxWindowTokens && K <= 8192)) return 0;
   return align256((size_t)n * (K / 2)) + align256((size_t)n * (K / kMxBlock));
 }
 
@@ -237,7 +241,7 @@ inline int mx_max_mtiles(int P, int E) {
 
 struct MxFfnWs {
   size_t tiles;   // int4 [max M-tiles] (expert, first grouped pair, pairs, 0)
-  size_t ntiles;  // int [1]
+  size_t xcd_first;  // int [9] first tile of each XCD, and their number
   size_t xq, xs;  // codes and scales of x [n]
   size_t hq, hs;  // codes and scales of the hidden rows [P]
   size_t y;       // fp32 [P][d]
@@ -251,8 +255,8 @@ inline MxFfnWs mx_ffn_ws(int n, int k, int d, int f, int E) {
   const bool window = mx_window(n, k);
   W.tiles = o;
   if (!window) o = align256(o + 16 * (size_t)(mx_max_mtiles((int)P, E) + 1));
-  W.ntiles = o;
-  if (!window) o = align256(o + 16);
+  W.xcd_first = o;
+  if (!window) o = align256(o + 64);
   W.xq = o;
   if (!window) o = align256(o + (size_t)n * (d / 2));
   W.xs = o;
