@@ -1,6 +1,7 @@
-// Short path of the attention half's Python calls: checks of the tensors, output
-// allocation and the C ABI call in one native step. The kernels behind these calls run for
-// a few microseconds, less than the same checks take in Python.
+// Short path of the Python calls of the attention half, of routing by a rule and of the
+// microscaled products: checks of the tensors, output allocation and the C ABI call in one
+// native step. The kernels behind these calls run for a few microseconds, less than the same
+// checks take in Python.
 //
 // Every function answers None when an argument is not exactly what the call needs (the
 // Python side then checks one by one and says which), the status of the C call when it is
@@ -11,6 +12,8 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
+
+#include <algorithm>
 
 #include "qmoe.h"
 
@@ -287,13 +290,236 @@ PyObject* attend(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
+// ---- routing by a rule and microscaled products
+
+int float_of(const Tensor& t) {
+  switch (t.scalar_type()) {
+    case at::kFloat:
+      return MOE_F32;
+    case at::kBFloat16:
+      return MOE_BF16;
+    case at::kHalf:
+      return MOE_F16;
+    default:
+      throw Mismatch();
+  }
+}
+
+at::ScalarType type_of(int dtype) {
+  return dtype == MOE_F32 ? at::kFloat : dtype == MOE_BF16 ? at::kBFloat16 : at::kHalf;
+}
+
+// Rows [n, cols] of floats, the last axis contiguous, and their stride.
+const Tensor& rows_of(Args& a, int64_t cols, int64_t* stride) {
+  const Tensor& t = a.required();
+  float_of(t);
+  if (t.dim() != 2 || (cols >= 0 && t.size(1) != cols) || t.size(0) > MOE_MAX_ROUTE_TOKENS ||
+      t.size(1) > MOE_MX_MAX_COLS || (t.size(1) > 1 && t.stride(1) != 1))
+    throw Mismatch();
+  *stride = t.size(0) > 1 ? t.stride(0) : t.size(1);
+  return t;
+}
+
+// Codes and scales of a matrix of `dims` axes.
+moe_mx_matrix mx_of(Args& a, int dims, const Tensor** codes_out) {
+  const Tensor &c = a.required(), &s = a.required();
+  if (c.scalar_type() != at::kByte || s.scalar_type() != at::kByte || c.dim() != dims || s.dim() != dims ||
+      !c.is_contiguous() || !s.is_contiguous())
+    throw Mismatch();
+  const int64_t half = c.size(dims - 1), rows = c.size(dims - 2);
+  if (half % 16 || half < 16 || half > MOE_MX_MAX_COLS / 2 || rows < 1 || rows > MOE_MX_MAX_ROWS ||
+      s.size(dims - 1) != half / 16)
+    throw Mismatch();
+  for (int i = 0; i + 1 < dims; ++i)
+    if (s.size(i) != c.size(i)) throw Mismatch();
+  if (codes_out) *codes_out = &c;
+  return moe_mx_matrix{(const uint8_t*)c.data_ptr(), (const uint8_t*)s.data_ptr(), (int32_t)rows,
+                       (int32_t)(2 * half)};
+}
+
+// (device, logits, top_k, score, bias, groups, top_groups, group_score, renormalize, scale, stream)
+// -> (topk_ids, topk_w, expert_offsets, pair_index)
+PyObject* route_scored(PyObject*, PyObject* const* args, Py_ssize_t n_args) {
+  return guarded(args, n_args, [](Args& a) -> PyObject* {
+    const Tensor& l = a.required();
+    const int dtype = float_of(l);
+    if (l.dim() != 2 || !l.is_contiguous() || l.size(0) > MOE_MAX_ROUTE_TOKENS || l.size(1) > MOE_MAX_EXPERTS)
+      throw Mismatch();
+    const int n = (int)l.size(0), E = (int)l.size(1), k = a.integer();
+    if (k < 1 || k > E || k > MOE_MAX_TOP_K) throw Mismatch();
+    moe_route_rule rule{};
+    rule.score = a.integer();
+    rule.bias = (const float*)a.vector(at::kFloat, E);
+    rule.groups = a.integer();
+    rule.top_groups = a.integer();
+    rule.group_score = a.integer();
+    rule.renormalize = a.integer();
+    rule.scale = (float)a.number();
+    void* stream = a.stream();
+    Tensor out[4];
+    moe_status s;
+    {
+      const WithoutGil free;
+      const auto ints = l.options().dtype(at::kInt);
+      out[0] = at::empty({n, k}, ints);
+      out[1] = at::empty({n, k}, l.options().dtype(at::kFloat));
+      out[2] = at::empty({E + 1}, ints);
+      out[3] = at::empty({std::max(n * k, 1)}, ints);
+      const moe_routing r{(int32_t*)out[0].data_ptr(), (float*)out[1].data_ptr(),
+                          (int32_t*)out[2].data_ptr(), (int32_t*)out[3].data_ptr()};
+      const size_t need = moe_route_workspace_bytes(n, E, k);
+      Tensor ws;
+      if (need) ws = at::empty({(int64_t)need}, l.options().dtype(at::kByte));
+      s = moe_route_scored(l.data_ptr(), dtype, n, E, k, &rule, &r, need ? ws.data_ptr() : nullptr, need,
+                           stream);
+    }
+    if (s != MOE_OK) return PyLong_FromLong(s);
+    PyObject* all = PyTuple_New(4);
+    if (!all) return nullptr;
+    for (int i = 0; i < 4; ++i) PyTuple_SET_ITEM(all, i, THPVariable_Wrap(std::move(out[i])));
+    return all;
+  });
+}
+
+// (device, x, stream) -> (codes, scales)
+PyObject* mx_quantize(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded(args, n, [](Args& a) -> PyObject* {
+    int64_t stride;
+    const Tensor& x = rows_of(a, -1, &stride);
+    const int64_t rows = x.size(0), cols = x.size(1);
+    if (cols < 32 || cols % 32) throw Mismatch();
+    void* stream = a.stream();
+    Tensor codes, scales;
+    moe_status s;
+    {
+      const WithoutGil free;
+      const auto bytes = x.options().dtype(at::kByte);
+      codes = at::empty({rows, cols / 2}, bytes);
+      scales = at::empty({rows, cols / 32}, bytes);
+      s = moe_mx_quantize(x.data_ptr(), float_of(x), rows, (int)cols, stride, (uint8_t*)codes.data_ptr(),
+                          (uint8_t*)scales.data_ptr(), stream);
+    }
+    if (s != MOE_OK) return PyLong_FromLong(s);
+    PyObject* pair = PyTuple_New(2);
+    if (!pair) return nullptr;
+    PyTuple_SET_ITEM(pair, 0, THPVariable_Wrap(std::move(codes)));
+    PyTuple_SET_ITEM(pair, 1, THPVariable_Wrap(std::move(scales)));
+    return pair;
+  });
+}
+
+// (device, codes, scales, dtype, stream) -> values
+PyObject* mx_dequantize(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded(args, n, [](Args& a) -> PyObject* {
+    const Tensor* codes;
+    const moe_mx_matrix m = mx_of(a, 2, &codes);
+    const int dtype = a.integer();
+    if (dtype != MOE_F32 && dtype != MOE_BF16 && dtype != MOE_F16) throw Mismatch();
+    void* stream = a.stream();
+    Tensor out;
+    moe_status s;
+    {
+      const WithoutGil free;
+      out = at::empty({m.rows, m.cols}, codes->options().dtype(type_of(dtype)));
+      s = moe_mx_dequantize(&m, m.rows, dtype, out.data_ptr(), stream);
+    }
+    if (s != MOE_OK) return PyLong_FromLong(s);
+    return THPVariable_Wrap(std::move(out));
+  });
+}
+
+// (device, x, w codes, w scales, dtype, stream) -> out
+PyObject* mx_linear(PyObject*, PyObject* const* args, Py_ssize_t n_args) {
+  return guarded(args, n_args, [](Args& a) -> PyObject* {
+    int64_t stride;
+    const Tensor& x = rows_of(a, -1, &stride);
+    const moe_mx_matrix w = mx_of(a, 2, nullptr);
+    if (x.size(1) != w.cols) throw Mismatch();
+    const int dtype = a.integer();
+    if (dtype != MOE_F32 && dtype != MOE_BF16 && dtype != MOE_F16) throw Mismatch();
+    void* stream = a.stream();
+    const int n = (int)x.size(0);
+    Tensor out;
+    moe_status s;
+    {
+      const WithoutGil free;
+      out = at::empty({n, w.rows}, x.options().dtype(type_of(dtype)));
+      const size_t need = moe_mx_linear_workspace_bytes(n, w.cols);
+      Tensor ws;
+      if (need) ws = at::empty({(int64_t)need}, x.options().dtype(at::kByte));
+      s = moe_mx_linear(x.data_ptr(), float_of(x), stride, n, &w, out.data_ptr(), dtype, w.rows,
+                        need ? ws.data_ptr() : nullptr, need, stream);
+    }
+    if (s != MOE_OK) return PyLong_FromLong(s);
+    return THPVariable_Wrap(std::move(out));
+  });
+}
+
+// (device, gate codes, scales, up codes, scales, down codes, scales, top_k, x, topk_ids, topk_w,
+// expert_offsets, pair_index, residual or None, out or None, stream) -> out
+PyObject* mx_ffn(PyObject*, PyObject* const* args, Py_ssize_t n_args) {
+  return guarded(args, n_args, [](Args& a) -> PyObject* {
+    const Tensor *gate, *up, *down;
+    moe_mx_layer L{};
+    L.gate = mx_of(a, 3, &gate);
+    L.up = mx_of(a, 3, &up);
+    L.down = mx_of(a, 3, &down);
+    if (gate->size(0) > MOE_MAX_EXPERTS || up->size(0) != gate->size(0) || down->size(0) != gate->size(0) ||
+        L.up.rows != L.gate.rows || L.up.cols != L.gate.cols || L.down.rows != L.gate.cols ||
+        L.down.cols != L.gate.rows)
+      throw Mismatch();
+    L.n_experts = (int32_t)gate->size(0);
+    L.d_ff = L.gate.rows;
+    L.d_model = L.gate.cols;
+    L.top_k = a.integer();
+    int64_t stride;
+    const Tensor& x = rows_of(a, L.d_model, &stride);
+    const int64_t n = x.size(0);
+    auto routing = [&](at::ScalarType type, int64_t least) {
+      const Tensor& t = a.required();
+      if (t.scalar_type() != type || t.numel() < least || !t.is_contiguous()) throw Mismatch();
+      return t.data_ptr();
+    };
+    moe_routing r;
+    r.topk_ids = (int32_t*)routing(at::kInt, n * L.top_k);
+    r.topk_w = (float*)routing(at::kFloat, n * L.top_k);
+    r.expert_offsets = (int32_t*)routing(at::kInt, L.n_experts + 1);
+    r.pair_index = (int32_t*)routing(at::kInt, n * L.top_k);
+    auto stream_rows = [&]() -> const Tensor* {
+      const Tensor* t = a.tensor();
+      if (t && (t->scalar_type() != at::kFloat || t->dim() != 2 || t->size(0) != n ||
+                t->size(1) != L.d_model || !t->is_contiguous()))
+        throw Mismatch();
+      return t;
+    };
+    const Tensor* residual = stream_rows();
+    const Tensor* given = stream_rows();
+    void* stream = a.stream();
+    Tensor out;
+    moe_status s;
+    {
+      const WithoutGil free;
+      out = given ? *given : at::empty({n, L.d_model}, x.options().dtype(at::kFloat));
+      const size_t need = moe_mx_ffn_workspace_bytes(&L, (int)n);
+      Tensor ws;
+      if (need) ws = at::empty({(int64_t)need}, x.options().dtype(at::kByte));
+      s = moe_mx_ffn(&L, x.data_ptr(), float_of(x), stride, (int)n, &r,
+                     residual ? (const float*)residual->data_ptr() : nullptr, (float*)out.data_ptr(),
+                     need ? ws.data_ptr() : nullptr, need, stream);
+    }
+    if (s != MOE_OK) return PyLong_FromLong(s);
+    return THPVariable_Wrap(std::move(out));
+  });
+}
+
 #define ENTRY(name) \
   { #name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr }
-PyMethodDef methods[] = {ENTRY(qk_norm_rope), ENTRY(kv_append), ENTRY(attend),
+PyMethodDef methods[] = {ENTRY(qk_norm_rope), ENTRY(kv_append), ENTRY(attend), ENTRY(route_scored),
+                         ENTRY(mx_quantize),  ENTRY(mx_dequantize), ENTRY(mx_linear), ENTRY(mx_ffn),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall",
-                      "Short path of the attention half's calls.", -1, methods,
+                      "Short path of the calls whose kernels run for a few microseconds.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,7 +1,9 @@
 """Python binding of the microscaled 4-bit products of libqmoe (C ABI in include/qmoe.h):
 quantization of rows, products with 4-bit matrices, and the routed-expert layer in them.
 
-Argument marshalling only, as in `qmoe`. Every call works on the GPU of its tensors (made
+Argument marshalling only, as in `qmoe`. The usual calls (nothing given for workspace and
+stream, tensors on the current device) go through a native short path with the same checks;
+whatever it does not take is checked and marshalled here. Every call works on the GPU of its tensors (made
 current for the call when it is not) and on that GPU's current stream, or on `stream`;
 outputs and workspaces that a call makes for itself belong to that stream.
 """
@@ -12,7 +14,8 @@ from dataclasses import dataclass
 
 import torch
 
-from .qmoe import BYTES, F32, FLOATS, MOE_OK, MoeError, Routing, _Args, _ptr, _Routing, lib
+from .qmoe import (BYTES, F32, FLOATS, MOE_OK, MoeError, Routing, _Args, _current_device, _fastcall,
+                   _ptr, _raw_stream, _Routing, lib)
 
 BLOCK = 32  # values that share a scale
 U8 = (torch.uint8,)
@@ -148,9 +151,21 @@ def _done(fn: str, rc: int) -> None:
         raise MoeError(fn, rc)
 
 
+def _result(fn: str, r):
+    """What a call on the short path returns, or its error."""
+    if type(r) is int:
+        raise MoeError(fn, r)
+    return r
+
+
 def quantize(x: torch.Tensor, out: MxMatrix | None = None, stream=None) -> MxMatrix:
     """moe_mx_quantize: x ``[..., rows, cols]`` (fp32, bf16 or fp16; contiguous, or two axes with
     a row stride) in 4 bits. A new matrix unless `out` is given."""
+    if stream is None and out is None and type(x) is torch.Tensor and x.is_cuda:
+        gpu = _current_device()
+        r = _fastcall.mx_quantize(gpu, x, _raw_stream(gpu))
+        if r is not None:
+            return MxMatrix(*_result("moe_mx_quantize", r))
     args = _RowArgs()
     if isinstance(x, torch.Tensor) and x.dim() == 2:
         stride = args.rows(x, "x", FLOATS)
@@ -177,6 +192,11 @@ def quantize(x: torch.Tensor, out: MxMatrix | None = None, stream=None) -> MxMat
 def dequantize(m: MxMatrix, dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None,
                stream=None) -> torch.Tensor:
     """moe_mx_dequantize: the values of `m` as fp32, bf16 or fp16 ``[..., rows, cols]``."""
+    if stream is None and out is None and m.codes.is_cuda:
+        gpu = _current_device()
+        r = _fastcall.mx_dequantize(gpu, m.codes, m.scales, FLOATS.get(dtype), _raw_stream(gpu))
+        if r is not None:
+            return _result("moe_mx_dequantize", r)
     args = _RowArgs()
     st = m.check("m", args)
     if out is not None:
@@ -201,6 +221,12 @@ def linear(x: torch.Tensor | MxMatrix, w: MxMatrix, out: torch.Tensor | None = N
     MxMatrix (one quantization then serves several products). w: ``[rows, cols]``. Returns
     ``[n, rows]`` of `dtype` (x's own, bf16 for an MxMatrix, unless `out` or `dtype` is given);
     `out` may have a row stride."""
+    if stream is None and out is None and ws is None and type(x) is torch.Tensor and x.is_cuda:
+        gpu = _current_device()
+        r = _fastcall.mx_linear(gpu, x, w.codes, w.scales, FLOATS.get(dtype or x.dtype),
+                                _raw_stream(gpu))
+        if r is not None:
+            return _result("moe_mx_linear", r)
     args = _RowArgs()
     wst = w.check("w", args, 2)
     quantized = isinstance(x, MxMatrix)
@@ -255,6 +281,14 @@ def ffn(layer: MxLayer, x: torch.Tensor, routing: Routing, residual: torch.Tenso
     """moe_mx_ffn: the routing-weighted sum of the experts' outputs for x ``[n, d_model]`` (fp32,
     bf16 or fp16), added to `residual` fp32 ``[n, d_model]`` (None: zeros). A new tensor unless
     `out` is given, which may be `residual`."""
+    if stream is None and ws is None and type(x) is torch.Tensor and x.is_cuda:
+        gpu = _current_device()
+        g, u, d = layer.gate, layer.up, layer.down
+        r = _fastcall.mx_ffn(gpu, g.codes, g.scales, u.codes, u.scales, d.codes, d.scales, layer.top_k,
+                             x, routing.topk_ids, routing.topk_w, routing.expert_offsets,
+                             routing.pair_index, residual, out, _raw_stream(gpu))
+        if r is not None:
+            return out if out is not None and type(r) is not int else _result("moe_mx_ffn", r)
     args = _RowArgs()
     st = layer.check(args)
     stride = args.rows(x, "x", FLOATS, (None, st.d_model))

@@ -114,6 +114,20 @@ def _load():
 
 lib = _load()
 
+try:
+    from . import _fastcall  # noqa: E402  (links against the library loaded above)
+except ImportError as e:
+    raise ImportError("_fastcall.so is missing or does not load: build it with "
+                      "`python -m quantized_routed_expert_router_amd.build`") from e
+
+
+def _raw_stream(device: int) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+_current_device = torch.cuda.current_device
+
 
 def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
@@ -334,6 +348,17 @@ def route_scored(logits: torch.Tensor, top_k: int, rule: RouteRule, out: Routing
     """moe_route_scored: experts, weights and grouping of `logits` [n, E] (fp32, bf16 or fp16)
     by `rule`. Works on the GPU of its tensors, on that GPU's current stream or on `stream`;
     what it allocates belongs to that stream."""
+    if stream is None and out is None and ws is None and type(logits) is torch.Tensor and \
+            logits.is_cuda:
+        gpu = _current_device()
+        keep = rule.groups if rule.top_groups is None else rule.top_groups
+        r = _fastcall.route_scored(gpu, logits, top_k, SCORES.get(rule.score), rule.bias, rule.groups,
+                                   keep, GROUP_SCORES.get(rule.group_score), rule.renormalize,
+                                   rule.scale, _raw_stream(gpu))
+        if r is not None:
+            if type(r) is int:
+                raise MoeError("moe_route_scored", r)
+            return Routing(*r)
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
         raise ValueError(f"logits: expected [n, E], got {getattr(logits, 'shape', type(logits))}")
     if stream is not None:
