@@ -45,89 +45,129 @@ struct Window {
   }
 };
 
-// Quantizes `rows` rows of x into LDS, a block of 32 a thread; blocks past K are zeros.
-template <int DT, class RowOf>
-__device__ __forceinline__ void stage_rows(const Window& w, int rows, RowOf row_of) {
-  const int nb = w.K / kMxBlock, padded = w.scale_bytes;
-  for (int i = threadIdx.x; i < rows * padded; i += blockDim.x) {
-    const int row = i / padded, b = i - row * padded;
-    uint4 c = make_uint4(0, 0, 0, 0);
-    uint32_t s = 0;
-    if (b < nb) {
-      const char* p = row_of(row) + (size_t)b * (kMxBlock * mx_type_size(DT));
-      MxValues<DT> v[4];
-      uint32_t m = 0;
+// What a thread brings into LDS in one go: a block of 32 values of x (or its codes and scale) and
+// 16 bytes of weight scales. The first goes are requested before the weights, since memory
+// answers in the order of the requests: the rows are then quantized while the weights arrive.
+template <int DT>
+struct XBlock {
+  MxValues<DT> v[4];
+  __device__ __forceinline__ void load(const char* row, const uint8_t*, int b) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j].load(p + j * 8 * mx_type_size(DT));
-#pragma unroll
-      for (int j = 0; j < 4; ++j) m = max(m, v[j].amax());
-      s = mx_scale_byte(m);
-      if (s != 255u) {
-        const float f = mx_scale_float(s);
-        c = make_uint4(v[0].codes(f), v[1].codes(f), v[2].codes(f), v[3].codes(f));
-      }
-    }
-    *reinterpret_cast<uint4*>(w.xq + row * w.row_bytes + b * 16) = c;
-    w.xs[row * w.scale_bytes + b] = (uint8_t)s;
+    for (int j = 0; j < 4; ++j) v[j].load(row + (b * 4 + j) * (8 * mx_type_size(DT)));
   }
-}
+  __device__ __forceinline__ void quantized(uint4& c, uint32_t& s) const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = max(m, v[j].amax());
+    s = mx_scale_byte(m);
+    const float f = mx_scale_float(s);
+    c = s == 255u ? make_uint4(0, 0, 0, 0)
+                  : make_uint4(v[0].codes(f), v[1].codes(f), v[2].codes(f), v[3].codes(f));
+  }
+};
 
-// The same for rows that are quantized already.
-template <class RowOf, class ScaleOf>
-__device__ __forceinline__ void stage_quantized(const Window& w, int rows, RowOf row_of,
-                                                ScaleOf scale_of) {
-  const int nb = w.K / kMxBlock, padded = w.scale_bytes;
-  for (int i = threadIdx.x; i < rows * padded; i += blockDim.x) {
-    const int row = i / padded, b = i - row * padded;
+template <>
+struct XBlock<MOE_E4M3> {  // rows that are quantized already
+  uint4 c;
+  uint32_t s;
+  __device__ __forceinline__ void load(const char* row, const uint8_t* scales, int b) {
+    c = reinterpret_cast<const uint4*>(row)[b];
+    s = scales[b];
+  }
+  __device__ __forceinline__ void quantized(uint4& codes, uint32_t& scale) const {
+    codes = c;
+    scale = s;
+  }
+};
+
+// Block i of `rows` rows, row by row (padded to whole steps: blocks past K are zeros).
+template <int DT>
+struct Rows {
+  XBlock<DT> first;
+  template <class RowOf, class ScaleOf>
+  __device__ __forceinline__ void read(XBlock<DT>& x, const Window& w, int rows, int i, RowOf row_of,
+                                       ScaleOf scale_of) const {
+    const int row = i / w.scale_bytes, b = i - row * w.scale_bytes;
+    if (row < rows && b < w.K / kMxBlock) x.load(row_of(row), scale_of(row), b);
+  }
+  __device__ __forceinline__ void write(const XBlock<DT>& x, const Window& w, int rows, int i) const {
+    const int row = i / w.scale_bytes, b = i - row * w.scale_bytes;
+    if (row >= rows) return;
     uint4 c = make_uint4(0, 0, 0, 0);
     uint32_t s = 0;
-    if (b < nb) {
-      c = *reinterpret_cast<const uint4*>(row_of(row) + 16 * b);
-      s = scale_of(row)[b];
-    }
+    if (b < w.K / kMxBlock) x.quantized(c, s);
     *reinterpret_cast<uint4*>(w.xq + row * w.row_bytes + b * 16) = c;
     w.xs[row * w.scale_bytes + b] = (uint8_t)s;
   }
-}
+  template <class RowOf, class ScaleOf>
+  __device__ __forceinline__ void request(const Window& w, int rows, RowOf row_of, ScaleOf scale_of) {
+    read(first, w, rows, threadIdx.x, row_of, scale_of);
+  }
+  template <class RowOf, class ScaleOf>
+  __device__ __forceinline__ void store(const Window& w, int rows, RowOf row_of, ScaleOf scale_of) const {
+    write(first, w, rows, threadIdx.x);
+    for (int i = threadIdx.x + blockDim.x; i < rows * w.scale_bytes; i += blockDim.x) {
+      XBlock<DT> x;
+      read(x, w, rows, i, row_of, scale_of);
+      write(x, w, rows, i);
+    }
+  }
+};
 
 // The scales of 32 neighbouring rows of a matrix (fewer at its end) are one piece of memory
-// that starts at a multiple of 32 bytes; copied in words of 16 bytes, the last ones as bytes.
-__device__ __forceinline__ void stage_scales(uint8_t* to, const uint8_t* from, int bytes) {
-  const int words = bytes / 16;
-  for (int i = threadIdx.x; i < words; i += blockDim.x)
-    reinterpret_cast<uint4*>(to)[i] = reinterpret_cast<const uint4*>(from)[i];
-  for (int i = 16 * words + threadIdx.x; i < bytes; i += blockDim.x) to[i] = from[i];
+// that starts at a multiple of 32 bytes: 16-byte words, the last ones as bytes.
+struct ScalePiece {
+  uint4 first;
+  __device__ __forceinline__ void request(const uint8_t* from, int bytes, int i) {
+    if (i < bytes / 16) first = reinterpret_cast<const uint4*>(from)[i];
+  }
+  __device__ __forceinline__ void store(uint8_t* to, const uint8_t* from, int bytes, int i, int step) const {
+    const int words = bytes / 16;
+    if (i < words) reinterpret_cast<uint4*>(to)[i] = first;
+    for (int j = i + step; j < words; j += step)
+      reinterpret_cast<uint4*>(to)[j] = reinterpret_cast<const uint4*>(from)[j];
+    for (int j = 16 * words + i; j < bytes; j += step) to[j] = from[j];
+  }
+};
+
+// A barrier for LDS alone: the weights stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 // Codes of up to kFlight steps of MATS matrices, two tiles of 16 rows each, as a lane holds them.
+// The rows' buffers start at the workgroup's first row; blocks past K read as zeros.
 template <int MATS>
 struct Flight {
   i32x4 c[kFlight][MATS][2];
 };
 
-// Requests the codes of steps s0 .. (clamped to valid blocks: the x codes past K are zeros, and
-// scales past K are taken as 1, so what is read twice there adds zeros).
+constexpr int kOutside = (int)0x80000000u;
+
 template <int MATS>
-__device__ __forceinline__ void request(Flight<MATS>& f, const uint8_t* const (&base)[MATS][2], int nb,
-                                        int s0, int chunk) {
+__device__ __forceinline__ void request(Flight<MATS>& f, const __amdgpu_buffer_rsrc_t (&buf)[MATS],
+                                        const int (&off)[2], int nb, int s0, int chunk) {
 #pragma unroll
   for (int s = 0; s < kFlight; ++s) {
-    const int b = min(4 * (s0 + s) + chunk, nb - 1);
+    const bool in = 4 * (s0 + s) + chunk < nb;
 #pragma unroll
     for (int m = 0; m < MATS; ++m)
 #pragma unroll
       for (int t = 0; t < 2; ++t)
-        f.c[s][m][t] = *reinterpret_cast<const i32x4*>(base[m][t] + 16 * (size_t)b);
+        f.c[s][m][t] = __builtin_amdgcn_raw_buffer_load_b128(buf[m], in ? off[t] : kOutside, 64 * (s0 + s), 0);
   }
 }
 
+// Steps s0 .. of the flight (past `send` none are left).
 template <int MATS>
 __device__ __forceinline__ void multiply(const Flight<MATS>& f, const Window& w, int s0, int send, int col,
                                          int chunk, int r, mx_f32x4 (&acc)[MATS][2]) {
   const int nb = w.K / kMxBlock;
 #pragma unroll
   for (int s = 0; s < kFlight; ++s) {
-    if (s0 + s >= send) break;
+    if (s0 + s >= send) continue;
     const int b = 4 * (s0 + s) + chunk;
     const i32x4 x = *reinterpret_cast<const i32x4*>(w.xq + col * w.row_bytes + 16 * b);
     const int xs = w.xs[col * w.scale_bytes + b];
@@ -176,23 +216,30 @@ __global__ __launch_bounds__(kThreads) void k_mx_win_linear(const char* __restri
   const int per = (steps + kWaves - 1) / kWaves;
   const int sbeg = min(steps, wave * per), send = min(steps, sbeg + per);
   const Window w(lds, K, min(n, kCols));
-  const uint8_t* base[1][2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t)
-    base[0][t] = wq + (size_t)min(n0 + 16 * t + r, N - 1) * (K / 2);
+  const __amdgpu_buffer_rsrc_t buf[1] = {buffer_rsrc(wq + (size_t)n0 * (K / 2), 0x80000000u)};
+  const int last = N - 1 - n0;  // rows past the matrix: its last, never stored
+  const int off[2] = {min(r, last) * (K / 2) + 16 * chunk, min(16 + r, last) * (K / 2) + 16 * chunk};
+  auto row_of = [&](int i) {
+    return DT == MOE_E4M3 ? reinterpret_cast<const char*>(xq) + (size_t)(t0 + i) * (K / 2)
+                          : x + (t0 + i) * row_bytes;
+  };
+  auto scale_of = [&](int i) { return xs + (size_t)(t0 + i) * nb; };
+  const uint8_t* scales = wsc + (size_t)n0 * nb;
+  const int bytes = min(32, N - n0) * nb;
+  Rows<DT> xr;
+  ScalePiece sp;
+  xr.request(w, rows, row_of, scale_of);
+  sp.request(scales, bytes, threadIdx.x);
   Flight<1> f;
-  request(f, base, nb, sbeg, chunk);
-  stage_scales(w.ws, wsc + (size_t)n0 * nb, min(32, N - n0) * nb);
-  if constexpr (DT == MOE_E4M3)
-    stage_quantized(w, rows, [&](int i) { return xq + (size_t)(t0 + i) * (K / 2); },
-                    [&](int i) { return xs + (size_t)(t0 + i) * nb; });
-  else
-    stage_rows<DT>(w, rows, [&](int i) { return x + (t0 + i) * row_bytes; });
-  __syncthreads();
+  request(f, buf, off, nb, sbeg, chunk);
+  xr.store(w, rows, row_of, scale_of);
+  sp.store(w.ws, scales, bytes, threadIdx.x, kThreads);
+  lds_barrier();
   mx_f32x4 acc[1][2] = {};
   const int col = min(r, rows - 1);
-  for (int s0 = sbeg; s0 < send; s0 += kFlight) {
-    if (s0 > sbeg) request(f, base, nb, s0, chunk);
+  multiply(f, w, sbeg, send, col, chunk, r, acc);
+  for (int s0 = sbeg + kFlight; s0 < send; s0 += kFlight) {
+    request(f, buf, off, nb, s0, chunk);
     multiply(f, w, s0, send, col, chunk, r, acc);
   }
 #pragma unroll
@@ -215,8 +262,9 @@ __global__ __launch_bounds__(kThreads) void k_mx_win_linear(const char* __restri
 
 // ---------------------------------------------------------------- gate and up
 
-// Grid (f / 32, pairs). The workgroups of an expert's first pair take all of its pairs (16 a
-// pass); the others leave. No work list has to be built before the launch.
+// Grid (f / 32, pairs). A workgroup takes 16 pairs of one expert: those from its own pair on, when
+// a multiple of 16 of the expert's pairs come before it; the others leave. No work list has to
+// be built before the launch.
 template <int DT>
 __global__ __launch_bounds__(kThreads) void k_mx_win_gateup(
     const char* __restrict__ x, int64_t row_bytes, const int32_t* __restrict__ ids, int P, int k, int d,
@@ -225,143 +273,166 @@ __global__ __launch_bounds__(kThreads) void k_mx_win_gateup(
     uint8_t* __restrict__ hs) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   __shared__ float part[kWaves][2][32][kCols + 1];
-  __shared__ int s_pairs[kMxWindowPairs];
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  __shared__ int s_pairs[kCols];
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
   const int r = lane & 15, chunk = lane >> 4;
   const int p = blockIdx.y;
-  const int e = ids[p];
+  // every wave looks at all the ids: they are requested at once
+  int id[kMxWindowPairs / kWave];
+#pragma unroll
+  for (int i = 0; i < kMxWindowPairs / kWave; ++i) id[i] = ids[min(kWave * i + lane, P - 1)];
+  const int e = __builtin_amdgcn_readfirstlane(ids[p]);
   if ((unsigned)e >= (unsigned)E) return;
-  int count = 0;
-  for (int q0 = 0; q0 < P; q0 += kWave) {
-    const bool mine = q0 + lane < P && ids[min(q0 + lane, P - 1)] == e;
-    const uint64_t b = __ballot(mine);
-    if (q0 <= p && (b & (q0 + kWave <= p ? ~0ull : (1ull << (p - q0)) - 1ull))) return;
-    if (wave == 0 && mine) s_pairs[count + __popcll(b & ((1ull << lane) - 1ull))] = q0 + lane;
-    count += __popcll(b);
+  int before = 0, rows = 0;
+#pragma unroll
+  for (int i = 0; i < kMxWindowPairs / kWave; ++i) {
+    const int q = kWave * i + lane;
+    const uint64_t same = __ballot(q < P && id[i] == e);
+    const uint64_t from = __ballot(q >= p) & same;  // this pair and later ones
+    before += __popcll(same & ~from);
+    const int at = rows + __popcll(from & ((1ull << lane) - 1ull));
+    if (wave == 0 && (from >> lane & 1) && at < kCols) s_pairs[at] = q;
+    rows += __popcll(from);
   }
+  if (before % kCols) return;
+  rows = min(rows, kCols);
   const int nb = d / kMxBlock, steps = (d + kStep - 1) / kStep;
   const int per = (steps + kWaves - 1) / kWaves;
   const int sbeg = min(steps, wave * per), send = min(steps, sbeg + per);
   const int n0 = blockIdx.x * 32;
   const Window w(lds, d, min(P, kCols));
-  const uint8_t* base[2][2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const size_t row = (size_t)e * f + n0 + 16 * t + r;
-    base[0][t] = gq + row * (d / 2);
-    base[1][t] = uq + row * (d / 2);
-  }
+  const size_t first = (size_t)e * f + n0;
+  const __amdgpu_buffer_rsrc_t buf[2] = {buffer_rsrc(gq + first * (d / 2), 0x80000000u),
+                                         buffer_rsrc(uq + first * (d / 2), 0x80000000u)};
+  const int off[2] = {r * (d / 2) + 16 * chunk, (16 + r) * (d / 2) + 16 * chunk};
+  auto row_of = [&](int i) { return x + (s_pairs[i] / k) * row_bytes; };
+  auto scale_of = [](int) { return (const uint8_t*)nullptr; };
+  lds_barrier();  // s_pairs is written
+  Rows<DT> xr;
+  xr.request(w, rows, row_of, scale_of);
+  // the first half of the threads brings in gate's scales, the second up's
+  const int half = threadIdx.x / (kThreads / 2), i = threadIdx.x % (kThreads / 2);
+  const uint8_t* scales = (half ? us : gs) + first * nb;
+  ScalePiece sp;
+  sp.request(scales, 32 * nb, i);
   Flight<2> fl;
-  request(fl, base, nb, sbeg, chunk);
-  stage_scales(w.ws, gs + ((size_t)e * f + n0) * nb, 32 * nb);
-  stage_scales(w.ws + 32 * nb, us + ((size_t)e * f + n0) * nb, 32 * nb);
-  for (int c0 = 0; c0 < count; c0 += kCols) {
-    __syncthreads();  // s_pairs is written; the last pass has read its rows and sums
-    const int rows = min(kCols, count - c0);
-    stage_rows<DT>(w, rows, [&](int i) { return x + (s_pairs[c0 + i] / k) * row_bytes; });
-    __syncthreads();
-    mx_f32x4 acc[2][2] = {};
-    const int col = min(r, rows - 1);
-    for (int s0 = sbeg; s0 < send; s0 += kFlight) {
-      if (s0 > sbeg || c0 > 0) request(fl, base, nb, s0, chunk);
-      multiply(fl, w, s0, send, col, chunk, r, acc);
+  request(fl, buf, off, nb, sbeg, chunk);
+  xr.store(w, rows, row_of, scale_of);
+  sp.store(w.ws + half * 32 * nb, scales, 32 * nb, i, kThreads / 2);
+  lds_barrier();
+  mx_f32x4 acc[2][2] = {};
+  const int col = min(r, rows - 1);
+  multiply(fl, w, sbeg, send, col, chunk, r, acc);
+  for (int s0 = sbeg + kFlight; s0 < send; s0 += kFlight) {
+    request(fl, buf, off, nb, s0, chunk);
+    multiply(fl, w, s0, send, col, chunk, r, acc);
+  }
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) part[wave][m][16 * t + 4 * chunk + q][r] = acc[m][t][q];
+  lds_barrier();
+  // half a wave holds the 32 rows of one pair: its block
+#pragma unroll 1
+  for (int c = threadIdx.x / 32; c < rows; c += kThreads / 32) {
+    const int j = threadIdx.x & 31;
+    float g = part[0][0][j][c], u = part[0][1][j][c];
+#pragma unroll
+    for (int q = 1; q < kWaves; ++q) {
+      g += part[q][0][j][c];
+      u += part[q][1][j][c];
     }
+    const double h = mx_silu_up64(g, u);
+    double m = fabs(h);
+    bool bad = !(m < __builtin_inf());
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) part[wave][m][16 * t + 4 * chunk + i][r] = acc[m][t][i];
-    __syncthreads();
-    // half a wave holds the 32 rows of one pair: its block
-    for (int c = threadIdx.x / 32; c < rows; c += kThreads / 32) {
-      const int j = threadIdx.x & 31;
-      float g = part[0][0][j][c], u = part[0][1][j][c];
-#pragma unroll
-      for (int q = 1; q < kWaves; ++q) {
-        g += part[q][0][j][c];
-        u += part[q][1][j][c];
-      }
-      const double h = mx_silu_up64(g, u);
-      double m = fabs(h);
-      bool bad = !(m < __builtin_inf());
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        m = fmax(m, __shfl_xor(m, o));
-        bad |= __shfl_xor((int)bad, o) != 0;
-      }
-      const uint32_t s = bad ? 255u : mx_scale_byte64(m);
-      uint32_t code = bad ? 0u : mx_code64(h, s);
-      code |= (uint32_t)__shfl_xor((int)code, 1) << 4;  // even lanes: their pair's byte
-      code |= (uint32_t)__shfl_xor((int)code, 2) << 8;
-      code |= (uint32_t)__shfl_xor((int)code, 4) << 16;
-      const size_t pair = s_pairs[c0 + c];
-      if ((j & 7) == 0)
-        *reinterpret_cast<uint32_t*>(hq + pair * (f / 2) + n0 / 2 + j / 2) = code;
-      if (j == 0) hs[pair * (f / kMxBlock) + n0 / kMxBlock] = (uint8_t)s;
+    for (int o = 1; o < 32; o <<= 1) {
+      m = fmax(m, __shfl_xor(m, o));
+      bad |= __shfl_xor((int)bad, o) != 0;
     }
+    const uint32_t s = bad ? 255u : mx_scale_byte64(m);
+    uint32_t code = bad ? 0u : mx_code64(h, s);
+    code |= (uint32_t)__shfl_xor((int)code, 1) << 4;  // even lanes: their pair's byte
+    code |= (uint32_t)__shfl_xor((int)code, 2) << 8;
+    code |= (uint32_t)__shfl_xor((int)code, 4) << 16;
+    const size_t pair = s_pairs[c];
+    if ((j & 7) == 0) *reinterpret_cast<uint32_t*>(hq + pair * (f / 2) + n0 / 2 + j / 2) = code;
+    if (j == 0) hs[pair * (f / kMxBlock) + n0 / kMxBlock] = (uint8_t)s;
   }
 }
 
 // ---------------------------------------------------------------- down and combine
 
 constexpr int kDownThreads = 512;
-constexpr int kDownParts = 2;                                       // of the reduction axis
-constexpr int kDownSlots = kDownThreads / kWave / kDownParts;       // slots at once
+constexpr int kDownRows = 16;                                  // of d
+constexpr int kDownParts = 2;                                  // of the reduction axis
+constexpr int kDownLanes = kDownThreads / kWave / kDownParts;  // slots at once
 
-// The workgroups of one row tile (of all tokens) run on one XCD, whose L2 keeps the rows of an
-// expert that several tokens of the window share.
-__global__ __launch_bounds__(kDownThreads) void k_mx_win_down(
+// 16 rows of d of one token. An instruction multiplies one slot's rows; its columns all hold the
+// slot's hidden row (a window has too few rows to fill them). The workgroups of one row tile (of
+// all tokens) run on one XCD, whose L2 keeps the rows of an expert that several tokens share.
+__global__ __launch_bounds__(kDownThreads, 4) void k_mx_win_down(
     const int32_t* __restrict__ ids, const float* __restrict__ wt, int n, int k, int d, int f, int E,
     const uint8_t* __restrict__ dq, const uint8_t* __restrict__ ds, const uint8_t* __restrict__ hq,
     const uint8_t* __restrict__ hs, const float* residual, float* out) {
-  __shared__ float part[kDownParts][MOE_MAX_TOP_K][16];
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  __shared__ __attribute__((aligned(16))) float part[kDownParts][MOE_MAX_TOP_K][kDownRows];
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
   const int r = lane & 15, chunk = lane >> 4;
-  const int slot = (int)blockIdx.x / 8;
-  const int tile = (int)blockIdx.x % 8 + 8 * (slot / n), t = slot % n;
-  const int r0 = 16 * tile;
-  if (r0 >= d) return;
+  const int place = (int)blockIdx.x / 8;
+  const int tile = (int)blockIdx.x % 8 + 8 * (place / n), t = place % n;
+  const int r0 = kDownRows * tile;
+  if (r0 >= d) return;  // d is a multiple of 32
   const int nb = f / kMxBlock, steps = (f + kStep - 1) / kStep;
   const int kp = wave % kDownParts;
   const int per = (steps + kDownParts - 1) / kDownParts;
   const int sbeg = min(steps, kp * per), send = min(steps, sbeg + per);
-  for (int j = wave / kDownParts; j < k; j += kDownSlots) {
-    const size_t p = (size_t)t * k + j;
-    const int e = ids[p];
+  const int first = wave / kDownParts;
+  // the experts and the weights of the token's slots, one a lane, and the residual that the end
+  // needs: requested together
+  const int my_e = ids[(size_t)t * k + min(lane, k - 1)];
+  const float my_w = wt[(size_t)t * k + min(lane, k - 1)];
+  const size_t at = (size_t)t * d + r0 + r;
+  const float my_r = residual ? residual[at] : 0.0f;
+  for (int j = first; j < k; j += kDownLanes) {
+    const int e = __builtin_amdgcn_readlane(my_e, j);
     mx_f32x4 acc = {};
     if ((unsigned)e < (unsigned)E) {
-      const size_t row = (size_t)e * d + r0 + r;  // d is a multiple of 32
-      const uint8_t* wq = dq + row * (f / 2);
-      const uint8_t* wsc = ds + row * nb;
-      const uint8_t* xq = hq + p * (f / 2);
-      const uint8_t* xs = hs + p * nb;
+      const size_t row = (size_t)e * d + r0 + r, p = (size_t)t * k + j;
+      const uint8_t *wq = dq + row * (f / 2), *wsc = ds + row * nb;
+      const uint8_t *xq = hq + p * (f / 2), *xs = hs + p * nb;
       for (int s = sbeg; s < send; ++s) {
         const int b = 4 * s + chunk, bc = min(b, nb - 1);
-        const i32x4 a = *reinterpret_cast<const i32x4*>(wq + 16 * (size_t)bc);
-        i32x4 h = *reinterpret_cast<const i32x4*>(xq + 16 * (size_t)bc);
+        const i32x4 a = *reinterpret_cast<const i32x4*>(wq + 16 * bc);
+        i32x4 h = *reinterpret_cast<const i32x4*>(xq + 16 * bc);
         const int sa = b < nb ? wsc[bc] : 127, sh = b < nb ? xs[bc] : 127;
-        if (b >= nb) h = i32x4{0, 0, 0, 0};
+        if (b >= nb) h = i32x4{0, 0, 0, 0};  // past f
         acc = mx_mma16(a, h, acc, sa, sh);
       }
     }
-    // every column holds the same sums
-    if (r == 0)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) part[kp][j][4 * chunk + i] = acc[i];
+    // lane r holds column r of rows 4 chunk ..
+    if (r == 0) *reinterpret_cast<mx_f32x4*>(&part[kp][j][4 * chunk]) = acc;
   }
   __syncthreads();
-  if (threadIdx.x < 16) {
-    const int i = threadIdx.x;
+  if (wave == 0) {
     double sum = 0.0;
-    for (int j = 0; j < k; ++j) {
-      float y = part[0][j][i];
+    for (int j0 = 0; j0 < k; j0 += 8) {
+      float y[8];
 #pragma unroll
-      for (int q = 1; q < kDownParts; ++q) y += part[q][j][i];
-      sum += (double)wt[(size_t)t * k + j] * (double)y;
+      for (int q = 0; q < 8; ++q) {
+        y[q] = part[0][min(j0 + q, k - 1)][r];
+        y[q] += part[1][min(j0 + q, k - 1)][r];
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const uint32_t w = __builtin_amdgcn_readlane(__float_as_uint(my_w), min(j0 + q, k - 1));
+        if (j0 + q < k) sum += (double)__uint_as_float(w) * (double)y[q];
+      }
     }
-    const size_t at = (size_t)t * d + r0 + i;
-    out[at] = (float)((residual ? (double)residual[at] : 0.0) + sum);
+    if (lane < kDownRows) out[at] = (float)((double)my_r + sum);
   }
 }
 
@@ -395,10 +466,10 @@ hipError_t launch_mx_ffn_window(const MxFfnArgs& a, hipStream_t stream) {
                      L.n_experts, hq, hs);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  const int tiles = (d + 15) / 16;
+  const int tiles = d / kDownRows;
   hipLaunchKernelGGL(k_mx_win_down, dim3((tiles + 7) / 8 * 8 * a.n), dim3(kDownThreads), 0, stream,
-                     a.r->topk_ids, a.r->topk_w, a.n, k, d, f, L.n_experts, L.down.codes, L.down.scales,
-                     hq, hs, a.residual, a.out);
+                     a.r->topk_ids, a.r->topk_w, a.n, k, d, f, L.n_experts, L.down.codes, L.down.scales, hq,
+                     hs, a.residual, a.out);
   return hipGetLastError();
 }
 
