@@ -7,13 +7,21 @@
 //   k with the largest c are taken (equal ones: the lower id first), in that order
 //   w_j = scale * s_j, or scale * s_j / sum_i s_i over the k taken
 //
-// all in binary64: a score's last bit decides between near experts, and the number of
-// operations is small (some 40 an expert for the exponential and the quotient). One wavefront
-// takes one token: lane l holds experts l, l + 64, ... in registers. Groups go through LDS:
-// 64 / G lanes (a power of two) scan one group each. The k best are found as in the plain
-// router, by a threshold on the upper halves of order-preserving 64-bit images: every expert
-// of the top k has an upper half of at least the k-th largest of the lanes' largest ones, and
-// the few that do are ranked by counting.
+// all in binary64: a score's last bit decides between near experts. One wavefront takes one
+// token: lane l holds experts l, l + 64, ... in registers. Bound by the vector units: binary64
+// for every expert costs some 35 instructions of double length each.
+//
+// Sigmoid scores are therefore taken in fp32 first (rule_fast): the groups are kept by fp32
+// worths where these are further apart than their errors, every expert that could be among the k
+// best becomes a candidate, and the candidates, at most one a lane, get their binary64 scores,
+// by which they are ranked. Where groups are too near or candidates too many, and for scores
+// that are not finite, the whole rule runs in binary64 (wave_rule, which softmax always does:
+// its sum needs every exponential).
+//
+// Groups go through LDS: 64 / G lanes (a power of two) scan one group each. The k best are found
+// as in the plain router, by a threshold on order-preserving images: every expert of the top k
+// has an image of at least the k-th largest of the lanes' largest ones, and the few that do are
+// ranked by counting.
 #include "qmoe_route_dev.h"
 
 namespace qmoe {
@@ -29,12 +37,6 @@ __device__ __forceinline__ uint64_t order_image(double v) {
 
 __device__ __forceinline__ double shfl_xor_f64(double v, int mask) { return __shfl_xor(v, mask); }
 
-__device__ __forceinline__ float logit_at(const void* p, int dtype, size_t i) {
-  if (dtype == MOE_F32) return static_cast<const float*>(p)[i];
-  const uint32_t b = static_cast<const uint16_t*>(p)[i];
-  return dtype == MOE_BF16 ? __uint_as_float(b << 16) : half_bits_to_float(b);
-}
-
 struct RuleArgs {
   const void* logits;
   const float* bias;
@@ -48,7 +50,7 @@ struct RuleArgs {
 
 template <int KPL>
 struct RuleScratch {
-  uint32_t hi[kWave], lo[kWave];
+  uint32_t hi[kWave], lo[kWave];  // images of the candidates; fast: their logits and biases
   int id[kWave];
   int slot_id[MOE_MAX_TOP_K];
   double score[KPL * kWave];
@@ -67,19 +69,184 @@ __device__ __forceinline__ void top2_merge(double& a, double& b, double c, doubl
   b = fmax(low, fmax(b, d));
 }
 
+template <int KPL>
+struct RuleRow {
+  float l[KPL], b[KPL];  // logits and biases of experts lane, lane + 64, ...
+};
+
+// Every load is issued before the first is used.
+template <int KPL>
+__device__ __forceinline__ void load_row(const RuleArgs& a, int t, RuleRow<KPL>& v) {
+  const int lane = threadIdx.x & (kWave - 1), E = a.E;
+  const size_t row = (size_t)t * E;
+  if (a.dtype == MOE_F32) {
+    const float* p = static_cast<const float*>(a.logits) + row;
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) v.l[i] = p[min(lane + kWave * i, E - 1)];
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(a.logits) + row;
+    uint32_t h[KPL];
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) h[i] = p[min(lane + kWave * i, E - 1)];
+#pragma unroll
+    for (int i = 0; i < KPL; ++i)
+      v.l[i] = a.dtype == MOE_BF16 ? __uint_as_float(h[i] << 16) : half_bits_to_float(h[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < KPL; ++i) v.b[i] = 0.0f;
+  if (a.bias) {
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) v.b[i] = a.bias[min(lane + kWave * i, E - 1)];
+  }
+}
+
+// Ranks the candidates by (image, lower id): lane q holds candidate q < total. Slots get the lanes.
+__device__ __forceinline__ int rank_of(uint64_t mine, int id, int total) {
+  int rank = 0;
+  for (int q = 0; q < total; ++q) {
+    const uint64_t o = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(mine >> 32), q) << 32 |
+                       (uint32_t)__builtin_amdgcn_readlane((int)mine, q);
+    const int oi = __builtin_amdgcn_readlane(id, q);
+    rank += o > mine || (o == mine && oi < id);
+  }
+  return rank;
+}
+
+// Weights of the slots: lane j < k holds slot j's expert and binary64 score.
+__device__ __forceinline__ void store_slots(const RuleArgs& a, int t, int id, double score) {
+  const int lane = threadIdx.x & (kWave - 1), k = a.k;
+  double sum = 1.0;
+  if (a.renormalize) {
+    sum = 0.0;
+    for (int j = 0; j < k; ++j) sum += readlane_f64(score, j);  // slot order
+  }
+  if (lane < k) {
+    a.ids[(size_t)t * k + lane] = id;
+    a.w[(size_t)t * k + lane] = (float)(sum > 0.0 ? score / sum * a.scale : 0.0);
+  }
+}
+
+__device__ __forceinline__ float wave_max_f32(float v) {
+#pragma unroll
+  for (int m = 1; m < kWave; m <<= 1) v = fmaxf(v, __shfl_xor(v, m));
+  return v;
+}
+
+// Sigmoid scores by fp32 first; false where that cannot decide. An fp32 score is off by less than
+// 2^-21 (the exponential's argument by |l| 2^-24 of itself, which times the slope s (1 - s) stays
+// under 2^-24; the exponential, the sum and the reciprocal by an ulp each) and c by 2^-24 of
+// itself more: within 2^-20 (1 + |c|).
+template <int KPL>
+__device__ __forceinline__ bool rule_fast(const RuleArgs& a, int t, const RuleRow<KPL>& v,
+                                          RuleScratch<KPL>* sc, int& my_id) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const int E = a.E, k = a.k;
+  constexpr float kErr = 0x1p-20f;
+  float c[KPL];
+  bool odd = false;
+#pragma unroll
+  for (int i = 0; i < KPL; ++i) {
+    c[i] = __builtin_amdgcn_rcpf(1.0f + __expf(-v.l[i])) + v.b[i];
+    odd |= !(fabsf(c[i]) < __builtin_inff());
+  }
+  if (__ballot(odd)) return false;
+
+  uint64_t kept = ~0ull;
+  const int size = E / a.groups;
+  if (a.top_groups < a.groups) {
+    float* score = reinterpret_cast<float*>(sc->score);
+#pragma unroll
+    for (int i = 0; i < KPL; ++i)
+      if (lane + kWave * i < E) score[lane + kWave * i] = c[i];
+    wave_sync();
+    const int g = lane / a.lanes, sub = lane & (a.lanes - 1);
+    float m1 = -__builtin_inff(), m2 = m1;
+    if (g < a.groups)
+      for (int j = sub; j < size; j += a.lanes) {
+        const float x = score[g * size + j];
+        m2 = fmaxf(m2, fminf(m1, x));
+        m1 = fmaxf(m1, x);
+      }
+    for (int m = 1; m < a.lanes; m <<= 1) {
+      const float o1 = __shfl_xor(m1, m), o2 = __shfl_xor(m2, m);
+      m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
+      m1 = fmaxf(m1, o1);
+    }
+    const bool two = a.top2 && size > 1;
+    const float worth = two ? m1 + m2 : m1;
+    const float err = 2.0f * kErr * (2.0f + fabsf(m1) + (two ? fabsf(m2) : 0.0f));
+    int rank = 0;
+    for (int q = 0; q < a.groups; ++q) {
+      const float o = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(worth), q * a.lanes));
+      rank += o > worth || (o == worth && q < g);
+    }
+    const bool in = g < a.groups, stays = in && rank < a.top_groups;
+    // the least of the kept and the largest of the others, each at the wrong end of its error
+    const float least = -wave_max_f32(stays ? err - worth : -__builtin_inff());
+    const float most = wave_max_f32(in && !stays ? worth + err : -__builtin_inff());
+    if (!(least > most)) return false;
+    const uint64_t stay = __ballot(stays && sub == 0);
+    kept = 0;
+    for (int q = 0; q < a.groups; ++q) kept |= (stay >> (q * a.lanes) & 1ull) << q;
+  }
+
+  bool in[KPL];
+  uint32_t lmax = 0;
+#pragma unroll
+  for (int i = 0; i < KPL; ++i) {
+    const int e = lane + kWave * i;
+    in[i] = e < E && (a.top_groups >= a.groups || (kept >> (min(e, E - 1) / size) & 1));
+    lmax = max(lmax, in[i] ? order_bits(c[i]) : 0u);
+  }
+  // a threshold that at least k lanes reach, to 20 bits; 0 where fewer lanes than k hold an expert
+  uint32_t T = 0;
+  for (int b = 31; b >= 12; --b) {
+    const uint32_t u = T | (1u << b);
+    if (__popcll(__ballot(lmax >= u)) >= k) T = u;
+  }
+  const float Tf = order_bits_to_float(T);
+  const float from = T ? Tf - 4.0f * kErr * (1.0f + fabsf(Tf)) : -__builtin_inff();
+  const uint64_t below = (1ull << lane) - 1ull;
+  int total = 0;
+#pragma unroll
+  for (int i = 0; i < KPL; ++i) {
+    const bool cand = in[i] && c[i] >= from;
+    const uint64_t b = __ballot(cand);
+    const int pos = total + __popcll(b & below);
+    if (cand && pos < kWave) {
+      sc->hi[pos] = __float_as_uint(v.l[i]);
+      sc->lo[pos] = __float_as_uint(v.b[i]);
+      sc->id[pos] = lane + kWave * i;
+    }
+    total += __popcll(b);
+  }
+  if (total > kWave) return false;
+  wave_sync();
+  const int at = min(lane, total - 1);
+  const double s = 1.0 / (1.0 + exp(-(double)__uint_as_float(sc->hi[at])));
+  const int id = sc->id[at];
+  const uint64_t mine = lane < total ? order_image(s + (double)__uint_as_float(sc->lo[at])) : 0ull;
+  const int rank = rank_of(mine, id, total);
+  if (lane < total && rank < k) sc->slot_id[rank] = lane;
+  wave_sync();
+  const int from_lane = sc->slot_id[min(lane, k - 1)];
+  my_id = __shfl(id, from_lane);
+  store_slots(a, t, my_id, __shfl(s, from_lane));
+  return true;
+}
+
 // One token by one wavefront; every lane returns the expert of slot `lane` (lane < k).
 template <int KPL>
 __device__ __forceinline__ int wave_rule(const RuleArgs& a, int t, RuleScratch<KPL>* sc) {
   const int lane = threadIdx.x & (kWave - 1);
   const int E = a.E, k = a.k;
   const double none = -__builtin_inf();
-  // every load is issued before the first is used
-  float lv[KPL], bv[KPL];
-#pragma unroll
-  for (int i = 0; i < KPL; ++i)
-    lv[i] = logit_at(a.logits, a.dtype, (size_t)t * E + min(lane + kWave * i, E - 1));
-#pragma unroll
-  for (int i = 0; i < KPL; ++i) bv[i] = a.bias ? a.bias[min(lane + kWave * i, E - 1)] : 0.0f;
+  RuleRow<KPL> row;
+  load_row(a, t, row);
+  int fast_id = 0;
+  if (!a.softmax && rule_fast(a, t, row, sc, fast_id)) return fast_id;
+  wave_sync();
+  const float(&lv)[KPL] = row.l, (&bv)[KPL] = row.b;
 
   double s[KPL];
   if (a.softmax) {
@@ -99,8 +266,9 @@ __device__ __forceinline__ int wave_rule(const RuleArgs& a, int t, RuleScratch<K
     }
 #pragma unroll
     for (int m = 1; m < kWave; m <<= 1) sum += shfl_xor_f64(sum, m);
+    const double inv = sum > 0.0 ? 1.0 / sum : 0.0;
 #pragma unroll
-    for (int i = 0; i < KPL; ++i) s[i] = sum > 0.0 ? s[i] / sum : 0.0;
+    for (int i = 0; i < KPL; ++i) s[i] *= inv;
   } else {
 #pragma unroll
     for (int i = 0; i < KPL; ++i)
@@ -180,13 +348,7 @@ __device__ __forceinline__ int wave_rule(const RuleArgs& a, int t, RuleScratch<K
   if (total <= kWave) {
     const uint64_t mine = lane < total ? (uint64_t)sc->hi[lane] << 32 | sc->lo[lane] : 0ull;
     const int mi = lane < total ? sc->id[lane] : 0x7fffffff;
-    int rank = 0;
-    for (int q = 0; q < total; ++q) {
-      const uint64_t o = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(mine >> 32), q) << 32 |
-                         (uint32_t)__builtin_amdgcn_readlane((int)mine, q);
-      const int oi = __builtin_amdgcn_readlane(mi, q);
-      rank += o > mine || (o == mine && oi < mi);
-    }
+    const int rank = rank_of(mine, mi, total);
     if (lane < total && rank < k) sc->slot_id[rank] = mi;
     wave_sync();
     if (lane < k) my_id = sc->slot_id[lane];
@@ -217,16 +379,7 @@ __device__ __forceinline__ int wave_rule(const RuleArgs& a, int t, RuleScratch<K
   for (int i = 0; i < KPL; ++i)
     if (lane + kWave * i < E) sc->score[lane + kWave * i] = s[i];
   wave_sync();
-  const double mine = lane < k ? sc->score[my_id] : 0.0;
-  double sum = 1.0;
-  if (a.renormalize) {
-    sum = 0.0;
-    for (int j = 0; j < k; ++j) sum += readlane_f64(mine, j);  // slot order
-  }
-  if (lane < k) {
-    a.ids[(size_t)t * k + lane] = my_id;
-    a.w[(size_t)t * k + lane] = (float)(sum > 0.0 ? mine / sum * a.scale : 0.0);
-  }
+  store_slots(a, t, my_id, lane < k ? sc->score[my_id] : 0.0);
   return my_id;
 }
 
