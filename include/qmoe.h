@@ -443,9 +443,9 @@ moe_status moe_attn_prefill(const moe_kv_cache* cache, const moe_heads* q, int d
  * lower; of their experts the k with the largest c are taken, of equal ones the lower id.
  * Slot order is the order of c. w = scale * s, or with renormalize scale * s / sum of the k
  * taken (0 where that sum is 0). All in binary64, w rounded once to fp32.
- * A logit that is NaN or a c that is NaN or -inf ranks last, whatever its group (such experts
- * by lower id), and has weight 0; where every logit is -inf, softmax scores are 0. In a
- * softmax, +inf logits share the weight. */
+ * An expert whose logit is NaN or whose c is NaN or -inf comes after all others of the groups
+ * that stay (several by lower id) and has weight 0; a group whose worth is NaN counts as -inf.
+ * Where every logit is -inf, softmax scores are 0. In a softmax, +inf logits share the weight. */
 typedef struct {
   int32_t score;       /* MOE_SCORE_SIGMOID or MOE_SCORE_SOFTMAX                       */
   const float* bias;   /* device fp32 [E], 4-byte aligned, or NULL                     */
