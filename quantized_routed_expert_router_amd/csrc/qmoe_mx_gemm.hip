@@ -484,13 +484,13 @@ __device__ __forceinline__ void hidden_block(const mx_f32x16& g, const mx_f32x16
   }
 }
 
-// LDS that a wave has for itself once the ring is free: WAVES / SLOTS waves (rounded up, at least
-// two) share a slot.
+// LDS that a wave has for itself once the ring is free: WAVES / SLOTS waves (rounded up) share a
+// slot.
 template <class R, int WAVES>
 struct WaveLds {
   typedef typename R::Slot S;
   static constexpr int SLOTS = R::kCount;
-  static constexpr int kShare = (WAVES + SLOTS - 1) / SLOTS < 2 ? 2 : (WAVES + SLOTS - 1) / SLOTS;
+  static constexpr int kShare = (WAVES + SLOTS - 1) / SLOTS;
   static constexpr size_t kBytes = sizeof(S) / kShare / 16 * 16;
   __device__ static __forceinline__ lds_float* of(const R& slots, int wave) {
     uint32_t at = lds_address(slots.s0);
@@ -682,14 +682,14 @@ __global__ __launch_bounds__(kWave * WM * WN) __attribute__((amdgpu_waves_per_eu
   constexpr int BN = 32 * NW * WN, BM = 32 * NX * WM;
   typedef Stage<BN, BM> S;
   typedef ScaleRing<BN, BM, TAIL ? 2 : 4> SC;
+  typedef Slots<S, SC, 4> R;
   __shared__ S slot0, slot1, slot2, slot3;
   __shared__ SC scales;
-  const Slots<S, SC, 4> ring{&slot0, &slot1, &slot2, &slot3, &scales};
+  const R ring{&slot0, &slot1, &slot2, &slot3, &scales};
   const int ntn = (a.N + BN - 1) / BN;
   int mt, nt;
   if (!grid_tile(a, (a.rows + BM - 1) / BM, ntn, mt, nt)) return;
-  tile<Slots<S, SC, 4>, WM, WN, NW, NX, TAIL, kLinear>(ring, a, 0, nt * BN, mt * BM,
-                                                              min(BM, a.rows - mt * BM));
+  tile<R, WM, WN, NW, NX, TAIL, kLinear>(ring, a, 0, nt * BN, mt * BM, min(BM, a.rows - mt * BM));
 }
 
 // ---------------------------------------------------------------- work list
@@ -850,10 +850,18 @@ hipError_t launch_mx_linear(const MxLinearArgs& a, hipStream_t stream) {
     g.xq = xq;
     g.xs = xs;
   }
-  if ((long long)a.n * a.N <= 1024ll * 1024)
-    linear<1, 4, 1, 2>(g, stream);
-  else
-    linear<2, 4, 2, 4>(g, stream);
+  // The largest tile that still gives most CUs one: a tile twice as large needs half the loads
+  // and LDS reads a product. Measured (us, K = 2048; tiles 64x64, 64x128, 128x128, 128x256,
+  // 256x256, rows of x first):  256 x 4096: 6.9 7.8 9.8 12.8 16.1;  1024 x 2048: 9.4 8.7 10.6
+  // 13.4 16.7;  2048 x 2048: 15.3 13.2 12.2 14.5 17.8;  1024 x 5120: 19.0 17.3 16.4 15.6 18.8;
+  // 4096 x 4096: 48.4 39.1 31.7 31.4 25.4.
+  const int most = device_cu_count() * 5 / 8;
+  auto tiles = [&](int rows, int cols) { return (long long)((a.n + rows - 1) / rows) * ((a.N + cols - 1) / cols); };
+  if (tiles(256, 256) >= most) linear<2, 4, 2, 4>(g, stream);
+  else if (tiles(128, 256) >= most) linear<2, 4, 2, 2>(g, stream);
+  else if (tiles(128, 128) >= most) linear<2, 2, 2, 2>(g, stream);
+  else if (tiles(64, 128) >= most) linear<1, 4, 1, 2>(g, stream);
+  else linear<2, 2, 1, 1>(g, stream);
   return hipGetLastError();
 }
 
