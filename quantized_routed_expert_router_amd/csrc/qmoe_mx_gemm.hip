@@ -429,7 +429,9 @@ __device__ __forceinline__ void hidden_block64(lds_float* gu, int lane, uint32_t
 }
 
 // A value is off by at most 2^-20 of itself (the exponential 2 ulp, the sum half of one, the
-// reciprocal 1, two products half each: 4.5 * 2^-23 < 2^-20).
+// reciprocal 1, two products half each: 4.5 * 2^-23 < 2^-20), or, where the exponential overflows
+// or a product is subnormal, by at most 2^-76 as long as |u| <= 2^32: |g| e^g < 2^-108 for
+// g < -80, and a subnormal's last bit is 2^-149.
 __device__ __forceinline__ float silu_up(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + expf(-g)) * u;
 }
@@ -441,17 +443,20 @@ template <class Stage16>
 __device__ __forceinline__ void hidden_block(const mx_f32x16& g, const mx_f32x16& u, int lane,
                                              uint32_t (&pieces)[4], uint32_t& scale, Stage16 stage) {
   float h[16];
-  float m = 0.0f;
+  float m = 0.0f, most_u = 0.0f;
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
     h[j] = silu_up(g[j], u[j]);
     m = fmaxf(m, fabsf(h[j]));
+    most_u = fmaxf(most_u, fabsf(u[j]));
   }
   m = fmaxf(m, __shfl_xor(m, 32));
   constexpr float kLess = 1.0f - 0x1p-20f, kMore = 1.0f + 0x1p-20f;
   scale = mx_scale_byte(__float_as_uint(m * kMore));
-  // tiny blocks (the products above may have lost bits) and ones that are not finite, too
-  bool redo = mx_scale_byte(__float_as_uint(m * kLess)) != scale || !(m < 0x1p120f) || m < 0x1p-90f;
+  // tiny blocks and large factors (2^-76 must be less than a thousandth of the largest value: far
+  // below the first border), and ones that are not finite, too
+  bool redo = mx_scale_byte(__float_as_uint(m * kLess)) != scale || !(m < 0x1p120f) || m < 0x1p-60f ||
+              most_u > 0x1p32f;
 #pragma unroll
   for (int j = 0; j < 16; ++j) redo |= !(fabsf(h[j]) <= m);  // NaN, which the maximum passes over
   const float f = mx_scale_float(scale);

@@ -316,6 +316,22 @@ def test_ffn_hidden_codes_next_to_borders():
     _check_ffn(layer, x, r, residual, mx.ffn(layer, x, r, residual))
 
 
+@pytest.mark.parametrize("n", [2, 64])
+@pytest.mark.parametrize("gate,up,x0", [(-96.0, 2.0 ** 120, 1.0), (2.0 ** -126, 2.0 ** 127, 1.5 * 2.0 ** -22)])
+def test_ffn_hidden_of_a_vanishing_gate_and_a_huge_up(n, gate, up, x0):
+    # e^-g beyond the fp32 range, or g below its normal numbers, with products in the range
+    wg, wu = torch.zeros((32, 64), dtype=torch.float32), torch.zeros((32, 64), dtype=torch.float32)
+    wg[:, 0], wu[:, 32] = 1.0, 2.0 ** -10
+    wg[5, 0], wu[5, 32] = gate, up
+    layer = mx.MxLayer(mx.MxMatrix(*_split(mx.quantize(wg.cuda()), 1)), mx.MxMatrix(*_split(mx.quantize(wu.cuda()), 1)),
+                       mx.MxMatrix(*_split(_weights(64, 32, 31), 1)), 1)
+    x = torch.zeros((n, 64))
+    x[:, 0], x[:, 32] = x0, 1.0
+    x, r = x.cuda(), _routing(n, 1, 1)
+    residual = torch.zeros((n, 64)).cuda()
+    _check_ffn(layer, x, r, residual, mx.ffn(layer, x, r, residual))
+
+
 def test_ffn_rows_behind_the_last_token():
     layer = _layer(8, 128, 64, 2, seed=15)
     for n in (3, 50):
