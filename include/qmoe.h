@@ -458,7 +458,8 @@ typedef struct {
 
 /* moe_route by a rule. logits: device [n][E] of dtype MOE_F32, MOE_BF16 or MOE_F16, aligned to
  * their size. out, ws, limits and errors as moe_route (the workspace is
- * moe_route_workspace_bytes); MOE_ERR_INVALID_ARGUMENT for a rule outside the ranges above. */
+ * moe_route_workspace_bytes); outputs and ws overlap neither each other nor the inputs.
+ * MOE_ERR_INVALID_ARGUMENT for a rule outside the ranges above. */
 moe_status moe_route_scored(const void* logits, int dtype, int n_tokens, int n_experts, int top_k,
                             const moe_route_rule* rule, const moe_routing* out, void* ws,
                             size_t ws_bytes, void* stream);

@@ -101,7 +101,7 @@ moe_status moe_route_scored(const void* logits, int dtype, int n_tokens, int n_e
   if (rule->renormalize != 0 && rule->renormalize != 1) return MOE_ERR_INVALID_ARGUMENT;
   if (!(rule->scale - rule->scale == 0.0f)) return MOE_ERR_INVALID_ARGUMENT;  // inf, NaN
   if (!aligned(rule->bias, 4)) return MOE_ERR_INVALID_ARGUMENT;
-  if (!out || !out->expert_offsets) return MOE_ERR_INVALID_ARGUMENT;
+  if (!out || !out->expert_offsets || !aligned(out->expert_offsets, 4)) return MOE_ERR_INVALID_ARGUMENT;
   if (n_tokens > 0) {
     if (!out->topk_ids || !out->topk_w || !out->pair_index || !logits ||
         !aligned(logits, mx_type_size(dtype)))
@@ -112,14 +112,21 @@ moe_status moe_route_scored(const void* logits, int dtype, int n_tokens, int n_e
     const Range writes[] = {range(out->topk_ids, 4 * P), range(out->topk_w, 4 * P),
                             range(out->pair_index, 4 * P),
                             range(out->expert_offsets, 4 * ((size_t)n_experts + 1))};
-    for (const Range& w : writes)
+    const size_t need = route_workspace_bytes(n_tokens, n_experts, top_k);
+    if (need > 0) {
+      if (!ws || ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+      if (!aligned(ws, 256)) return MOE_ERR_INVALID_ARGUMENT;
+    }
+    const Range work = range(ws, need);
+    for (const Range& r : reads)
+      if (!disjoint(work, r)) return MOE_ERR_INVALID_ARGUMENT;
+    for (int i = 0; i < 4; ++i) {
+      if (!aligned((const void*)writes[i].lo, 4) || !disjoint(work, writes[i])) return MOE_ERR_INVALID_ARGUMENT;
       for (const Range& r : reads)
-        if (!disjoint(w, r)) return MOE_ERR_INVALID_ARGUMENT;
-  }
-  const size_t need = route_workspace_bytes(n_tokens, n_experts, top_k);
-  if (need > 0) {
-    if (!ws || ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
-    if (!aligned(ws, 256)) return MOE_ERR_INVALID_ARGUMENT;
+        if (!disjoint(writes[i], r)) return MOE_ERR_INVALID_ARGUMENT;
+      for (int j = 0; j < i; ++j)
+        if (!disjoint(writes[i], writes[j])) return MOE_ERR_INVALID_ARGUMENT;
+    }
   }
   return status_of(launch_route_scored(logits, dtype, n_tokens, n_experts, top_k, *rule, out, ws,
                                        (hipStream_t)stream));

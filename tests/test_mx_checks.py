@@ -48,6 +48,16 @@ def test_route_rule_refusals():
     assert _route(_rule(), n=65536, ws=at(9) + 128) == INVALID
 
 
+def test_route_outputs_that_overlap_are_refused():
+    # 4 tokens of 4 experts each: 64 bytes an output; 65536 tokens of 32 experts also use ws
+    for kw in (dict(out=qmoe._Routing(at(2), at(2) + 60, at(4), at(5))), dict(out=qmoe._Routing(at(2), at(3), at(2), at(5))),
+               dict(out=qmoe._Routing(at(2), at(3), at(4), at(4) + 60)), dict(out=qmoe._Routing(at(2) + 2, at(3), at(4), at(5))),
+               dict(out=qmoe._Routing(at(2), at(3), at(4), at(5) + 1)), dict(n=0, out=qmoe._Routing(None, None, None, at(5) + 2)),
+               dict(n=65536, ws=at(1)), dict(n=65536, ws=at(2)), dict(n=65536, ws=at(5))):
+        assert _route(_rule(), **kw) == INVALID, kw
+    assert _route(_rule(bias=at(9) + 256), n=65536) == INVALID
+
+
 def test_quantize_refusals():
     q = lib.moe_mx_quantize
     assert q(at(1), BF16, 0, 64, 64, None, None, None) == OK
