@@ -18,7 +18,6 @@ __device__ __forceinline__ uint32_t lds_address(void* p) { return (uint32_t)(uin
 
 constexpr int kThreads = 256;
 constexpr int kTileRows = 256;  // most weight rows, and rows of x, of a tile
-constexpr int kStepBytes = 64;  // codes of a row in one stage: 128 values, 4 blocks
 
 enum Mode { kLinear, kGateUp, kDown };
 
@@ -47,22 +46,25 @@ struct GemmArgs {
 constexpr uint32_t kBufferBytes = 0x80000000u;
 constexpr int kOutside = (int)0x80000000u;
 
-__device__ __forceinline__ int swz(int row, int seg) { return seg ^ ((row >> 2) & 3); }
-
-// One stage of the ring in LDS: 128 values of the reduction axis. Row r's four 16-byte blocks
-// sit at positions swz(r, block), so that 16 neighbouring rows' reads of one block fall into
-// different banks.
-template <int BN, int BM>
+// One stage of the ring in LDS: KB blocks (of 32 values) of the reduction axis. Row r's 16-byte
+// blocks sit at positions swz(r, block), so that 16 neighbouring rows' reads of one block fall
+// into different banks.
+template <int BN, int BM, int KB>
 struct Stage {
-  uint4 w[BN * 4];
-  uint4 x[(BM < 64 ? 64 : BM) * 4];
+  static constexpr int kBlocks = KB;
+  uint4 w[BN * KB];
+  uint4 x[(BM < 64 ? 64 : BM) * KB];
+  __device__ static __forceinline__ int swz(int row, int seg) {
+    static_assert(KB == 4 || KB == 8, "64 or 128 bytes a row");
+    return KB == 4 ? seg ^ ((row >> 2) & 3) : seg ^ ((row >> 1) & 7);
+  }
 };
 
-// Scales of two rounds of ROUND stages: a word (four blocks) a row and stage.
-template <int BN, int BM, int ROUND>
+// Scales of two rounds: WORDS words (of four blocks) a row and round.
+template <int BN, int BM, int WORDS>
 struct ScaleRing {
-  static constexpr int kRound = ROUND;
-  uint32_t s[2][ROUND][BN + BM];
+  static constexpr int kWords = WORDS;
+  uint32_t s[2][WORDS][BN + BM];
 };
 
 // The ring's slots by name: an array of them would be kept in memory.
@@ -103,11 +105,12 @@ template <class R, int WM, int WN, int NW, int NX, bool TAIL, int MODE>
 struct Tile {
   typedef typename R::Slot S;
   typedef typename R::Scale SC;
-  static constexpr int SLOTS = R::kCount, ROUND = SC::kRound;
-  static constexpr int NT = kWave * WM * WN;  // threads: each load brings in NT / 4 rows
+  static constexpr int SLOTS = R::kCount, KB = S::kBlocks, WORDS = SC::kWords;
+  static constexpr int ROUND = 4 * WORDS / KB;  // stages a round of scales
+  static constexpr int NT = kWave * WM * WN;  // threads: each load brings in NT / KB rows
   static constexpr int BN = 32 * NW * WN, BM = 32 * NX * WM;
   static constexpr int kGroupsW = NW, kGroupsX = NX;  // 32-row groups a wave
-  static constexpr int kRows = NT / 4;
+  static constexpr int kRows = NT / KB;
   static constexpr int kWLoads = BN / kRows, kXLoads = BM < kRows ? 1 : BM / kRows;
   static constexpr int kOps = kWLoads + kXLoads;  // direct loads a thread and stage
   // rows of scales a thread fetches: with 8 waves, each half those of one matrix
@@ -120,10 +123,10 @@ struct Tile {
   __amdgpu_buffer_rsrc_t wbuf[MODE == kGateUp ? 2 : 1], xbuf;
   int woff[kWLoads], xoff[kXLoads];  // byte offsets of this thread at stage 0
   const uint8_t* sbase[kKinds];      // scales: the tensor from the tile's first row on,
-  int soff[kKinds], send[kKinds];    // this thread's row in it, and its last 4 ROUND bytes (before
+  int soff[kKinds], send[kKinds];    // this thread's row in it, and its last 4 WORDS bytes (before
                                      // its start where it is shorter: only in the workspace)
   int srow[kKinds];                  // its place in the scale ring (-1: none)
-  uint32_t held[kKinds][ROUND];      // the round that is requested
+  uint32_t held[kKinds][WORDS];      // the round that is requested
   int held_by[kKinds];               // bytes that its words lie further on
   int tid, lane, wave, wm, wn, nk, nb;
   mx_f32x16 acc[NW][NX];
@@ -135,7 +138,7 @@ struct Tile {
     int w[NW], x[NX];
   };
 
-  __device__ __forceinline__ int block_of() const { return swz(tid >> 2, tid & 3); }
+  __device__ __forceinline__ int block_of() const { return S::swz(tid / KB, tid % KB); }
 
   // 16 bytes a lane, into LDS in the order of the lanes
   __device__ __forceinline__ void bring(__amdgpu_buffer_rsrc_t b, void* lds, int off, int at) const {
@@ -146,14 +149,14 @@ struct Tile {
   __device__ __forceinline__ void load(int stage) const {
     const int s = min(stage, nk - 1);
     S& g = *st.template get<SLOT>();
-    const bool in = !TAIL || 4 * s + block_of() < nb;
+    const bool in = !TAIL || KB * s + block_of() < nb;
 #pragma unroll
     for (int i = 0; i < kWLoads; ++i)
-      bring(wbuf[MODE == kGateUp ? i / 2 : 0], g.w + NT * i + kWave * wave, in ? woff[i] : kOutside,
-            s * kStepBytes);
+      bring(wbuf[MODE == kGateUp ? i / (kWLoads / 2) : 0], g.w + NT * i + kWave * wave, in ? woff[i] : kOutside,
+            s * (16 * KB));
 #pragma unroll
     for (int i = 0; i < kXLoads; ++i)
-      bring(xbuf, g.x + NT * i + kWave * wave, in ? xoff[i] : kOutside, s * kStepBytes);
+      bring(xbuf, g.x + NT * i + kWave * wave, in ? xoff[i] : kOutside, s * (16 * KB));
   }
 
   // Requests this thread's scales of a round (TAIL: the last bytes of the tensor from where a
@@ -161,10 +164,10 @@ struct Tile {
   __device__ __forceinline__ void fetch(int round) {
 #pragma unroll
     for (int t = 0; t < kKinds; ++t) {
-      const int want = soff[t] + 4 * ROUND * min(round, (nk - 1) / ROUND);
+      const int want = soff[t] + 4 * WORDS * min(round, (nb - 1) / (4 * WORDS));
       const int at = TAIL ? min(want, send[t]) : want;
       if constexpr (TAIL) held_by[t] = want - at;
-      __builtin_memcpy(held[t], sbase[t] + at, 4 * ROUND);
+      __builtin_memcpy(held[t], sbase[t] + at, 4 * WORDS);
     }
   }
 
@@ -173,7 +176,7 @@ struct Tile {
 #pragma unroll
     for (int t = 0; t < kKinds; ++t) {
       if constexpr (TAIL) {
-        static_assert(!TAIL || ROUND == 2, "a round is one 64-bit word");
+        static_assert(!TAIL || WORDS == 2, "a round is one 64-bit word");
         const int there = nb - 8 * round;  // scales of the row from this round on
         const uint64_t mask = there >= 8 ? ~0ull : there <= 0 ? 0ull : (1ull << (8 * there)) - 1ull;
         const uint64_t v = ((uint64_t)held[t][1] << 32 | held[t][0]) >> (8 * held_by[t]) & mask;
@@ -181,7 +184,7 @@ struct Tile {
         held[t][1] = (uint32_t)(v >> 32);
       }
 #pragma unroll
-      for (int j = 0; j < ROUND; ++j)
+      for (int j = 0; j < WORDS; ++j)
         if (srow[t] >= 0) st.scales->s[round & 1][j][srow[t]] = held[t][j];
     }
   }
@@ -197,21 +200,22 @@ struct Tile {
   }
   __device__ __forceinline__ int xrow(int i) const { return (wm * NX + i) * 32 + (lane & 31); }
 
-  // Lane l of the half h = l / 32 takes blocks 2h (first instruction) and 2h + 1 (second).
-  template <int SLOT, int HALF>
+  // Of four blocks, lane l of the half h = l / 32 takes blocks 2h (even instruction PART) and
+  // 2h + 1 (odd).
+  template <int SLOT, int PART>
   __device__ __forceinline__ void read(Ops& o) const {
     const S& g = *st.template get<SLOT>();
-    const int b = 2 * (lane >> 5) + HALF;
+    const int b = 4 * (PART / 2) + 2 * (lane >> 5) + PART % 2;
 #pragma unroll
     for (int i = 0; i < NX; ++i)
-      __builtin_memcpy(&o.x[i], &g.x[4 * xrow(i) + swz(lane & 31, b)], 16);
+      __builtin_memcpy(&o.x[i], &g.x[KB * xrow(i) + S::swz(lane & 31, b)], 16);
 #pragma unroll
     for (int q = 0; q < NW; ++q)
-      __builtin_memcpy(&o.w[q], &g.w[4 * wrow(q) + swz(lane & 31, b)], 16);
+      __builtin_memcpy(&o.w[q], &g.w[KB * wrow(q) + S::swz(lane & 31, b)], 16);
   }
 
-  __device__ __forceinline__ void scales(int stage, Scales& o) const {
-    const uint32_t* p = st.scales->s[stage / ROUND & 1][stage % ROUND];
+  __device__ __forceinline__ void scales(int word, Scales& o) const {
+    const uint32_t* p = st.scales->s[word / WORDS & 1][word % WORDS];
 #pragma unroll
     for (int q = 0; q < NW; ++q) o.w[q] = (int)p[wrow(q)];
 #pragma unroll
@@ -267,35 +271,58 @@ struct Tile {
     }
   }
 
-  // Stage s, s modulo SLOTS = I: its first half's operands and its scales are in a and sc.
+  // Instruction PART of a stage, not the last one: the next one's operands are read meanwhile,
+  // and where it begins another word of scales, these.
+  template <int SLOT, int PART>
+  __device__ __forceinline__ void part(int s, Ops& a, Scales& sc) {
+    constexpr bool kWord = PART % 2 == 1;
+    Ops b;
+    Scales next;
+    if constexpr (PART % 2 == 0) halve(sc);
+    if constexpr (kWord) scales(s * (KB / 4) + (PART + 1) / 2, next);
+    read<SLOT, PART + 1>(b);
+    multiply<PART % 2>(a, sc);
+    interleave<(kWord ? 2 : 1) * (NW + NX), 0>();
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (PART + 2 < KB / 2) pin(b);
+    a = b;
+    if constexpr (kWord) {
+      pin(next);
+      sc = next;
+    }
+  }
+
+  // Stage s, s modulo SLOTS = I: its first operands and scales are in a and sc.
   template <int I>
   __device__ __forceinline__ void step(int s, Ops& a, Scales& sc) {
     constexpr int SLOT = I % SLOTS, NEXT = (I + 1) % SLOTS;
-    Ops b;
-    if (SLOTS % ROUND == 0 ? I % ROUND == ROUND - 1 : (s + 1) % ROUND == 0) {
-      // the last stage of a round: the next one to LDS, the one after it requested (before this
-      // stage's barrier, behind which the next stage's scales are read)
+    const bool round = SLOTS % ROUND == 0 ? I % ROUND == ROUND - 1 : (s + 1) % ROUND == 0;
+    // the last stage of a round: the next one's scales to LDS, the one after it requested (before
+    // this stage's barrier, behind which the next stage's scales are read)
+    if (round) {
       keep((s + 1) / ROUND);
       fetch((s + 1) / ROUND + 1);
     }
-    halve(sc);
-    read<SLOT, 1>(b);
-    multiply<0>(a, sc);
-    interleave<NW + NX, 0>();
-    __builtin_amdgcn_sched_barrier(0);
+    part<SLOT, 0>(s, a, sc);
+    if constexpr (KB == 8) {
+      part<SLOT, 1>(s, a, sc);
+      part<SLOT, 2>(s, a, sc);
+    }
     __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's reads of the stage are done
     wait_vmcnt<(SLOTS - 2) * kOps>();    // and its loads of the next one
     barrier_after_lds_dma();
     __builtin_amdgcn_sched_barrier(0);
     load<SLOT>(s + SLOTS);
+    Ops b;
     Scales next;
-    scales(s + 1, next);
-    read<NEXT, 0>(a);
-    multiply<1>(b, sc);
+    scales((s + 1) * (KB / 4), next);
+    read<NEXT, 0>(b);
+    multiply<1>(a, sc);
     interleave<2 * (NW + NX), kOps>();
     __builtin_amdgcn_sched_barrier(0);
-    pin(a);
+    pin(b);
     pin(next);
+    a = b;
     sc = next;
   }
 
@@ -355,7 +382,7 @@ struct Tile {
     wm = wave % WM;
     wn = wave / WM;
     nb = a.K / kMxBlock;
-    nk = (nb + 3) / 4;
+    nk = (nb + KB - 1) / KB;
     const int codes = a.K / 2;
     // weights: a buffer from the tile's first row; rows past the matrix: its last, never stored
     const size_t first = (size_t)e * a.N + n0;
@@ -365,7 +392,7 @@ struct Tile {
     constexpr int kOwn = MODE == kGateUp ? BN / 2 : BN;  // tile rows of one matrix
 #pragma unroll
     for (int i = 0; i < kWLoads; ++i)
-      woff[i] = min((kRows * i + (tid >> 2)) % kOwn, last) * codes + 16 * block_of();
+      woff[i] = min((kRows * i + tid / KB) % kOwn, last) * codes + 16 * block_of();
     // rows of x: those of the pairs' tokens (gate and up), or the tile's own from its first
     const size_t x0 = MODE == kGateUp ? 0 : (size_t)m0;
     xbuf = buffer_rsrc(a.xq + x0 * codes, kBufferBytes);
@@ -374,11 +401,11 @@ struct Tile {
       return MODE == kGateUp ? a.pair_index[m0 + j] / a.k : j;
     };
 #pragma unroll
-    for (int i = 0; i < kXLoads; ++i) xoff[i] = source(kRows * i + (tid >> 2)) * codes + 16 * block_of();
+    for (int i = 0; i < kXLoads; ++i) xoff[i] = source(kRows * i + tid / KB) * codes + 16 * block_of();
     auto row_of_scales = [&](int t, const uint8_t* base, int64_t tensor_rows, int row, int place) {
       sbase[t] = base;
       soff[t] = row * nb;
-      send[t] = (int)min((int64_t)1 << 30, tensor_rows * nb - 4 * ROUND);
+      send[t] = (int)min((int64_t)1 << 30, tensor_rows * nb - 4 * WORDS);
       srow[t] = place;
     };
     const uint8_t* ws = (MODE == kGateUp && wave >= 2 ? a.s1 : a.s0) + first * nb;
@@ -663,7 +690,7 @@ __device__ __forceinline__ bool grid_tile(const GemmArgs& a, int mtiles, int nti
 // The grouped product: 256 weight rows by up to 128 pairs. Two workgroups a CU: 80 KB of LDS.
 template <bool TAIL, int MODE>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_mx_grouped(GemmArgs a) {
-  typedef Stage<256, 128> S;
+  typedef Stage<256, 128, 4> S;
   typedef ScaleRing<256, 128, 2> SC;
   __shared__ S slot0, slot1, slot2;
   __shared__ SC scales;
@@ -685,12 +712,12 @@ template <int WM, int WN, int NW, int NX, bool TAIL>
 __global__ __launch_bounds__(kWave * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_mx_linear(
     GemmArgs a) {
   constexpr int BN = 32 * NW * WN, BM = 32 * NX * WM;
-  typedef Stage<BN, BM> S;
+  typedef Stage<BN, BM, 8> S;
   typedef ScaleRing<BN, BM, TAIL ? 2 : 4> SC;
-  typedef Slots<S, SC, 4> R;
-  __shared__ S slot0, slot1, slot2, slot3;
+  typedef Slots<S, SC, 2> R;
+  __shared__ S slot0, slot1;
   __shared__ SC scales;
-  const R ring{&slot0, &slot1, &slot2, &slot3, &scales};
+  const R ring{&slot0, &slot1, nullptr, nullptr, &scales};
   const int ntn = (a.N + BN - 1) / BN;
   int mt, nt;
   if (!grid_tile(a, (a.rows + BM - 1) / BM, ntn, mt, nt)) return;
