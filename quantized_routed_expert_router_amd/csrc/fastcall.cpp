@@ -41,6 +41,12 @@ class Args {
     if (!t) throw Mismatch();
     return *t;
   }
+  // The next argument, a tensor, which stays the next one.
+  const Tensor* peek() {
+    const Tensor& t = required();
+    --at_;
+    return &t;
+  }
   // A contiguous tensor of a type and one dimension of n entries (n < 0: any), or none.
   const void* vector(at::ScalarType type, int64_t n) {
     const Tensor* t = tensor();
@@ -428,27 +434,44 @@ PyObject* mx_dequantize(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
-// (device, x, w codes, w scales, dtype, stream) -> out
+// (device, x or its codes, None or its scales, w codes, w scales, dtype, out or None, stream) -> out
 PyObject* mx_linear(PyObject*, PyObject* const* args, Py_ssize_t n_args) {
   return guarded(args, n_args, [](Args& a) -> PyObject* {
-    int64_t stride;
-    const Tensor& x = rows_of(a, -1, &stride);
+    const Tensor* x = a.peek();
+    int64_t stride = 0;
+    moe_mx_matrix xq{};
+    if (x->scalar_type() == at::kByte) {
+      xq = mx_of(a, 2, nullptr);
+    } else {
+      rows_of(a, -1, &stride);
+      if (a.tensor()) throw Mismatch();
+    }
     const moe_mx_matrix w = mx_of(a, 2, nullptr);
-    if (x.size(1) != w.cols) throw Mismatch();
+    if (xq.codes ? xq.cols != w.cols : x->size(1) != w.cols) throw Mismatch();
+    if (x->size(0) > MOE_MAX_ROUTE_TOKENS) throw Mismatch();
+    const int n = (int)x->size(0);
     const int dtype = a.integer();
     if (dtype != MOE_F32 && dtype != MOE_BF16 && dtype != MOE_F16) throw Mismatch();
+    const Tensor* given = a.tensor();
+    if (given && (given->scalar_type() != type_of(dtype) || given->dim() != 2 || given->size(0) != n ||
+                  given->size(1) != w.rows || (w.rows > 1 && given->stride(1) != 1)))
+      throw Mismatch();
     void* stream = a.stream();
-    const int n = (int)x.size(0);
     Tensor out;
     moe_status s;
     {
       const WithoutGil free;
-      out = at::empty({n, w.rows}, x.options().dtype(type_of(dtype)));
-      const size_t need = moe_mx_linear_workspace_bytes(n, w.cols);
-      Tensor ws;
-      if (need) ws = at::empty({(int64_t)need}, x.options().dtype(at::kByte));
-      s = moe_mx_linear(x.data_ptr(), float_of(x), stride, n, &w, out.data_ptr(), dtype, w.rows,
-                        need ? ws.data_ptr() : nullptr, need, stream);
+      out = given ? *given : at::empty({n, w.rows}, x->options().dtype(type_of(dtype)));
+      const int64_t step = n > 1 ? out.stride(0) : w.rows;
+      if (xq.codes) {
+        s = moe_mx_linear_quantized(&xq, &w, out.data_ptr(), dtype, step, stream);
+      } else {
+        const size_t need = moe_mx_linear_workspace_bytes(n, w.cols);
+        Tensor ws;
+        if (need) ws = at::empty({(int64_t)need}, x->options().dtype(at::kByte));
+        s = moe_mx_linear(x->data_ptr(), float_of(*x), stride, n, &w, out.data_ptr(), dtype, step,
+                          need ? ws.data_ptr() : nullptr, need, stream);
+      }
     }
     if (s != MOE_OK) return PyLong_FromLong(s);
     return THPVariable_Wrap(std::move(out));

@@ -1,8 +1,8 @@
 """Python binding of the microscaled 4-bit products of libqmoe (C ABI in include/qmoe.h):
 quantization of rows, products with 4-bit matrices, and the routed-expert layer in them.
 
-Argument marshalling only, as in `qmoe`. The usual calls (nothing given for workspace and
-stream, tensors on the current device) go through a native short path with the same checks;
+Argument marshalling only, as in `qmoe`. The usual calls (no workspace and no stream given,
+tensors on the current device) go through a native short path with the same checks;
 whatever it does not take is checked and marshalled here. Every call works on the GPU of its tensors (made
 current for the call when it is not) and on that GPU's current stream, or on `stream`;
 outputs and workspaces that a call makes for itself belong to that stream.
@@ -86,7 +86,9 @@ class MxMatrix:
         if shape is not None and (*c[:-1], self.cols) != tuple(shape):
             raise ValueError(f"{name}: shape {(*c[:-1], self.cols)}, expected {tuple(shape)}")
         args.need(self.scales, f"{name}.scales", U8, shape=(*c[:-1], self.cols // BLOCK))
-        return _MxMatrix(self.codes.data_ptr(), self.scales.data_ptr(), self.rows, self.cols)
+        most = 0x7fffffff  # stays out of range where it does not fit
+        return _MxMatrix(self.codes.data_ptr(), self.scales.data_ptr(), min(self.rows, most),
+                         min(self.cols, most))
 
 
 @dataclass
@@ -144,6 +146,11 @@ def _on(device: torch.device, stream):
 
 def _current() -> int:
     return torch.cuda.current_stream().cuda_stream
+
+
+def _count(n: int) -> None:
+    if n > 0x7fffffff:  # would not reach the library as it is
+        raise ValueError(f"x: {n} rows")
 
 
 def _done(fn: str, rc: int) -> None:
@@ -221,15 +228,18 @@ def linear(x: torch.Tensor | MxMatrix, w: MxMatrix, out: torch.Tensor | None = N
     MxMatrix (one quantization then serves several products). w: ``[rows, cols]``. Returns
     ``[n, rows]`` of `dtype` (x's own, bf16 for an MxMatrix, unless `out` or `dtype` is given);
     `out` may have a row stride."""
-    if stream is None and out is None and ws is None and type(x) is torch.Tensor and x.is_cuda:
+    quantized = isinstance(x, MxMatrix)
+    rows, scales = (x.codes, x.scales) if quantized else (x, None)
+    if stream is None and ws is None and type(rows) is torch.Tensor and rows.is_cuda:
         gpu = _current_device()
-        r = _fastcall.mx_linear(gpu, x, w.codes, w.scales, FLOATS.get(dtype or x.dtype),
+        to = dtype or (out.dtype if out is not None else torch.bfloat16 if quantized else x.dtype)
+        r = _fastcall.mx_linear(gpu, rows, scales, w.codes, w.scales, FLOATS.get(to), out,
                                 _raw_stream(gpu))
         if r is not None:
-            return _result("moe_mx_linear", r)
+            r = _result("moe_mx_linear_quantized" if quantized else "moe_mx_linear", r)
+            return r if out is None else out
     args = _RowArgs()
     wst = w.check("w", args, 2)
-    quantized = isinstance(x, MxMatrix)
     if quantized:
         xst = x.check("x", args, 2)
         if x.cols != w.cols:
@@ -238,6 +248,7 @@ def linear(x: torch.Tensor | MxMatrix, w: MxMatrix, out: torch.Tensor | None = N
     else:
         stride = args.rows(x, "x", FLOATS, (None, w.cols))
         n = x.shape[0]
+    _count(n)
     if out is not None:
         if dtype is not None and dtype != out.dtype:
             raise ValueError(f"out: dtype {out.dtype}, expected {dtype}")
@@ -293,6 +304,7 @@ def ffn(layer: MxLayer, x: torch.Tensor, routing: Routing, residual: torch.Tenso
     st = layer.check(args)
     stride = args.rows(x, "x", FLOATS, (None, st.d_model))
     n = x.shape[0]
+    _count(n)
     routing.check(n, st.n_experts, layer.top_k, args)
     if residual is not None:
         args.need(residual, "residual", F32, shape=(n, st.d_model))

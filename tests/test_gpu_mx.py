@@ -174,6 +174,28 @@ def test_linear_nan_blocks_and_wide_scales(n, K, N):
     assert not fine.any()
 
 
+@pytest.mark.parametrize("n", [1, 9, 200])
+def test_linear_into_given_rows_and_of_quantized_rows(n):
+    w, x = _weights(72, 160, 3), _normal((n, 160), "bf16", seed=n)
+    q = mx.quantize(x)
+    for dtype in TYPES.values():
+        ref = mx.linear(x, w, dtype=dtype)
+        frame = torch.full((n + 1, 80), 5.0, dtype=dtype).cuda()
+        out = frame[:n, :72]
+        assert mx.linear(x, w, out=out) is out and torch.equal(out, ref)
+        out.zero_()
+        assert mx.linear(q, w, out=out) is out and torch.equal(out, ref)
+        assert torch.equal(mx.linear(q, w, dtype=dtype), ref)
+        assert (frame[n:] == 5).all() and (frame[:, 72:] == 5).all()
+    for bad in (torch.empty((n + 1, 72)), torch.empty((n, 71)), torch.empty((n, 72), dtype=torch.float64)):
+        with pytest.raises(ValueError):
+            mx.linear(q, w, out=bad.cuda())
+    with pytest.raises(ValueError):
+        mx.linear(x, w, out=torch.empty((n, 72)).cuda(), dtype=torch.float16)
+    with pytest.raises(ValueError):
+        mx.linear(mx.quantize(_normal((n, 128))), w)
+
+
 def test_linear_at_the_end_of_its_memory():
     # the last scales are read in whole requests: nothing behind them is, wherever they end
     for n, K, N in ((20, 32, 16), (33, 32, 17), (33, 64, 9), (64, 96, 19), (40, 288, 21), (1200, 416, 1001)):

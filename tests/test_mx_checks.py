@@ -185,6 +185,12 @@ def test_binding_refuses_cpu_tensors_and_shapes():
     assert (m.rows, m.cols) == (5, 96) and m.codes.shape == (3, 5, 48) and m.scales.shape == (3, 5, 3)
 
 
+def test_binding_refuses_more_rows_than_fit_an_int():
+    w = mx.MxMatrix(torch.zeros((8, 16), dtype=torch.uint8), torch.zeros((8, 1), dtype=torch.uint8))
+    with pytest.raises(ValueError, match="rows"):
+        mx.linear(torch.zeros((1, 32)).expand(2 ** 32 + 4, 32), w)
+
+
 def test_launch_splits():
     """The work list's shares: every tile is in one XCD's run, and no run is longer than the grid
     that the host launches for it (the arithmetic of the tile kernel, in Python)."""
