@@ -117,7 +117,7 @@ struct Tile {
   static constexpr int kKinds = NT == 2 * kTileRows ? 1 : 2;
   static_assert(NT == kTileRows || NT == 2 * kTileRows, "a row of scales a thread and kind");
   static_assert(BN >= kRows && BN <= kTileRows && BM <= kTileRows, "whole loads");
-  static_assert(MODE != kGateUp || (BN == 256 && NT == 256), "gate rows and up rows in loads of their own");
+  static_assert(MODE != kGateUp || BN == 256, "gate rows and up rows in loads and waves of their own");
 
   R st;
   __amdgpu_buffer_rsrc_t wbuf[MODE == kGateUp ? 2 : 1], xbuf;
@@ -455,65 +455,94 @@ __device__ __forceinline__ void hidden_block64(lds_float* gu, int lane, uint32_t
   for (int p = 0; p < 4; ++p) pieces[p] = (uint32_t)(all >> (16 * p)) & 0xffffu;
 }
 
-// A value is off by at most 2^-20 of itself (the exponential 2 ulp, the sum half of one, the
-// reciprocal 1, two products half each: 4.5 * 2^-23 < 2^-20), or, where the exponential overflows
-// or a product is subnormal, by at most 2^-76 as long as |u| <= 2^32: |g| e^g < 2^-108 for
-// g < -80, and a subnormal's last bit is 2^-149.
-__device__ __forceinline__ float silu_up(float g, float u) {
-  return g * __builtin_amdgcn_rcpf(1.0f + expf(-g)) * u;
+// h = silu(g) u in fp32, from above: h (1 + 2^-20) within 4.1 2^-23 of itself (the exponential,
+// whose argument's rounding is made good, 1.6 2^-23, the sum half of that unit, the reciprocal 1,
+// two products half each), so that it is at least h, and less 2^-19 of itself at most h. For
+// |g|, |u| <= 2^32, where the exponential is cut off or a product is subnormal, it is off by at
+// most 2^-76: |g| e^g < 2^-108 for g <= -80, and a subnormal's last bit is 2^-149.
+__device__ __forceinline__ float silu_up_above(float g, float u) {
+  constexpr float kHigh = -0x1.715476p+0f, kLow = -0x1.4ae0cp-26f;  // -1 / ln 2
+  const float c = fmaxf(g, -80.0f);
+  const float t = c * kHigh;
+  const float r = fmaf(c, kLow, fmaf(c, kHigh, -t));
+  float e = __builtin_amdgcn_exp2f(t);
+  e = fmaf(e, r * 0x1.62e43p-1f, e);
+  constexpr float kLess = 1.0f - 0x1p-20f;
+  return c * __builtin_amdgcn_rcpf(fmaf(e, kLess, kLess)) * u;
 }
 
 // 16 values of h (half of a block; lane ^ 32 holds the other half) to four pieces of four codes
-// and the scale. The fast values decide where the slightly smaller and the slightly larger
-// block give the same codes; otherwise the block is computed again in binary64.
+// and the scale. Where a value's bounds have different codes, a value in some six thousand, it is
+// computed again in binary64; where the scale's have, and for values that are tiny, huge or not
+// finite, the whole block.
 template <class Stage16>
 __device__ __forceinline__ void hidden_block(const mx_f32x16& g, const mx_f32x16& u, int lane,
                                              uint32_t (&pieces)[4], uint32_t& scale, Stage16 stage) {
+  constexpr float kBelow = 1.0f - 0x1p-19f;
   float h[16];
-  float m = 0.0f, most_u = 0.0f;
+  float m = 0.0f, most = 0.0f;
+  bool odd = false;
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
-    h[j] = silu_up(g[j], u[j]);
+    h[j] = silu_up_above(g[j], u[j]);
     m = fmaxf(m, fabsf(h[j]));
-    most_u = fmaxf(most_u, fabsf(u[j]));
+    most = fmaxf(most, fmaxf(fabsf(g[j]), fabsf(u[j])));
+    odd |= __builtin_isunordered(g[j], u[j]);  // which the maxima pass over
   }
   m = fmaxf(m, __shfl_xor(m, 32));
-  constexpr float kLess = 1.0f - 0x1p-20f, kMore = 1.0f + 0x1p-20f;
-  scale = mx_scale_byte(__float_as_uint(m * kMore));
-  // tiny blocks and large factors (2^-76 must be less than a thousandth of the largest value: far
-  // below the first border), and ones that are not finite, too
-  bool redo = mx_scale_byte(__float_as_uint(m * kLess)) != scale || !(m < 0x1p120f) || m < 0x1p-60f ||
-              most_u > 0x1p32f;
-#pragma unroll
-  for (int j = 0; j < 16; ++j) redo |= !(fabsf(h[j]) <= m);  // NaN, which the maximum passes over
+  scale = mx_scale_byte(__float_as_uint(m));
+  // 2^-76 must be less than a thousandth of the largest value: far below the first border
+  odd |= mx_scale_byte(__float_as_uint(m * kBelow)) != scale || !(m < 0x1p120f) || m < 0x1p-60f || most > 0x1p32f;
   const float f = mx_scale_float(scale);
+  uint32_t differ = 0;
+  uint32_t by[4];
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
     uint32_t lo = 0, hi = 0;
-    lo = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(lo, h[4 * p] * kLess, h[4 * p + 1] * kLess, f, 0);
-    lo = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(lo, h[4 * p + 2] * kLess, h[4 * p + 3] * kLess, f, 1);
-    hi = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(hi, h[4 * p] * kMore, h[4 * p + 1] * kMore, f, 0);
-    hi = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(hi, h[4 * p + 2] * kMore, h[4 * p + 3] * kMore, f, 1);
-    redo |= lo != hi;
+    lo = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(lo, h[4 * p] * kBelow, h[4 * p + 1] * kBelow, f, 0);
+    lo = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(lo, h[4 * p + 2] * kBelow, h[4 * p + 3] * kBelow, f, 1);
+    hi = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(hi, h[4 * p], h[4 * p + 1], f, 0);
+    hi = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(hi, h[4 * p + 2], h[4 * p + 3], f, 1);
+    by[p] = lo ^ hi;
+    differ |= by[p];
     pieces[p] = lo;
   }
+  if (!__ballot(odd || differ)) return;
   // a block of zeros (a row of zeros) is what it is
-  bool some = false;
+  bool some = m != 0.0f;
 #pragma unroll
   for (int j = 0; j < 16; ++j) some |= g[j] != 0.0f && u[j] != 0.0f;
   some |= __shfl_xor((int)some, 32) != 0;
-  redo = redo && (some || m != 0.0f);
-  if (__ballot(redo)) {
-    lds_float* gu = stage();
+  odd = odd && some;
+  lds_float* gu = stage();
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      gu[j * kWave + lane] = g[j];
-      gu[(16 + j) * kWave + lane] = u[j];
-    }
-    __builtin_amdgcn_wave_barrier();
-    hidden_block64(gu, lane, pieces, scale);
-    __builtin_amdgcn_wave_barrier();
+  for (int j = 0; j < 16; ++j) {
+    gu[j * kWave + lane] = g[j];
+    gu[(16 + j) * kWave + lane] = u[j];
   }
+  __builtin_amdgcn_wave_barrier();
+  if (__ballot(odd)) {
+    hidden_block64(gu, lane, pieces, scale);
+  } else {
+    uint64_t all = 0, open = 0;  // codes; those to decide
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      all |= (uint64_t)pieces[p] << (16 * p);
+      open |= (uint64_t)by[p] << (16 * p);
+    }
+#pragma unroll 1
+    while (__ballot(open != 0)) {
+      const int at = open ? __builtin_ctzll(open) & ~3 : 0;
+      const lds_float* v = gu + (at >> 2) * kWave + lane;
+      const uint64_t code = mx_code64(mx_silu_up64(v[0], v[16 * kWave]), scale);
+      const uint64_t mask = open ? 15ull << at : 0ull;
+      all = (all & ~mask) | (code << at & mask);
+      open &= ~mask;
+    }
+#pragma unroll
+    for (int p = 0; p < 4; ++p) pieces[p] = (uint32_t)(all >> (16 * p)) & 0xffffu;
+  }
+  __builtin_amdgcn_wave_barrier();
 }
 
 // LDS that a wave has for itself once the ring is free: WAVES / SLOTS waves (rounded up) share a
