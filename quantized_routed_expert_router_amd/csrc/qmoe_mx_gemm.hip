@@ -1,10 +1,17 @@
 // Microscaled 4-bit matrix products of many rows: y = Q(x) W^T, and the routed experts'
 // products of a batch or a prefill chunk.
 //
-//   k_mx_tiles    M-tile work list of the grouped product (expert, first grouped pair, pairs)
-//   k_mx_gemm     one workgroup per tile of the product; as the gate and up products it ends
-//                 in h = silu(g) u and its 4-bit blocks, as the down product in fp32 rows
+//   k_mx_linear   one workgroup per tile of the product; rows out through LDS
+//   k_mx_tiles    M-tile work list of the grouped products (expert, first grouped pair, pairs)
+//   k_mx_grouped  one workgroup per tile of an expert's product; as gate and up it ends in
+//                 h = silu(g) u and its 4-bit blocks, as the down product in fp32 rows
 //   k_mx_combine  out[t] = residual[t] + sum_j w[t][j] y[t k + j], slot order, binary64 sum
+//
+// Measured: 8192 rows by 4096 by 8192 columns 135 us, 4.1 PFLOP/s (the bare scaled matrix
+// instructions reach 6.6 on random codes, which the power limit sets, a bf16 product of the
+// library 1.25); 512 experts of 768 by 2048, top 10: 256 tokens 164 + 105 us (gate and up, down),
+// the weights at 5.1 TB/s; 8192 tokens 260 + 273 us, and 130 us (5.1 TB/s) for the sum over the
+// slots.
 #include "qmoe_mx_internal.h"
 
 namespace qmoe {
@@ -28,8 +35,8 @@ struct GemmArgs {
   const int32_t* pair_index;
   const int4* tiles;
   const int* xcd_first;  // [kXcds + 1] first tile of each XCD
-  int xcd_m, xcd_n;      // linear: column of XCDs over rows of x, tiles of an XCD: xcd_rm x xcd_rn,
-  int xcd_rm, xcd_rn;    // taken in panels of `panel` column tiles
+  int xcd_m;             // linear: XCDs side by side over the rows of x; an XCD's tiles are
+  int xcd_rm, xcd_rn;    // xcd_rm x xcd_rn, taken in panels of `panel` column tiles
   int panel;
   int64_t wrows, xrows;  // rows of the weights' and of x's tensors
   int rows;   // linear: rows of x
@@ -84,21 +91,24 @@ struct Slots {
   }
 };
 
-// A workgroup of WM x WN waves multiplies BM rows of x by BN weight rows; a wave holds NW x NX accumulators of 32 x 32 (weight rows by rows of x, so
-// that a lane holds 16 weight rows of one row of x: half of a block of h). For gate and up the
-// first half of the tile's weight rows are gate, the second the same rows of up, and a wave
-// holds both of its rows.
+// A workgroup of WM x WN waves multiplies BM rows of x by BN weight rows; a wave holds NW x NX
+// accumulators of 32 x 32 (weight rows by rows of x, so that a lane holds 16 weight rows of one
+// row of x: half of a block of h). For gate and up the first half of the tile's weight rows are
+// gate, the second the same rows of up, and a wave holds both of its rows.
 //
 // A ring of SLOTS stages is filled by direct loads into LDS; the offset of a lane never changes
 // and the stage is a scalar offset, so a load costs no arithmetic. Every slot is an LDS variable
 // of its own: the compiler then sees that the slots being filled are not the one being read, and
-// adds no wait for them. A stage is two instructions deep: while the first half multiplies, the
-// second half's operands are read, and while the second multiplies, those of the next stage.
-// Between them the stage's reads are complete and its slot is refilled.
+// adds no wait for them. While an instruction's products run, the next one's operands are read;
+// before the last of a stage all reads of its slot are complete, and the slot is refilled.
+//
+// A stage of eight blocks is 128 bytes of a row, whole lines of memory: with four, every line is
+// asked for twice, which cost the 256 x 256 tile 1.06 us per 128 values instead of 0.95 (8192
+// rows by 8192 columns) although its four slots reach a stage further ahead than two.
 //
 // Scales come through registers, ROUND stages of a row at once: a word a row and stage would
 // cost the memory path as many requests as the codes do (a line a lane), and rows of scales need
-// not be whole words. They are requested a round ahead and go to LDS a word a stage.
+// not be whole words. They are requested a round ahead and go to LDS a word per four blocks.
 //
 // TAIL: K is not a whole number of rounds. Codes and scales past K are zeros.
 template <class R, int WM, int WN, int NW, int NX, bool TAIL, int MODE>
@@ -256,8 +266,8 @@ struct Tile {
     for (int q = 0; q < NW; ++q) asm volatile("" : "+v"(o.w[q]));
   }
 
-  // One product, then up to one LDS read and one direct load: the four waves' reads and loads
-  // are spread over the stage and do not hold up the matrix cores.
+  // One product, then a share of the LDS reads and direct loads: the waves' reads and loads are
+  // spread over the stage and do not hold up the matrix cores.
   template <int READS, int LOADS>
   __device__ __forceinline__ static void interleave() {
     constexpr int M = NW * NX;
@@ -692,8 +702,8 @@ __device__ __forceinline__ void tile(const R& ring, const GemmArgs& a, int e, in
 // Workgroups are dealt to the 8 XCDs round robin. Each XCD has a run of the tile list, whose
 // tiles of one expert are neighbours, and takes a tile's column tiles one after another: the
 // tiles of an expert then read its weights, and a tile's workgroups its rows of x, through one
-// L2. (Dealt out tile by tile, every tile fetched its weights from the memory-side cache, which
-// bounded the product at about 4.6 TB/s: gate and up of 64 experts with 1024 rows each, 197 us.)
+// L2. (Gate and up of 8192 tokens 282 us dealt out tile by tile, 267 in runs; of 256 tokens, whose
+// experts have one tile each, 162 and 161.)
 constexpr int kXcds = 8;
 
 __device__ __forceinline__ bool list_tile(const int* xcd_first, int ntn, int& mt, int& nt) {
@@ -716,7 +726,11 @@ __device__ __forceinline__ bool grid_tile(const GemmArgs& a, int mtiles, int nti
   return mt < mtiles && nt < ntiles;
 }
 
-// The grouped product: 256 weight rows by up to 128 pairs. Two workgroups a CU: 80 KB of LDS.
+// The grouped product: 256 weight rows by up to 128 pairs, two workgroups a CU (80 KB of LDS), one's
+// start and end beside the other's loop. Few rows an expert: bound by the weights from memory.
+// Many: by the direct loads (without them 180 of 260 us, without the LDS reads 255, without the
+// end 250). Stages of whole lines would need 128 x 128 tiles (10% slower at 256 and at 8192
+// tokens) or one workgroup of 256 x 256 a CU (15% slower at 256 tokens, 1% at 8192).
 template <bool TAIL, int MODE>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_mx_grouped(GemmArgs a) {
   typedef Stage<256, 128, 4> S;
@@ -737,6 +751,9 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     tile<Slots<S, SC, 3>, 1, 4, 2, 4, TAIL, MODE>(ring, a, t.x, nt * kN, t.y, t.z);
 }
 
+// The dense product: stages of whole lines, two slots. Of the 256 x 256 tile's 0.95 us per 128
+// values, the matrix instructions need 0.76 (without loads and LDS reads); a tile's start and end
+// cost 8 us, since it takes all of a CU's LDS and nothing runs beside it.
 template <int WM, int WN, int NW, int NX, bool TAIL>
 __global__ __launch_bounds__(kWave * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_mx_linear(
     GemmArgs a) {
@@ -755,9 +772,9 @@ __global__ __launch_bounds__(kWave * WM * WN) __attribute__((amdgpu_waves_per_eu
 
 // ---------------------------------------------------------------- work list
 
-// A tile costs its weights (4) and its groups of 32 rows (1 each), in the units of the split of
-// the list over the XCDs. Both are read from the measured times of 64 experts with full tiles and
-// of 490 experts with a few rows each.
+// A tile's cost in the split of the list over the XCDs: 4 for its weights and 1 for each 32 rows
+// of x. By loads alone it would be 8 to 1, by products 0; between them, since neither hides the
+// other wholly.
 constexpr int kTileCost = 4;
 
 // Inclusive scan over the workgroup (1024 threads) of two values at once.
@@ -819,6 +836,7 @@ __global__ __launch_bounds__(1024) void k_mx_tiles(const int32_t* __restrict__ o
 
 // ---------------------------------------------------------------- combine
 
+// Reads y once, sixteen slots' words in flight a thread: 5.1 TB/s.
 constexpr int kCombineBatch = 16;
 
 __global__ __launch_bounds__(1024) void k_mx_combine(const float* __restrict__ y, const float* __restrict__ w,
@@ -913,9 +931,9 @@ hipError_t launch_mx_linear(const MxLinearArgs& a, hipStream_t stream) {
   }
   // The largest tile that still gives most CUs one: a tile twice as large needs half the loads
   // and LDS reads a product. Measured (us, K = 2048; tiles 64x64, 64x128, 128x128, 128x256,
-  // 256x256, rows of x first):  256 x 4096: 6.9 7.8 9.8 12.8 16.1;  1024 x 2048: 9.4 8.7 10.6
-  // 13.4 16.7;  2048 x 2048: 15.3 13.2 12.2 14.5 17.8;  1024 x 5120: 19.0 17.3 16.4 15.6 18.8;
-  // 4096 x 4096: 48.4 39.1 31.7 31.4 25.4.
+  // 256x256, rows of x first):  256 x 4096: 6.5 7.6 9.7 12.7 16.4;  1024 x 2048: 8.4 8.4 10.4
+  // 12.9 17.0;  2048 x 2048: 14.1 12.4 11.7 14.0 17.9;  1024 x 5120: 18.0 16.0 15.4 14.8 18.8;
+  // 4096 x 4096: 50.2 36.6 29.2 30.2 24.1.
   const int most = device_cu_count() * 5 / 8;
   auto tiles = [&](int rows, int cols) { return (long long)((a.n + rows - 1) / rows) * ((a.N + cols - 1) / cols); };
   if (tiles(256, 256) >= most) linear<2, 4, 2, 4>(g, stream);
