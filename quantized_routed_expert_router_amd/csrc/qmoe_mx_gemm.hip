@@ -5,7 +5,7 @@
 //   k_mx_tiles    M-tile work list of the grouped products (expert, first grouped pair, pairs)
 //   k_mx_grouped  one workgroup per tile of an expert's product; as gate and up it ends in
 //                 h = silu(g) u and its 4-bit blocks, as the down product in fp32 rows
-//   k_mx_combine  out[t] = residual[t] + sum_j w[t][j] y[t k + j], slot order, binary64 sum
+//   k_mx_combine  out[t] = residual[t] + sum_j w[t][j] y[place of pair t k + j], slot order, binary64
 //
 // Measured: 8192 rows by 4096 by 8192 columns 135 us, 4.1 PFLOP/s (the bare scaled matrix
 // instructions reach 6.6 on random codes, which the power limit sets, a bf16 product of the
@@ -33,6 +33,7 @@ struct GemmArgs {
   const uint8_t *w1, *s1;  // up
   const uint8_t *xq, *xs;  // codes and scales of the rows to multiply
   const int32_t* pair_index;
+  int32_t* place;        // [P] grouped place of each pair, which gate and up write
   const int4* tiles;
   const int* xcd_first;  // [kXcds + 1] first tile of each XCD
   int xcd_m;             // linear: XCDs side by side over the rows of x; an XCD's tiles are
@@ -42,7 +43,7 @@ struct GemmArgs {
   int rows;   // linear: rows of x
   int N, K;   // weight rows (of one expert) and the reduction axis
   int k;      // top_k
-  void* out;  // linear: rows; down: fp32 [P][N]
+  void* out;  // linear: rows; down: fp32 [P][N], in the order of the grouped pairs
   int out_dtype;
   int64_t out_stride;
   uint8_t *hq, *hs;  // gate and up: codes and scales of h [P]
@@ -638,8 +639,7 @@ __device__ __forceinline__ void rows_epilogue(T& c, const GemmArgs& a, int n0, i
         const int r = j * kStep + lane / kLanes;
         if (r >= count || col0 + col >= a.N) continue;
         const mx_f32x4 v = *reinterpret_cast<const lds_f32x4*>(lds + r * kPitch + col);
-        const size_t at = MODE == kDown ? (size_t)a.pair_index[m0 + first + r] * a.N
-                                        : (size_t)(m0 + first + r) * a.out_stride;
+        const size_t at = (size_t)(m0 + first + r) * (MODE == kDown ? a.N : a.out_stride);
         __builtin_nontemporal_store(
             v, reinterpret_cast<mx_f32x4*>(static_cast<float*>(a.out) + at + col0 + col));
       }
@@ -743,6 +743,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
   int mt, nt;
   if (!list_tile(a.xcd_first, ntn, mt, nt)) return;
   const int4 t = load_uniform(a.tiles + mt);
+  if (MODE == kGateUp && nt == 0 && (int)threadIdx.x < t.z)
+    a.place[a.pair_index[t.y + threadIdx.x]] = t.y + threadIdx.x;
   if (t.z <= 32)
     tile<Slots<S, SC, 3>, 1, 4, 2, 1, TAIL, MODE>(ring, a, t.x, nt * kN, t.y, t.z);
   else if (t.z <= 64)
@@ -836,12 +838,15 @@ __global__ __launch_bounds__(1024) void k_mx_tiles(const int32_t* __restrict__ o
 
 // ---------------------------------------------------------------- combine
 
-// Reads y once, sixteen slots' words in flight a thread: 5.1 TB/s.
+// Reads y once, sixteen slots' words in flight a thread: 5.1 TB/s. y lies in the order of the
+// grouped pairs: rows stored to the places of their tokens cost the down product of 8192 tokens 40
+// us more, and reading them from there nothing.
 constexpr int kCombineBatch = 16;
 
-__global__ __launch_bounds__(1024) void k_mx_combine(const float* __restrict__ y, const float* __restrict__ w,
-                                                     int d, int k, const float* residual, float* out) {
-  const int t = blockIdx.x;
+__global__ __launch_bounds__(1024) void k_mx_combine(const float* __restrict__ y, const int32_t* __restrict__ place,
+                                                     const float* __restrict__ w, int d, int k,
+                                                     const float* residual, float* out) {
+  const int t = blockIdx.x, P = gridDim.x * k;
   for (int c = 4 * threadIdx.x; c < d; c += 4 * blockDim.x) {
     double acc[4] = {0.0, 0.0, 0.0, 0.0};
     for (int j0 = 0; j0 < k; j0 += kCombineBatch) {
@@ -852,7 +857,9 @@ __global__ __launch_bounds__(1024) void k_mx_combine(const float* __restrict__ y
         if (j0 + i < k) {
           const size_t p = (size_t)t * k + j0 + i;
           wj[i] = w[p];
-          v[i] = __builtin_nontemporal_load(reinterpret_cast<const mx_f32x4*>(y + p * d + c));
+          // (a pair that the routing left out has no place: any of the rows)
+          const size_t g = min((unsigned)place[p], (unsigned)(P - 1));
+          v[i] = __builtin_nontemporal_load(reinterpret_cast<const mx_f32x4*>(y + g * d + c));
         }
 #pragma unroll
       for (int i = 0; i < kCombineBatch; ++i)
@@ -967,6 +974,7 @@ hipError_t launch_mx_ffn(const MxFfnArgs& a, hipStream_t stream) {
   const int max_mt = mx_max_mtiles(P, E);
   GemmArgs g{};
   g.pair_index = a.r->pair_index;
+  g.place = reinterpret_cast<int32_t*>(a.work + W.place);
   g.tiles = tiles;
   g.xcd_first = xcd_first;
   g.k = k;
@@ -1007,7 +1015,7 @@ hipError_t launch_mx_ffn(const MxFfnArgs& a, hipStream_t stream) {
   err = hipGetLastError();
   if (err != hipSuccess) return err;
   const int threads = std::min(1024, ((d / 4 + kWave - 1) / kWave) * kWave);
-  hipLaunchKernelGGL(k_mx_combine, dim3(n), dim3(threads), 0, stream, y, a.r->topk_w, d, k, a.residual,
+  hipLaunchKernelGGL(k_mx_combine, dim3(n), dim3(threads), 0, stream, y, g.place, a.r->topk_w, d, k, a.residual,
                      a.out);
   return hipGetLastError();
 }

@@ -242,9 +242,10 @@ inline int mx_max_mtiles(int P, int E) {
 struct MxFfnWs {
   size_t tiles;   // int4 [max M-tiles] (expert, first grouped pair, pairs, 0)
   size_t xcd_first;  // int [9] first tile of each XCD, and their number
+  size_t place;   // int [P] grouped place of each pair
   size_t xq, xs;  // codes and scales of x [n]
   size_t hq, hs;  // codes and scales of the hidden rows [P]
-  size_t y;       // fp32 [P][d]
+  size_t y;       // fp32 [P][d], grouped pairs
   size_t total;
 };
 
@@ -257,6 +258,8 @@ inline MxFfnWs mx_ffn_ws(int n, int k, int d, int f, int E) {
   if (!window) o = align256(o + 16 * (size_t)(mx_max_mtiles((int)P, E) + 1));
   W.xcd_first = o;
   if (!window) o = align256(o + 64);
+  W.place = o;
+  if (!window) o = align256(o + 4 * P);
   W.xq = o;
   if (!window) o = align256(o + (size_t)n * (d / 2));
   W.xs = o;
