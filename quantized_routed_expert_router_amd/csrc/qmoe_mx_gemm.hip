@@ -2,7 +2,8 @@
 // products of a batch or a prefill chunk.
 //
 //   k_mx_linear   one workgroup per tile of the product; rows out through LDS
-//   k_mx_tiles    M-tile work list of the grouped products (expert, first grouped pair, pairs)
+//   k_mx_prepare  M-tile work list of the grouped products (expert, first grouped pair, pairs), and
+//                 the rows of x in 4 bits
 //   k_mx_grouped  one workgroup per tile of an expert's product; as gate and up it ends in
 //                 h = silu(g) u and its 4-bit blocks, as the down product in fp32 rows
 //   k_mx_combine  out[t] = residual[t] + sum_j w[t][j] y[place of pair t k + j], slot order, binary64
@@ -794,10 +795,10 @@ __device__ __forceinline__ int2 block_scan(int2 v, int2* wsum) {
   return v;
 }
 
-// One workgroup: tiles in expert order, and the XCDs' shares of their cost. A thread finds an
-// expert's first tile; then the threads write the tiles, each looking its expert up.
-__global__ __launch_bounds__(1024) void k_mx_tiles(const int32_t* __restrict__ offsets, int E,
-                                                   int4* __restrict__ tiles, int* __restrict__ xcd_first) {
+// One workgroup of 1024: tiles in expert order, and the XCDs' shares of their cost. A thread finds
+// an expert's first tile; then the threads write the tiles, each looking its expert up.
+__device__ __forceinline__ void list_tiles(const int32_t* __restrict__ offsets, int E,
+                                           int4* __restrict__ tiles, int* __restrict__ xcd_first) {
   __shared__ int2 s_wsum[16];
   __shared__ int s_first[1024], s_cost[1024], s_beg[1025];
   __shared__ int2 s_total;
@@ -834,6 +835,25 @@ __global__ __launch_bounds__(1024) void k_mx_tiles(const int32_t* __restrict__ o
     }
   }
   if (tid <= kXcds && (tid == kXcds || ntiles == 0)) xcd_first[tid] = ntiles;
+}
+
+// What the grouped products need first: the first workgroup lists the tiles (5 us, one latency
+// after another) while the others quantize the rows.
+constexpr int kPrepareThreads = 1024;
+
+template <int DT, bool STRIDED>
+__global__ __launch_bounds__(kPrepareThreads) void k_mx_prepare(const char* __restrict__ x, int64_t words,
+                                                                int row_words, int64_t row_bytes,
+                                                                uint32_t* __restrict__ codes,
+                                                                uint8_t* __restrict__ scales,
+                                                                const int32_t* __restrict__ offsets, int E,
+                                                                int4* __restrict__ tiles,
+                                                                int* __restrict__ xcd_first) {
+  if (blockIdx.x == 0)
+    list_tiles(offsets, E, tiles, xcd_first);
+  else
+    mx_quantize_words<DT, STRIDED, kPrepareThreads>(x, words, row_words, row_bytes, codes, scales,
+                                                    (int64_t)blockIdx.x - 1);
 }
 
 // ---------------------------------------------------------------- combine
@@ -964,11 +984,18 @@ hipError_t launch_mx_ffn(const MxFfnArgs& a, hipStream_t stream) {
   float* y = reinterpret_cast<float*>(a.work + W.y);
   int4* tiles = reinterpret_cast<int4*>(a.work + W.tiles);
   int* xcd_first = reinterpret_cast<int*>(a.work + W.xcd_first);
-  hipLaunchKernelGGL(k_mx_tiles, dim3(1), dim3(1024), 0, stream, a.r->expert_offsets, E, tiles,
-                     xcd_first);
+  {
+    const int64_t words = (int64_t)n * (d / 8);
+    const int share = kPrepareThreads * kMxQuantUnroll;
+    const bool strided = n > 1 && a.row_stride != d;
+    auto kern = a.dtype == MOE_BF16  ? (strided ? k_mx_prepare<MOE_BF16, true> : k_mx_prepare<MOE_BF16, false>)
+                : a.dtype == MOE_F16 ? (strided ? k_mx_prepare<MOE_F16, true> : k_mx_prepare<MOE_F16, false>)
+                                     : (strided ? k_mx_prepare<MOE_F32, true> : k_mx_prepare<MOE_F32, false>);
+    hipLaunchKernelGGL(kern, dim3((unsigned)((words + share - 1) / share + 1)), dim3(kPrepareThreads), 0, stream,
+                       static_cast<const char*>(a.x), words, d / 8, a.row_stride * mx_type_size(a.dtype),
+                       reinterpret_cast<uint32_t*>(xq), xs, a.r->expert_offsets, E, tiles, xcd_first);
+  }
   hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return err;
-  err = launch_mx_quantize(MxQuantArgs{a.x, a.dtype, n, a.row_stride, d, xq, xs}, stream);
   if (err != hipSuccess) return err;
 
   const int max_mt = mx_max_mtiles(P, E);

@@ -148,6 +148,40 @@ __device__ __forceinline__ uint32_t mx_quad_max(uint32_t v) {
   return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));
 }
 
+// Codes and scales of a workgroup's share of rows: a quad of lanes holds a block, a lane 8
+// consecutive values (a word of codes). The loads of a thread's words are in flight at once.
+constexpr int kMxQuantUnroll = 4;
+
+template <int DT, bool STRIDED, int THREADS>
+__device__ __forceinline__ void mx_quantize_words(const char* __restrict__ x, int64_t words, int row_words,
+                                                  int64_t row_bytes, uint32_t* __restrict__ codes,
+                                                  uint8_t* __restrict__ scales, int64_t block) {
+  const int64_t first = block * (THREADS * kMxQuantUnroll) + threadIdx.x;
+  MxValues<DT> v[kMxQuantUnroll];
+#pragma unroll
+  for (int i = 0; i < kMxQuantUnroll; ++i) {
+    // words is a multiple of 4, so the lanes of a quad are inside or outside together
+    const int64_t at = min(first + i * THREADS, words - 4 + (threadIdx.x & 3));
+    if (STRIDED) {
+      const int64_t row = at / row_words;
+      v[i].load(x + row * row_bytes + (at - row * row_words) * (8 * mx_type_size(DT)));
+    } else {
+      v[i].load(x + at * (8 * mx_type_size(DT)));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kMxQuantUnroll; ++i) {
+    const int64_t at = first + i * THREADS;
+    const uint32_t s = mx_scale_byte(mx_quad_max(v[i].amax()));
+    // a block with an infinity or a NaN is NaN as a whole: its codes are zeros
+    const uint32_t c = s == 255u ? 0u : v[i].codes(mx_scale_float(s));
+    if (at < words) {
+      codes[at] = c;
+      if ((threadIdx.x & 3) == 0) scales[at >> 2] = (uint8_t)s;
+    }
+  }
+}
+
 // ---- the hidden vector's codes are those of its 64-bit value
 //
 // A 4-bit step is a quarter to a half of the value, so a last-bit difference in h next to a

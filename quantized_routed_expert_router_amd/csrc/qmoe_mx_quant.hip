@@ -12,37 +12,14 @@ namespace qmoe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;  // words of 8 values a thread: their loads are in flight at once
+constexpr int kUnroll = kMxQuantUnroll;
 
 template <int DT, bool STRIDED>
 __global__ __launch_bounds__(kThreads) void k_mx_quantize(const char* __restrict__ x, int64_t words,
                                                           int row_words, int64_t row_bytes,
                                                           uint32_t* __restrict__ codes,
                                                           uint8_t* __restrict__ scales) {
-  const int64_t first = (int64_t)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
-  MxValues<DT> v[kUnroll];
-#pragma unroll
-  for (int i = 0; i < kUnroll; ++i) {
-    // words is a multiple of 4, so the lanes of a quad are inside or outside together
-    const int64_t at = min(first + i * kThreads, words - 4 + (threadIdx.x & 3));
-    if (STRIDED) {
-      const int64_t row = at / row_words;
-      v[i].load(x + row * row_bytes + (at - row * row_words) * (8 * mx_type_size(DT)));
-    } else {
-      v[i].load(x + at * (8 * mx_type_size(DT)));
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kUnroll; ++i) {
-    const int64_t at = first + i * kThreads;
-    const uint32_t s = mx_scale_byte(mx_quad_max(v[i].amax()));
-    // a block with an infinity or a NaN is NaN as a whole: its codes are zeros
-    const uint32_t c = s == 255u ? 0u : v[i].codes(mx_scale_float(s));
-    if (at < words) {
-      codes[at] = c;
-      if ((threadIdx.x & 3) == 0) scales[at >> 2] = (uint8_t)s;
-    }
-  }
+  mx_quantize_words<DT, STRIDED, kThreads>(x, words, row_words, row_bytes, codes, scales, blockIdx.x);
 }
 
 template <int DT>
