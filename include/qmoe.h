@@ -27,6 +27,10 @@
  *                          most 8192 tokens) with bf16 dequantized weights, bf16
  *                          activations and fp32 accumulation on the matrix cores.
  *
+ * Beside it: the attention half of the layer (moe_qk_norm_rope, moe_kv_append, moe_attn_*),
+ * routing by a rule of scores, bias and groups (moe_route_scored), and products with weights in
+ * microscaled 4-bit floats, dense and of the routed experts (moe_mx_*).
+ *
  * Conventions for every entry point:
  *   * Pointers named device are GPU memory of the current HIP device; the caller owns
  *     all memory, including the workspace. The library allocates nothing.

@@ -5,6 +5,7 @@ Modules:
                compiled library is missing
     attention  binding of its attention half: head norms and rotation, paged key-value cache,
                decode-window and prefill attention
+    mx         binding of the microscaled 4-bit floats: quantization, products, routed experts
     synth      seeded synthetic inputs (host and device fills of the packed weights)
     workloads  synthetic layers and inputs in device memory
     build      hipcc build of the two shared libraries

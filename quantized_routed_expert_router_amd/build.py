@@ -4,7 +4,8 @@ Produced next to this file:
 
 * ``libqmoe.so``       - the MoE layer library (C ABI declared in ``include/qmoe.h``);
 * ``libqmoe_synth.so`` - the seeded input generator (host and device fill routines);
-* ``_fastcall.so``     - the short path of the attention half's Python calls (host code).
+* ``_fastcall.so``     - the short path of the Python calls of the attention half, of routing by
+  a rule and of the microscaled products (host code).
 
 Run ``python -m quantized_routed_expert_router_amd.build`` or call :func:`build`.
 """
