@@ -756,17 +756,26 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
 
 // The dense product: stages of whole lines, two slots. Of the 256 x 256 tile's 0.95 us per 128
 // values, the matrix instructions need 0.76 (without loads and LDS reads); a tile's start and end
-// cost 8 us, since it takes all of a CU's LDS and nothing runs beside it.
+// cost 8 us, since it takes all of a CU's LDS and nothing runs beside it. The smallest tile, which
+// runs where there are few, has room for four slots; it takes them where the scales' requests,
+// one a stage with a TAIL, stand between the codes' (517 rows by 1441 by 2080 columns 10.4 -> 9.8
+// us; without a TAIL 64 x 5120 x 2048 5.8 -> 6.2).
 template <int WM, int WN, int NW, int NX, bool TAIL>
 __global__ __launch_bounds__(kWave * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_mx_linear(
     GemmArgs a) {
   constexpr int BN = 32 * NW * WN, BM = 32 * NX * WM;
   typedef Stage<BN, BM, 8> S;
   typedef ScaleRing<BN, BM, TAIL ? 2 : 4> SC;
-  typedef Slots<S, SC, 2> R;
+  constexpr bool kDeep = TAIL && BN + BM <= 128;
+  typedef Slots<S, SC, kDeep ? 4 : 2> R;
   __shared__ S slot0, slot1;
   __shared__ SC scales;
-  const R ring{&slot0, &slot1, nullptr, nullptr, &scales};
+  R ring{&slot0, &slot1, nullptr, nullptr, &scales};
+  if constexpr (kDeep) {
+    __shared__ S slot2, slot3;
+    ring.s2 = &slot2;
+    ring.s3 = &slot3;
+  }
   const int ntn = (a.N + BN - 1) / BN;
   int mt, nt;
   if (!grid_tile(a, (a.rows + BM - 1) / BM, ntn, mt, nt)) return;
