@@ -137,6 +137,7 @@ moe_status moe_mx_quantize(const void* x, int dtype, int64_t rows, int cols, int
   const moe_status s = check_rows(x, dtype, rows, cols, row_stride);
   if (s != MOE_OK || rows == 0) return s;
   if (!codes || !scales || !aligned(codes, 16) || !aligned(scales, 16)) return MOE_ERR_INVALID_ARGUMENT;
+  if (rows == 1) row_stride = cols;  // whatever it said
   const Range in = rows_range(x, dtype, rows, cols, row_stride);
   const Range c = range(codes, (size_t)rows * (cols / 2)), sc = range(scales, (size_t)rows * (cols / kMxBlock));
   if (!disjoint(in, c) || !disjoint(in, sc) || !disjoint(c, sc)) return MOE_ERR_INVALID_ARGUMENT;
@@ -178,6 +179,10 @@ moe_status moe_mx_linear(const void* x, int dtype, int64_t row_stride, int n_tok
   s = check_rows(x, dtype, n_tokens, w->cols, row_stride);
   if (s != MOE_OK) return s;
   if (n_tokens == 0) return dtype_ok(out_dtype) ? MOE_OK : MOE_ERR_UNSUPPORTED;
+  if (n_tokens == 1) {
+    row_stride = w->cols;
+    out_stride = w->rows;
+  }
   Range o{};
   s = check_out(out, out_dtype, n_tokens, w->rows, out_stride, &o);
   if (s != MOE_OK) return s;
@@ -218,6 +223,7 @@ moe_status moe_mx_linear_quantized(const moe_mx_matrix* x, const moe_mx_matrix* 
   if (x->rows == 0) return dtype_ok(out_dtype) ? MOE_OK : MOE_ERR_UNSUPPORTED;
   s = check_matrix(x);
   if (s != MOE_OK) return s;
+  if (x->rows == 1) out_stride = w->rows;
   Range o{};
   s = check_out(out, out_dtype, x->rows, w->rows, out_stride, &o);
   if (s != MOE_OK) return s;
@@ -259,6 +265,7 @@ moe_status moe_mx_ffn(const moe_mx_layer* L, const void* x, int dtype, int64_t r
   if (n_tokens < 0 || n_tokens > MOE_MAX_PREFILL_TOKENS) return MOE_ERR_INVALID_ARGUMENT;
   s = check_rows(x, dtype, n_tokens, d, row_stride);
   if (s != MOE_OK || n_tokens == 0) return s;
+  if (n_tokens == 1) row_stride = d;
   if (!r || !r->topk_ids || !r->topk_w || !r->expert_offsets || !r->pair_index)
     return MOE_ERR_INVALID_ARGUMENT;
   if (!out || !aligned(out, 16) || !aligned(residual, 16)) return MOE_ERR_INVALID_ARGUMENT;
