@@ -984,7 +984,7 @@ hipError_t launch_mx_ffn(const MxFfnArgs& a, hipStream_t stream) {
   const moe_mx_layer& L = *a.L;
   const int n = a.n, d = L.d_model, f = L.d_ff, k = L.top_k, E = L.n_experts, P = n * k;
   if (P == 0) return hipSuccess;
-  if (mx_window(n, k)) return launch_mx_ffn_window(a, stream);
+  if (mx_window(n, k, d, f, E)) return launch_mx_ffn_window(a, stream);
   const MxFfnWs W = mx_ffn_ws(n, k, d, f, E);
   uint8_t* xq = reinterpret_cast<uint8_t*>(a.work + W.xq);
   uint8_t* xs = reinterpret_cast<uint8_t*>(a.work + W.xs);

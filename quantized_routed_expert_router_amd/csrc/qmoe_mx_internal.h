@@ -7,6 +7,8 @@
 // block's scale in a byte of a register.
 #pragma once
 
+#include <cmath>
+
 #include "qmoe_internal.h"
 
 namespace qmoe {
@@ -245,12 +247,22 @@ struct MxFfnArgs {
   char* work;
 };
 
-// Up to this many tokens the expert FFN runs on the window kernels (one workgroup per
-// touched expert and 32 rows), above it on the grouped matrix product.
+// Up to 16 tokens and 256 pairs the expert FFN runs on the window kernels (one workgroup per
+// touched expert and 32 rows), above on the grouped products, which take two launches and some
+// 13 us more but read an expert's down weights once for all its tokens. The window reads them
+// for each pair, at about 3 TB/s where an expert comes again: it is left where these readings,
+// with experts drawn evenly, are more than 40 MB. Measured, us, window and grouped: 512 experts of
+// 768 x 2048, top 10, 16 tokens 83 and 94; 64 of 1024 x 2048, top 8, 8 tokens 45 and 48, 10 tokens
+// 55 and 51; 8 of 4096 x 4096, top 2, 4 tokens 43 and 53, 6 tokens 65 and 56, 16 tokens 119 and 60.
 constexpr int kMxWindowTokens = 16;
 constexpr int kMxWindowPairs = 256;
 
-inline bool mx_window(int n, int k) { return n <= kMxWindowTokens && n * k <= kMxWindowPairs; }
+inline bool mx_window(int n, int k, int d, int f, int E) {
+  const int P = n * k;
+  if (n > kMxWindowTokens || P > kMxWindowPairs) return false;
+  const double again = P - E * (1.0 - std::pow(1.0 - 1.0 / E, P));
+  return again * d * (f / 2 + f / kMxBlock) <= 40e6;
+}
 
 // Whether a linear product runs on the window kernel: the rows to multiply are then quantized in
 // LDS (up to 70 KB at 16 rows of 8192) and need no workspace. Weights with fewer than 16 scales
@@ -287,7 +299,7 @@ inline MxFfnWs mx_ffn_ws(int n, int k, int d, int f, int E) {
   MxFfnWs W{};
   size_t o = 0;
   const size_t P = (size_t)n * k;
-  const bool window = mx_window(n, k);
+  const bool window = mx_window(n, k, d, f, E);
   W.tiles = o;
   if (!window) o = align256(o + 16 * (size_t)(mx_max_mtiles((int)P, E) + 1));
   W.xcd_first = o;

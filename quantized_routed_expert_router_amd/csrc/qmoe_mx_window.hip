@@ -366,18 +366,21 @@ __global__ __launch_bounds__(kThreads) void k_mx_win_gateup(
 
 // ---------------------------------------------------------------- down and combine
 
-constexpr int kDownThreads = 512;
-constexpr int kDownRows = 16;                                  // of d
-constexpr int kDownParts = 2;                                  // of the reduction axis
-constexpr int kDownLanes = kDownThreads / kWave / kDownParts;  // slots at once
+constexpr int kDownRows = 16;  // of d
+constexpr int kDownParts = 2;  // of the reduction axis
 
 // 16 rows of d of one token. An instruction multiplies one slot's rows; its columns all hold the
 // slot's hidden row (a window has too few rows to fill them). The workgroups of one row tile (of
 // all tokens) run on one XCD, whose L2 keeps the rows of an expert that several tokens share.
-__global__ __launch_bounds__(kDownThreads, 4) void k_mx_win_down(
+// THREADS: 4 or 8 slots at once. 8 where every workgroup has a CU of its own (d = 2048, top 10, us a
+// call with 512 and 1024 threads: 1 token 16.3 and 14.8, 2 tokens 18.3 and 17.4), 4 where they
+// share CUs (8 tokens 28.4 and 29.4, 16 tokens 44.3 and 46.5).
+template <int THREADS>
+__global__ __launch_bounds__(THREADS, 4) void k_mx_win_down(
     const int32_t* __restrict__ ids, const float* __restrict__ wt, int n, int k, int d, int f, int E,
     const uint8_t* __restrict__ dq, const uint8_t* __restrict__ ds, const uint8_t* __restrict__ hq,
     const uint8_t* __restrict__ hs, const float* residual, float* out) {
+  constexpr int kDownLanes = THREADS / kWave / kDownParts;  // slots at once
   __shared__ __attribute__((aligned(16))) float part[kDownParts][MOE_MAX_TOP_K][kDownRows];
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
@@ -467,9 +470,11 @@ hipError_t launch_mx_ffn_window(const MxFfnArgs& a, hipStream_t stream) {
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   const int tiles = d / kDownRows;
-  hipLaunchKernelGGL(k_mx_win_down, dim3((tiles + 7) / 8 * 8 * a.n), dim3(kDownThreads), 0, stream,
-                     a.r->topk_ids, a.r->topk_w, a.n, k, d, f, L.n_experts, L.down.codes, L.down.scales, hq,
-                     hs, a.residual, a.out);
+  const bool alone = tiles * a.n <= device_cu_count();
+  auto down = alone ? k_mx_win_down<1024> : k_mx_win_down<512>;
+  hipLaunchKernelGGL(down, dim3((tiles + 7) / 8 * 8 * a.n), dim3(alone ? 1024 : 512), 0, stream, a.r->topk_ids,
+                     a.r->topk_w, a.n, k, d, f, L.n_experts, L.down.codes, L.down.scales, hq, hs, a.residual,
+                     a.out);
   return hipGetLastError();
 }
 

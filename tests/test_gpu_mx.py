@@ -265,6 +265,19 @@ def test_ffn_uneven_experts(n):
     _check_ffn(layer, x, r, residual, mx.ffn(layer, x, r, residual))
 
 
+@pytest.mark.parametrize("n", [1, 5, 6, 16])
+def test_ffn_few_large_experts(n):
+    # few tokens whose pairs read the same large experts: on both sides of the window's end
+    layer = _layer(2, 2048, 4096, 2, seed=41)
+    x, residual = _normal((n, 2048), "bf16", seed=n), _normal((n, 2048), "f32", seed=42)
+    r = _routing(n, 2, 2, seed=43)
+    out = mx.ffn(layer, x, r, residual)
+    _check_ffn(layer, x, r, residual, out)
+    assert torch.equal(mx.ffn(layer, x, r, residual), out)
+    ws = torch.empty(mx.ffn_workspace_bytes(layer, n), dtype=torch.uint8, device="cuda")
+    assert torch.equal(mx.ffn(layer, x, r, residual, ws=ws), out)
+
+
 @pytest.mark.parametrize("n", [1, 4, 20, 300])
 def test_ffn_same_rows_whatever_the_batch(n):
     # a token's result does not depend on the others, nor on the path that its batch takes
