@@ -531,7 +531,8 @@ typedef struct {
  * weighted sum is binary64 and is rounded once. x: n_tokens rows of d values as in
  * moe_mx_quantize. residual: device fp32 [n][d] or NULL (zeros); out: device fp32 [n][d], which
  * may be residual; both 16-byte aligned, and otherwise out overlaps no input. r: routing of
- * moe_route or moe_route_scored for the same n, E and k. ws: device workspace of
+ * moe_route or moe_route_scored for the same n, E and k, or one in their form; a pair whose id is
+ * outside 0..E-1, and which the groups then leave out, adds nothing. ws: device workspace of
  * moe_mx_ffn_workspace_bytes bytes, 256-byte aligned, no initialisation needed. One entry
  * point serves single tokens, verify windows and prefill chunks. n_tokens <=
  * MOE_MAX_PREFILL_TOKENS; n_tokens == 0 enqueues nothing. */

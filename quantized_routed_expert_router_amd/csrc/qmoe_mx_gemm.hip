@@ -756,7 +756,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
 
 // The dense product: stages of whole lines, two slots. Of the 256 x 256 tile's 0.95 us per 128
 // values, the matrix instructions need 0.76 (without loads and LDS reads); a tile's start and end
-// cost 8 us, since it takes all of a CU's LDS and nothing runs beside it. The smallest tile, which
+// cost 8 us (2 the start, 2 the rows' way through LDS, 4 their stores), since it takes all of a
+// CU's LDS and nothing runs beside it. The smallest tile, which
 // runs where there are few, has room for four slots; it takes them where the scales' requests,
 // one a stage with a TAIL, stand between the codes' (517 rows by 1441 by 2080 columns 10.4 -> 9.8
 // us; without a TAIL 64 x 5120 x 2048 5.8 -> 6.2).
@@ -873,35 +874,44 @@ __global__ __launch_bounds__(kPrepareThreads) void k_mx_prepare(const char* __re
 constexpr int kCombineBatch = 16;
 
 __global__ __launch_bounds__(1024) void k_mx_combine(const float* __restrict__ y, const int32_t* __restrict__ place,
-                                                     const float* __restrict__ w, int d, int k,
+                                                     const int32_t* __restrict__ ids,
+                                                     const float* __restrict__ w, int E, int d, int k,
                                                      const float* residual, float* out) {
-  const int t = blockIdx.x, P = gridDim.x * k;
-  for (int c = 4 * threadIdx.x; c < d; c += 4 * blockDim.x) {
+  const int t = blockIdx.x, P = gridDim.x * k, lane = threadIdx.x & (kWave - 1);
+  // lane j: weight and row of slot j. A pair of no expert has no place and adds nothing.
+  const size_t pair = (size_t)t * k + min(lane, k - 1);
+  const bool in = (unsigned)ids[pair] < (unsigned)E;
+  const int my_row = min((unsigned)place[pair], (unsigned)(P - 1));
+  const int row_of = in ? my_row : -1;
+  const float my_w = in ? w[pair] : 0.0f;
+  // Every lane stays in the loop, since any may hold a slot: lanes past d read its last columns.
+  for (int c0 = 0; c0 < d; c0 += 4 * blockDim.x) {
+    const int c = min(c0 + 4 * (int)threadIdx.x, d - 4);
     double acc[4] = {0.0, 0.0, 0.0, 0.0};
     for (int j0 = 0; j0 < k; j0 += kCombineBatch) {
       mx_f32x4 v[kCombineBatch];
-      float wj[kCombineBatch];
 #pragma unroll
       for (int i = 0; i < kCombineBatch; ++i)
         if (j0 + i < k) {
-          const size_t p = (size_t)t * k + j0 + i;
-          wj[i] = w[p];
-          // (a pair that the routing left out has no place: any of the rows)
-          const size_t g = min((unsigned)place[p], (unsigned)(P - 1));
-          v[i] = __builtin_nontemporal_load(reinterpret_cast<const mx_f32x4*>(y + g * d + c));
+          const int g = __builtin_amdgcn_readlane(row_of, j0 + i);
+          v[i] = mx_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+          if (g >= 0)
+            v[i] = __builtin_nontemporal_load(reinterpret_cast<const mx_f32x4*>(y + (size_t)g * d + c));
         }
 #pragma unroll
       for (int i = 0; i < kCombineBatch; ++i)
-        if (j0 + i < k)
+        if (j0 + i < k) {
+          const float wj = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_w), j0 + i));
 #pragma unroll
-          for (int q = 0; q < 4; ++q) acc[q] += (double)wj[i] * (double)v[i][q];
+          for (int q = 0; q < 4; ++q) acc[q] += (double)wj * (double)v[i][q];
+        }
     }
     const size_t at = (size_t)t * d + c;
     mx_f32x4 r = {0.0f, 0.0f, 0.0f, 0.0f};
     if (residual) r = *reinterpret_cast<const mx_f32x4*>(residual + at);
 #pragma unroll
     for (int q = 0; q < 4; ++q) r[q] = (float)((double)r[q] + acc[q]);
-    *reinterpret_cast<mx_f32x4*>(out + at) = r;
+    if (c0 + 4 * (int)threadIdx.x < d) *reinterpret_cast<mx_f32x4*>(out + at) = r;
   }
 }
 
@@ -1051,7 +1061,7 @@ hipError_t launch_mx_ffn(const MxFfnArgs& a, hipStream_t stream) {
   err = hipGetLastError();
   if (err != hipSuccess) return err;
   const int threads = std::min(1024, ((d / 4 + kWave - 1) / kWave) * kWave);
-  hipLaunchKernelGGL(k_mx_combine, dim3(n), dim3(threads), 0, stream, y, g.place, a.r->topk_w, d, k, a.residual,
+  hipLaunchKernelGGL(k_mx_combine, dim3(n), dim3(threads), 0, stream, y, g.place, a.r->topk_ids, a.r->topk_w, E, d, k, a.residual,
                      a.out);
   return hipGetLastError();
 }

@@ -311,6 +311,29 @@ def test_ffn_repeated_and_missing_experts(n):
         _check_ffn(layer, x, r, residual, mx.ffn(layer, x, r, residual))
 
 
+@pytest.mark.parametrize("n", [3, 40, 300])
+def test_ffn_pairs_of_no_expert(n):
+    # a record that keeps the pairs of some experts only, as a shard of them has it: a token with
+    # none of its pairs left keeps its residual, and what the workspace held does not matter
+    layer = _layer(6, 128, 64, 4, seed=17)
+    x, residual = _normal((n, 128), "bf16", seed=18), _normal((n, 128), "f32", seed=19)
+    ids = torch.randint(0, 6, (n, 4), generator=_gen(20), dtype=torch.int32)
+    drop = torch.rand((n, 4), generator=_gen(21)) < 0.4
+    drop[1] = True
+    ids[drop] = torch.where(torch.rand(int(drop.sum()), generator=_gen(22)) < 0.5, -1, 6).int()
+    flat = ids.view(-1).numpy()
+    pairs = np.argsort(flat, kind="stable")
+    pairs = pairs[(flat[pairs] >= 0) & (flat[pairs] < 6)]
+    offsets = np.concatenate(([0], np.bincount(flat[pairs], minlength=6).cumsum())).astype(np.int32)
+    pairs = np.concatenate((pairs, np.zeros(4 * n - len(pairs)))).astype(np.int32)
+    w = torch.rand((n, 4), generator=_gen(23)).cuda()
+    r = qmoe.Routing(ids.cuda(), w, torch.from_numpy(offsets).cuda(), torch.from_numpy(pairs).cuda())
+    ws = torch.full((mx.ffn_workspace_bytes(layer, n),), 0xff, dtype=torch.uint8, device="cuda")
+    out = mx.ffn(layer, x, r, residual, ws=ws)
+    _check_ffn(layer, x, r, residual, out)
+    assert torch.equal(out[1], residual[1])
+
+
 @pytest.mark.parametrize("n", [5, 70])
 def test_ffn_zero_rows_nan_rows_and_ends(n):
     layer = _layer(8, 256, 128, 2, seed=13)
