@@ -400,7 +400,9 @@ __global__ __launch_bounds__(THREADS, 4) void k_mx_win_down(
   // the experts and the weights of the token's slots, one a lane, and the residual that the end
   // needs: requested together
   const int my_e = ids[(size_t)t * k + min(lane, k - 1)];
-  const float my_w = wt[(size_t)t * k + min(lane, k - 1)];
+  const float slot_w = wt[(size_t)t * k + min(lane, k - 1)];
+  // a pair of no expert adds nothing, whatever its weight
+  const float my_w = (unsigned)my_e < (unsigned)E ? slot_w : 0.0f;
   const size_t at = (size_t)t * d + r0 + r;
   const float my_r = residual ? residual[at] : 0.0f;
   for (int j = first; j < k; j += kDownLanes) {
