@@ -520,10 +520,13 @@ __device__ __forceinline__ void hidden_block(const mx_f32x16& g, const mx_f32x16
     pieces[p] = lo;
   }
   if (!__ballot(odd || differ)) return;
-  // a block of zeros (a row of zeros) is what it is
+  // a block of zeros (a row of zeros) is what it is; a NaN or an infinity times 0 is no zero
   bool some = m != 0.0f;
 #pragma unroll
-  for (int j = 0; j < 16; ++j) some |= g[j] != 0.0f && u[j] != 0.0f;
+  for (int j = 0; j < 16; ++j) {
+    const float size = fabsf(g[j]) + fabsf(u[j]);
+    some |= (g[j] != 0.0f && u[j] != 0.0f) || !(size < __builtin_inff());
+  }
   some |= __shfl_xor((int)some, 32) != 0;
   odd = odd && some;
   lds_float* gu = stage();
