@@ -14,8 +14,10 @@ from dataclasses import dataclass
 
 import torch
 
-from .qmoe import (BYTES, F32, FLOATS, MOE_OK, MoeError, Routing, _Args, _current_device, _fastcall,
-                   _ptr, _raw_stream, _Routing, lib)
+from .qmoe import (BYTES, F32, FLOATS, MOE_OK, MoeError, Routing, _Args, _current_device,
+                   _load_fastcall, _ptr, _raw_stream, _Routing, lib)
+
+_fastcall = _load_fastcall()
 
 BLOCK = 32  # values that share a scale
 U8 = (torch.uint8,)

@@ -114,11 +114,21 @@ def _load():
 
 lib = _load()
 
+
+def _load_fastcall():
+    """The native short path, which links against the library loaded above and against torch."""
+    try:
+        from . import _fastcall
+    except ImportError as e:
+        raise ImportError("_fastcall.so is missing or does not load: build it with "
+                          "`python -m quantized_routed_expert_router_amd.build`") from e
+    return _fastcall
+
+
 try:
-    from . import _fastcall  # noqa: E402  (links against the library loaded above)
-except ImportError as e:
-    raise ImportError("_fastcall.so is missing or does not load: build it with "
-                      "`python -m quantized_routed_expert_router_amd.build`") from e
+    _fastcall = _load_fastcall()
+except ImportError:  # of the calls here only route_scored needs it, and says so
+    _fastcall = None
 
 
 def _raw_stream(device: int) -> int:
@@ -352,9 +362,9 @@ def route_scored(logits: torch.Tensor, top_k: int, rule: RouteRule, out: Routing
             logits.is_cuda:
         gpu = _current_device()
         keep = rule.groups if rule.top_groups is None else rule.top_groups
-        r = _fastcall.route_scored(gpu, logits, top_k, SCORES.get(rule.score), rule.bias, rule.groups,
-                                   keep, GROUP_SCORES.get(rule.group_score), rule.renormalize,
-                                   rule.scale, _raw_stream(gpu))
+        r = (_fastcall or _load_fastcall()).route_scored(
+            gpu, logits, top_k, SCORES.get(rule.score), rule.bias, rule.groups, keep,
+            GROUP_SCORES.get(rule.group_score), rule.renormalize, rule.scale, _raw_stream(gpu))
         if r is not None:
             if type(r) is int:
                 raise MoeError("moe_route_scored", r)
