@@ -15,7 +15,7 @@ from dataclasses import dataclass
 import torch
 
 from .qmoe import (BYTES, F32, FLOATS, MOE_OK, MoeError, Routing, _Args, _current_device,
-                   _load_fastcall, _ptr, _raw_stream, _Routing, lib)
+                   _int, _load_fastcall, _ptr, _raw_stream, _Routing, lib)
 
 _fastcall = _load_fastcall()
 
@@ -88,9 +88,8 @@ class MxMatrix:
         if shape is not None and (*c[:-1], self.cols) != tuple(shape):
             raise ValueError(f"{name}: shape {(*c[:-1], self.cols)}, expected {tuple(shape)}")
         args.need(self.scales, f"{name}.scales", U8, shape=(*c[:-1], self.cols // BLOCK))
-        most = 0x7fffffff  # stays out of range where it does not fit
-        return _MxMatrix(self.codes.data_ptr(), self.scales.data_ptr(), min(self.rows, most),
-                         min(self.cols, most))
+        return _MxMatrix(self.codes.data_ptr(), self.scales.data_ptr(), _int(self.rows),
+                         _int(self.cols))
 
 
 @dataclass
@@ -110,7 +109,7 @@ class MxLayer:
 
     def check(self, args: _Args) -> _MxLayer:
         E, f, d = self._shape()
-        return _MxLayer(d, f, E, self.top_k, self.gate.check("gate", args, 3),
+        return _MxLayer(_int(d), _int(f), _int(E), _int(self.top_k), self.gate.check("gate", args, 3),
                         self.up.check("up", args, 3, (E, f, d)),
                         self.down.check("down", args, 3, (E, d, f)))
 
@@ -150,9 +149,9 @@ def _current() -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
-def _count(n: int) -> None:
+def _count(n: int, what: str = "rows") -> None:
     if n > 0x7fffffff:  # would not reach the library as it is
-        raise ValueError(f"x: {n} rows")
+        raise ValueError(f"x: {n} {what}")
 
 
 def _done(fn: str, rc: int) -> None:
@@ -186,6 +185,7 @@ def quantize(x: torch.Tensor, out: MxMatrix | None = None, stream=None) -> MxMat
     cols = x.shape[-1]
     if cols % BLOCK or cols == 0:
         raise ValueError(f"x: {cols} columns, expected a multiple of {BLOCK}")
+    _count(cols, "columns")
     if out is not None:
         out.check("out", args, x.dim(), x.shape)
     device = args.gpu()
@@ -285,8 +285,8 @@ def linear(x: torch.Tensor | MxMatrix, w: MxMatrix, out: torch.Tensor | None = N
 def ffn_workspace_bytes(layer: MxLayer, n_tokens: int) -> int:
     """Bytes of the workspace of `ffn`; 0 for sizes out of range."""
     E, f, d = layer._shape()
-    st = _MxLayer(d, f, E, layer.top_k)
-    return int(lib.moe_mx_ffn_workspace_bytes(ctypes.byref(st), n_tokens))
+    st = _MxLayer(_int(d), _int(f), _int(E), _int(layer.top_k))
+    return int(lib.moe_mx_ffn_workspace_bytes(ctypes.byref(st), _int(n_tokens)))
 
 
 def ffn(layer: MxLayer, x: torch.Tensor, routing: Routing, residual: torch.Tensor | None = None,

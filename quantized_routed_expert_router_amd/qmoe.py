@@ -143,6 +143,11 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
+def _int(n: int) -> int:
+    """n as the library takes it: it stays out of range where it does not fit."""
+    return max(-1, min(n, 0x7fffffff))
+
+
 class _Args:
     """Checks of the tensors of one call before their pointers go to the library: first
     each tensor's dtype, layout and extent (need), then that all of them sit on one GPU
@@ -349,7 +354,7 @@ class RouteRule:
             raise ValueError(f"group_score: {self.group_score!r}, expected one of "
                              f"{tuple(GROUP_SCORES)}")
         keep = self.groups if self.top_groups is None else self.top_groups
-        return _RouteRule(SCORES[self.score], _ptr(self.bias), self.groups, keep,
+        return _RouteRule(SCORES[self.score], _ptr(self.bias), _int(self.groups), _int(keep),
                           GROUP_SCORES[self.group_score], 1 if self.renormalize else 0, self.scale)
 
 
@@ -379,6 +384,8 @@ def route_scored(logits: torch.Tensor, top_k: int, rule: RouteRule, out: Routing
     n, E = logits.shape
     args = _Args()
     args.need(logits, "logits", tuple(FLOATS))
+    if max(n, E, top_k) > 0x7fffffff:  # would not reach the library as it is
+        raise ValueError(f"logits: {n} rows of {E}, top_k {top_k}")
     if rule.bias is not None:
         args.need(rule.bias, "bias", F32, shape=(E,))
     if out is not None:
