@@ -384,7 +384,7 @@ def route_scored(logits: torch.Tensor, top_k: int, rule: RouteRule, out: Routing
     n, E = logits.shape
     args = _Args()
     args.need(logits, "logits", tuple(FLOATS))
-    if max(n, E, top_k) > 0x7fffffff:  # would not reach the library as it is
+    if max(n, E, abs(top_k)) > 0x7fffffff:  # would not reach the library as it is
         raise ValueError(f"logits: {n} rows of {E}, top_k {top_k}")
     if rule.bias is not None:
         args.need(rule.bias, "bias", F32, shape=(E,))

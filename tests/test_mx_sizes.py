@@ -22,7 +22,7 @@ def test_quantize_columns(rows):
         mx.quantize(_meta(2, rows, WRAPS + 64, dtype=torch.float32))
 
 
-@pytest.mark.parametrize("n,E,k", [(WRAPS + 4, 8, 2), (4, WRAPS + 8, 2), (4, 8, WRAPS + 2)])
+@pytest.mark.parametrize("n,E,k", [(WRAPS + 4, 8, 2), (4, WRAPS + 8, 2), (4, 8, WRAPS + 2), (4, 8, 2 - WRAPS)])
 def test_route_sizes(n, E, k):
     with pytest.raises(ValueError, match="rows of"):
         qmoe.route_scored(_meta(n, E, dtype=torch.bfloat16), k, qmoe.RouteRule())
