@@ -83,7 +83,7 @@ class MxMatrix:
         c = tuple(self.codes.shape)
         if len(c) < 2 or (dims is not None and len(c) != dims):
             raise ValueError(f"{name}.codes: shape {c}, expected {dims or 'at least 2'} axes")
-        if self.cols % BLOCK:
+        if self.cols % BLOCK or self.cols == 0:
             raise ValueError(f"{name}: {self.cols} columns, expected a multiple of {BLOCK}")
         if shape is not None and (*c[:-1], self.cols) != tuple(shape):
             raise ValueError(f"{name}: shape {(*c[:-1], self.cols)}, expected {tuple(shape)}")
