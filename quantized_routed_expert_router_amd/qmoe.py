@@ -369,7 +369,7 @@ def route_scored(logits: torch.Tensor, top_k: int, rule: RouteRule, out: Routing
         keep = rule.groups if rule.top_groups is None else rule.top_groups
         r = (_fastcall or _load_fastcall()).route_scored(
             gpu, logits, top_k, SCORES.get(rule.score), rule.bias, rule.groups, keep,
-            GROUP_SCORES.get(rule.group_score), rule.renormalize, rule.scale, _raw_stream(gpu))
+            GROUP_SCORES.get(rule.group_score), 1 if rule.renormalize else 0, rule.scale, _raw_stream(gpu))
         if r is not None:
             if type(r) is int:
                 raise MoeError("moe_route_scored", r)
