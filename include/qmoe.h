@@ -502,7 +502,8 @@ moe_status moe_mx_dequantize(const moe_mx_matrix* m, int64_t rows, int dtype, vo
 /* out[t][r] = sum_c Q(x)[t][c] * w[r][c] with Q as moe_mx_quantize: products and scales exact,
  * sums fp32, rounded once to out_dtype. x: n_tokens rows as in moe_mx_quantize (cols = w->cols).
  * out: device, w->rows values a row, rows out_stride elements apart, aligned to their size,
- * overlapping none of the inputs. n_tokens <= MOE_MAX_ROUTE_TOKENS. ws: device workspace of
+ * overlapping none of the inputs (rows of x and of out one distance apart may be columns of one
+ * buffer). n_tokens <= MOE_MAX_ROUTE_TOKENS. ws: device workspace of
  * moe_mx_linear_workspace_bytes bytes, 256-byte aligned, no initialisation needed (NULL when
  * that is 0). */
 size_t moe_mx_linear_workspace_bytes(int n_tokens, int cols);

@@ -38,6 +38,19 @@ Range rows_range(const void* x, int dtype, int64_t rows, int cols, int64_t strid
   return range(x, ((size_t)(rows - 1) * (rows > 1 ? (size_t)stride : 0) + cols) * mx_type_size(dtype));
 }
 
+// Whether n rows of a and n of b certainly share no byte: their ranges are apart, or rows of both
+// lie one distance apart and each row's parts side by side in it (columns of one buffer).
+bool rows_apart(const void* a, int64_t a_step, int64_t a_bytes, const void* b, int64_t b_step, int64_t b_bytes,
+                int n) {
+  const Range ra = range(a, (size_t)((n - 1) * a_step + a_bytes)), rb = range(b, (size_t)((n - 1) * b_step + b_bytes));
+  if (disjoint(ra, rb)) return true;
+  if (n == 1 || a_step != b_step || a_step <= 0) return false;
+  // from the start of a row of a to that of the next row of b
+  const uintptr_t step = (uintptr_t)a_step, ahead = rb.lo % step, at = ra.lo % step;
+  const uintptr_t gap = ahead >= at ? ahead - at : ahead + step - at;
+  return gap >= (uintptr_t)a_bytes && gap + (uintptr_t)b_bytes <= step;
+}
+
 moe_status check_matrix(const moe_mx_matrix* m) {
   if (!m) return MOE_ERR_INVALID_ARGUMENT;
   if (m->rows < 1 || m->rows > MOE_MX_MAX_ROWS) return MOE_ERR_INVALID_ARGUMENT;
@@ -187,7 +200,9 @@ moe_status moe_mx_linear(const void* x, int dtype, int64_t row_stride, int n_tok
   s = check_out(out, out_dtype, n_tokens, w->rows, out_stride, &o);
   if (s != MOE_OK) return s;
   const Range in = rows_range(x, dtype, n_tokens, w->cols, row_stride);
-  if (!disjoint(o, in) || !disjoint(o, codes_range(*w, 1)) || !disjoint(o, scales_range(*w, 1)))
+  const int64_t xs = mx_type_size(dtype), os = mx_type_size(out_dtype);
+  if (!rows_apart(x, row_stride * xs, w->cols * xs, out, out_stride * os, w->rows * os, n_tokens) ||
+      !disjoint(o, codes_range(*w, 1)) || !disjoint(o, scales_range(*w, 1)))
     return MOE_ERR_INVALID_ARGUMENT;
   const size_t need = mx_linear_ws(n_tokens, w->cols);
   if (need > 0) {
