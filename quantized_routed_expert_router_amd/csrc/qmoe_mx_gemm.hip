@@ -708,7 +708,7 @@ __device__ __forceinline__ void tile(const R& ring, const GemmArgs& a, int e, in
 // tiles of an expert then read its weights, and a tile's workgroups its rows of x, through one
 // L2. (Gate and up of 8192 tokens 282 us dealt out tile by tile, 267 in runs; of 256 tokens, whose
 // experts have one tile each, 162 and 161.)
-constexpr int kXcds = 8;
+constexpr int kXcds = kMxXcds;
 
 __device__ __forceinline__ bool list_tile(const int* xcd_first, int ntn, int& mt, int& nt) {
   const int x = (int)blockIdx.x % kXcds, slot = (int)blockIdx.x / kXcds;
@@ -788,11 +788,6 @@ __global__ __launch_bounds__(kWave * WM * WN) __attribute__((amdgpu_waves_per_eu
 
 // ---------------------------------------------------------------- work list
 
-// A tile's cost in the split of the list over the XCDs: 4 for its weights and 1 for each 32 rows
-// of x. By loads alone it would be 8 to 1, by products 0; between them, since neither hides the
-// other wholly.
-constexpr int kTileCost = 4;
-
 // Inclusive scan over the workgroup (1024 threads) of two values at once.
 __device__ __forceinline__ int2 block_scan(int2 v, int2* wsum) {
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
@@ -819,7 +814,7 @@ __device__ __forceinline__ void list_tiles(const int32_t* __restrict__ offsets, 
   const int beg = offsets[min(tid, E)];
   const int m = tid < E ? offsets[tid + 1] - beg : 0;
   const int count = (m + kMxBM - 1) / kMxBM;
-  const int2 mine = make_int2(count, kTileCost * count + (m + 31) / 32);
+  const int2 mine = make_int2(count, mx_tiles_cost(count, m));
   const int2 incl = block_scan(mine, s_wsum);
   s_first[tid] = incl.x - mine.x;
   s_cost[tid] = incl.y - mine.y;
@@ -837,15 +832,8 @@ __device__ __forceinline__ void list_tiles(const int32_t* __restrict__ offsets, 
     const int i = j - s_first[lo], g0 = s_beg[lo] + i * kMxBM;
     const int rows = min(kMxBM, s_beg[lo + 1] - g0);
     tiles[j] = make_int4(lo, g0, rows, 0);
-    // XCD x starts at the first tile whose cost before it is x / 8 of the whole or more
-    const int cost = s_cost[lo] + i * (kTileCost + kMxBM / 32);
-    const int next = cost + kTileCost + (rows + 31) / 32;
-#pragma unroll
-    for (int x = 0; x < kXcds; ++x) {
-      const long long at = (long long)x * total;
-      if (at == (long long)cost * kXcds) xcd_first[x] = j;
-      else if (at > (long long)cost * kXcds && at < (long long)next * kXcds) xcd_first[x] = j + 1;
-    }
+    const int cost = s_cost[lo] + mx_tiles_cost(i, i * kMxBM);
+    mx_xcd_starts(j, cost, cost + mx_tiles_cost(1, rows), total, xcd_first);
   }
   if (tid <= kXcds && (tid == kXcds || ntiles == 0)) xcd_first[tid] = ntiles;
 }
@@ -916,13 +904,6 @@ __global__ __launch_bounds__(1024) void k_mx_combine(const float* __restrict__ y
     for (int q = 0; q < 4; ++q) r[q] = (float)((double)r[q] + acc[q]);
     if (c0 + 4 * (int)threadIdx.x < d) *reinterpret_cast<mx_f32x4*>(out + at) = r;
   }
-}
-
-// Workgroups that cover the tiles of any XCD: its share of the cost is at most an eighth of the
-// whole and one tile, a tile costs kTileCost + 1 to kTileCost + 4.
-inline int list_grid(int max_mt, int ntn) {
-  const int most = ((kTileCost + 4) * ((max_mt + kXcds - 1) / kXcds + 1)) / (kTileCost + 1) + 2;
-  return kXcds * std::min(max_mt, most) * ntn;
 }
 
 // Splits the tiles over the XCDs: the split that leaves the largest share smallest, of those the
@@ -1039,7 +1020,7 @@ hipError_t launch_mx_ffn(const MxFfnArgs& a, hipStream_t stream) {
   g.xrows = n;
   g.hq = hq;
   g.hs = hs;
-  const dim3 gu(list_grid(max_mt, (f + 127) / 128));
+  const dim3 gu(mx_list_grid(max_mt, (f + 127) / 128));
   if (d % 256 == 0)
     hipLaunchKernelGGL((k_mx_grouped<false, kGateUp>), gu, dim3(kThreads), 0, stream, g);
   else
@@ -1056,7 +1037,7 @@ hipError_t launch_mx_ffn(const MxFfnArgs& a, hipStream_t stream) {
   g.wrows = (int64_t)E * d;
   g.xrows = P;
   g.out = y;
-  const dim3 dn(list_grid(max_mt, (d + 255) / 256));
+  const dim3 dn(mx_list_grid(max_mt, (d + 255) / 256));
   if (f % 256 == 0)
     hipLaunchKernelGGL((k_mx_grouped<false, kDown>), dn, dim3(kThreads), 0, stream, g);
   else

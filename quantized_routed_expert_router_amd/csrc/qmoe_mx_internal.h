@@ -285,6 +285,37 @@ inline int mx_max_mtiles(int P, int E) {
   return (int)(((long long)P + busy * (kMxBM - 1)) / kMxBM);
 }
 
+// ---- the split of the grouped products' tile list over the XCDs (used by the kernel that writes
+// the list and by the host that sizes the grid)
+
+constexpr int kMxXcds = 8;
+
+// Cost of `count` tiles with `rows` rows of x: 4 a tile for its weights and 1 for each 32 rows
+// of x. By loads alone it would be 8 to 1, by products 0; between them, since neither hides the
+// other wholly.
+constexpr int kMxTileCost = 4;
+__host__ __device__ constexpr int mx_tiles_cost(int count, int rows) {
+  return kMxTileCost * count + (rows + 31) / 32;
+}
+
+// XCD x starts at the first tile whose cost before it is x / 8 of the whole or more. Tile j, with
+// the cost `before` it and `next` with it, finds the starts that are it or the tile behind it.
+__host__ __device__ inline void mx_xcd_starts(int j, int before, int next, int total, int* first) {
+#pragma unroll
+  for (int x = 0; x < kMxXcds; ++x) {
+    const long long at = (long long)x * total;
+    if (at == (long long)before * kMxXcds) first[x] = j;
+    else if (at > (long long)before * kMxXcds && at < (long long)next * kMxXcds) first[x] = j + 1;
+  }
+}
+
+// Workgroups that cover the tiles of any XCD, `ntn` a tile: an XCD's share of the cost is at most
+// an eighth of the whole and one tile, a tile costs kMxTileCost + 1 to kMxTileCost + 4.
+inline int mx_list_grid(int max_mt, int ntn) {
+  const int most = ((kMxTileCost + 4) * ((max_mt + kMxXcds - 1) / kMxXcds + 1)) / (kMxTileCost + 1) + 2;
+  return kMxXcds * std::min(max_mt, most) * ntn;
+}
+
 struct MxFfnWs {
   size_t tiles;   // int4 [max M-tiles] (expert, first grouped pair, pairs, 0)
   size_t xcd_first;  // int [9] first tile of each XCD, and their number
