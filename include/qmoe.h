@@ -475,7 +475,10 @@ moe_status moe_route_scored(const void* logits, int dtype, int n_tokens, int n_e
  *   codes   uint8 [rows][cols/2]    e2m1 (sign, 2 exponent bits, 1 fraction bit: 0, .5, 1, 1.5,
  *                                   2, 3, 4, 6), column 2i in the low half of byte i
  *   scales  uint8 [rows][cols/32]   e8m0: the factor 2^(byte - 127) of 32 columns; 255: NaN
- * Both 16-byte aligned. E experts' matrices follow each other. */
+ * Both 16-byte aligned. E experts' matrices follow each other.
+ * Products take both sides in this form: the rows of x, and the hidden vector of the experts, are
+ * quantized on the way. There is no form with 16-bit activations, with a bias, or with a clamped
+ * gate. */
 typedef struct {
   const uint8_t* codes;
   const uint8_t* scales;

@@ -8,11 +8,12 @@
 //                 h = silu(g) u and its 4-bit blocks, as the down product in fp32 rows
 //   k_mx_combine  out[t] = residual[t] + sum_j w[t][j] y[place of pair t k + j], slot order, binary64
 //
-// Measured: 8192 rows by 4096 by 8192 columns 135 us, 4.1 PFLOP/s (the bare scaled matrix
+// Measured (kernel traces): 8192 rows, a reduction of 4096 and 8192 outputs 157-162 us, 3.4-3.5
+// PFLOP/s, a reduction of 8192 and 4096 outputs 142-148, 3.7-3.9 (the bare scaled matrix
 // instructions reach 6.6 on random codes, which the power limit sets, a bf16 product of the
-// library 1.25); 512 experts of 768 by 2048, top 10: 256 tokens 164 + 105 us (gate and up, down),
-// the weights at 5.1 TB/s; 8192 tokens 260 + 273 us, and 130 us (5.1 TB/s) for the sum over the
-// slots.
+// library 1.25); 512 experts of 768 by 2048, top 10: 256 tokens 162 + 102 us (gate and up, down),
+// the weights at 5 TB/s; 8192 tokens 257-300 + 227-250 us, and 137 us (5.4 TB/s) for the sum over
+// the slots.
 #include "qmoe_mx_internal.h"
 
 namespace qmoe {
@@ -438,7 +439,8 @@ struct Tile {
 
 // The four pieces and the scale of a block of h from its 64-bit values. The gate and up sums of
 // the block lie in LDS as gu[value][lane], gate first; lanes l and l + 32 hold its two halves.
-// Rolled loops: taken by a block in some two hundred.
+// Rolled loops: only blocks whose scale the bounds leave open and odd ones (hidden_block) come here,
+// with the rest of their wave.
 __device__ __forceinline__ void hidden_block64(lds_float* gu, int lane, uint32_t (&pieces)[4], uint32_t& scale) {
   double m = 0.0;
   bool bad = false;
@@ -734,7 +736,9 @@ __device__ __forceinline__ bool grid_tile(const GemmArgs& a, int mtiles, int nti
 // start and end beside the other's loop. Few rows an expert: bound by the weights from memory.
 // Many: by the direct loads (without them 180 of 260 us, without the LDS reads 255, without the
 // end 250). Stages of whole lines would need 128 x 128 tiles (10% slower at 256 and at 8192
-// tokens) or one workgroup of 256 x 256 a CU (15% slower at 256 tokens, 1% at 8192).
+// tokens) or one workgroup of 256 x 256 a CU (15% slower at 256 tokens, 1% at 8192). The down form
+// with a TAIL (f no multiple of 256) keeps 4 of its 256 registers in scratch memory: 4096 tokens of
+// 64 experts, top 6, d = 2048, 104-110 us at f = 1408 and 93-102 at f = 1536.
 template <bool TAIL, int MODE>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_mx_grouped(GemmArgs a) {
   typedef Stage<256, 128, 4> S;

@@ -265,8 +265,11 @@ inline bool mx_window(int n, int k, int d, int f, int E) {
 }
 
 // Whether a linear product runs on the window kernel: the rows to multiply are then quantized in
-// LDS (up to 70 KB at 16 rows of 8192) and need no workspace. Weights with fewer than 16 scales
-// in all run there too: the tiles fetch 16 at once.
+// LDS (up to 70 KB at 16 rows of 8192) and need no workspace, which the query must know from
+// the rows and columns alone. Weights with fewer than 16 scales in all run there too: the tiles
+// fetch 16 at once. Columns past 8192 leave the window whatever the rows are, a limit that was not
+// measured from both sides: 4 rows by 8192 columns and 7168 outputs take 10.8 us here, 4 rows by
+// 18432 columns and 7168 outputs 4.8 + 36.8 us on the tiles (70 MB of weights at 1.9 TB/s).
 inline bool mx_linear_window(int n, int N, int K) {
   return (n <= kMxWindowTokens && K <= 8192) || (int64_t)N * (K / kMxBlock) < 16;
 }

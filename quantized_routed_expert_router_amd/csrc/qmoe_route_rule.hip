@@ -16,7 +16,9 @@
 // best becomes a candidate, and the candidates, at most one a lane, get their binary64 scores,
 // by which they are ranked. Where groups are too near or candidates too many, and for scores
 // that are not finite, the whole rule runs in binary64 (wave_rule, which softmax always does:
-// its sum needs every exponential).
+// its sum needs every exponential). The fused kernel holds both, and the grouping: it spills
+// scalar registers into lanes of vector registers (76 at 512 experts, 131 at 1024; k_rule_topk 47
+// at 1024). 4 tokens, us: 256 experts 6.1, 512 experts 7.0 (softmax 8.6), 1024 experts 9.6.
 //
 // Groups go through LDS: 64 / G lanes (a power of two) scan one group each. The k best are found
 // as in the plain router, by a threshold on order-preserving images: every expert of the top k
