@@ -2,11 +2,9 @@
 end where other memory begins."""
 from __future__ import annotations
 
-import numpy as np
 import pytest
 import torch
 
-import mx_ref
 from quantized_routed_expert_router_amd import mx, qmoe
 
 pytestmark = pytest.mark.gpu
